@@ -16,19 +16,26 @@ combine, with R virtual EP ranks held as slabs of one GPU's HBM:
   ep_combine_send    send phase of a split combine (expert-major rows -> rank slabs);
                      ep_combine is its receive phase
   ep_combine_permuted_ll   the expert-major combine shaped for decode-sized batches
+  ep_dispatch_permuted_fp8 / ep_dispatch_permuted_fp8_ll  E4M3 rows and their scales into
+                     expert order, with the layout at hand or in one launch
+  ep_combine_permuted_bwd / ep_dispatch_permuted_bwd  gradients of the weighted return and
+                     of the sort
+  ep_rmsnorm / ep_rmsnorm_bwd  residual addition + RMS norm to bf16 and E4M3 rows, and its
+                     gradient
 
 The C ABI is include/ep.h (libep_gb300.so, built in-tree by build.py); the
 functions here with the same names are its ctypes binding, and api.py
 allocates buffers and chains the calls.
 """
 from ._lib import (  # noqa: F401
-    ABI_VERSION, DTYPE_BF16, DTYPE_E4M3, EP_ERR_CUDA, EP_ERR_INVALID, EP_ERR_SCRATCH, EP_OK,
+    ABI_VERSION, DTYPE_BF16, DTYPE_E4M3, DTYPE_F32, EP_ERR_CUDA, EP_ERR_INVALID, EP_ERR_SCRATCH, EP_OK,
     LAYOUT_NOALLOC_SCRATCH_BYTES, EXPORTS, FLAG_BAD_EXPERT,
     FLAG_CAPACITY, FLAG_TIMEOUT, FLAG_WORKSPACE, NODES_DENSE, NODES_SPARSE, EpError, ep_combine, ep_dispatch,
     ep_dispatch_nodes, ep_get_layout, ep_get_layout_noalloc, ep_layout_workspace_size, ep_restripe_prob, lib,
     ep_combine_permuted, ep_dispatch_permuted, ep_expert_layout_workspace_size, ep_get_expert_layout,
     ep_permute_received, ep_combine_fp8, ep_combine_weights, ep_dispatch_permuted_ll, ep_combine_send,
-    ep_combine_permuted_ll,
+    ep_combine_permuted_ll, ep_dispatch_permuted_fp8, ep_dispatch_permuted_fp8_ll, ep_dispatch_permuted_bwd,
+    ep_combine_permuted_bwd, ep_rmsnorm, ep_rmsnorm_bwd, ep_rmsnorm_bwd_workspace_size,
 )
 from .api import (  # noqa: F401
     Dispatched, Layout, alloc_dispatch, alloc_layout, combine, combine_fp8, combine_weights, dispatch, get_layout,

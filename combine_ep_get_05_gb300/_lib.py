@@ -29,6 +29,7 @@ FLAG_WORKSPACE = 8
 
 DTYPE_BF16 = 0
 DTYPE_E4M3 = 1
+DTYPE_F32 = 2
 
 NODES_DENSE = 0
 NODES_SPARSE = 1
@@ -41,6 +42,8 @@ EXPORTS = (
     "ep_combine_fp8", "ep_combine_weights",
     "ep_expert_layout_workspace_size", "ep_get_expert_layout", "ep_dispatch_permuted", "ep_permute_received",
     "ep_combine_permuted", "ep_dispatch_permuted_ll", "ep_combine_send", "ep_combine_permuted_ll",
+    "ep_dispatch_permuted_fp8", "ep_dispatch_permuted_fp8_ll", "ep_dispatch_permuted_bwd", "ep_combine_permuted_bwd",
+    "ep_rmsnorm", "ep_rmsnorm_bwd_workspace_size", "ep_rmsnorm_bwd",
 )
 
 
@@ -71,7 +74,7 @@ def lib():
                         f"{LIB_PATH} is missing: build the CUDA library first "
                         "(python -m combine_ep_get_05_gb300.build or __graft_entry__.build())")
                 L = ctypes.CDLL(LIB_PATH)
-                P, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+                P, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
                 sigs = {
                     "ep_abi_version": (i32, []),
                     "ep_status_str": (ctypes.c_char_p, [i32]),
@@ -94,6 +97,15 @@ def lib():
                     "ep_combine_permuted": (i32, [P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P]),
                     "ep_combine_permuted_ll": (i32, [P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P]),
                     "ep_combine_send": (i32, [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, P, P]),
+                    "ep_dispatch_permuted_fp8": (i32, [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P, P,
+                                                       P]),
+                    "ep_dispatch_permuted_fp8_ll": (i32, [P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P,
+                                                          P, P]),
+                    "ep_dispatch_permuted_bwd": (i32, [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P]),
+                    "ep_combine_permuted_bwd": (i32, [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P]),
+                    "ep_rmsnorm": (i32, [P, P, P, i32, i32, f32, i32, i32, P, P, P, P, P]),
+                    "ep_rmsnorm_bwd_workspace_size": (sz, [i32, i32]),
+                    "ep_rmsnorm_bwd": (i32, [P, P, P, P, i32, i32, f32, i32, i32, P, P, P, P, sz, P]),
                 }
                 for name, (res, args) in sigs.items():
                     f = getattr(L, name)
@@ -412,3 +424,162 @@ def ep_combine_send(y_perm, recv_src_idx, recv_topk_idx, recv_topk_w, tokens_per
                                _ptr(tokens_per_rank), _ptr(expert_offsets), _ptr(expert_slot), T, H, k, E, R, M,
                                max_rows, _ptr(y_rank), _ptr(status), _stream(stream))
     _done("ep_combine_send", rc)
+
+
+# --------------------------------------------------------------------------- E4M3 rows and gradients
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)  # E4M3 codes, as bytes or as torch's own type
+
+
+def _check_codes(name, t, shape):
+    _check(name, t, t.dtype if t is not None and t.dtype in _CODES else torch.uint8, shape)
+
+
+def ep_dispatch_permuted_fp8(x_q, x_scales, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, num_ranks,
+                             max_rows, perm_q, perm_scales, perm_src=None, perm_w=None, status=None, stream=None):
+    """ep_dispatch_permuted for E4M3 rows: codes [T][H] (uint8 or float8_e4m3fn) and scales [T][H/128]."""
+    T, H = x_q.shape
+    k = topk_idx.shape[1]
+    E, R = num_experts, num_ranks
+    _check_codes("x_q", x_q, (T, H))
+    _check("x_scales", x_scales, torch.float32, (T, H // 128))
+    _check("topk_idx", topk_idx, torch.int64, (T, k))
+    _check("topk_w", topk_w, torch.float32, (T, k), optional=True)
+    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _check("expert_slot", expert_slot, torch.int32, (T, k))
+    _check_codes("perm_q", perm_q, (R, max_rows, H))
+    _check("perm_scales", perm_scales, torch.float32, (R, max_rows, H // 128))
+    _check("perm_src", perm_src, torch.int32, (R, max_rows), optional=True)
+    _check("perm_w", perm_w, torch.float32, (R, max_rows), optional=True)
+    _check("status", status, torch.int32, (1,), optional=True)
+    rc = lib().ep_dispatch_permuted_fp8(_ptr(x_q), _ptr(x_scales), _ptr(topk_idx), _ptr(topk_w), _ptr(expert_offsets),
+                                        _ptr(expert_slot), T, H, k, E, R, max_rows, _ptr(perm_q), _ptr(perm_scales),
+                                        _ptr(perm_src), _ptr(perm_w), _ptr(status), _stream(stream))
+    _done("ep_dispatch_permuted_fp8", rc)
+
+
+def ep_dispatch_permuted_fp8_ll(x_q, x_scales, topk_idx, topk_w, num_experts, num_ranks, max_rows, expert_offsets,
+                                expert_slot, perm_q, perm_scales, perm_src=None, perm_w=None, status=None, stream=None):
+    """ep_dispatch_permuted_fp8 for a decode-sized batch (T <= 1024), expert layout included, in one launch."""
+    T, H = x_q.shape
+    k = topk_idx.shape[1]
+    E, R = num_experts, num_ranks
+    _check_codes("x_q", x_q, (T, H))
+    _check("x_scales", x_scales, torch.float32, (T, H // 128))
+    _check("topk_idx", topk_idx, torch.int64, (T, k))
+    _check("topk_w", topk_w, torch.float32, (T, k), optional=True)
+    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _check("expert_slot", expert_slot, torch.int32, (T, k))
+    _check_codes("perm_q", perm_q, (R, max_rows, H))
+    _check("perm_scales", perm_scales, torch.float32, (R, max_rows, H // 128))
+    _check("perm_src", perm_src, torch.int32, (R, max_rows), optional=True)
+    _check("perm_w", perm_w, torch.float32, (R, max_rows), optional=True)
+    _check("status", status, torch.int32, (1,), optional=True)
+    rc = lib().ep_dispatch_permuted_fp8_ll(_ptr(x_q), _ptr(x_scales), _ptr(topk_idx), _ptr(topk_w), T, H, k, E, R,
+                                           max_rows, _ptr(expert_offsets), _ptr(expert_slot), _ptr(perm_q),
+                                           _ptr(perm_scales), _ptr(perm_src), _ptr(perm_w), _ptr(status),
+                                           _stream(stream))
+    _done("ep_dispatch_permuted_fp8_ll", rc)
+
+
+def ep_dispatch_permuted_bwd(dperm_x, dperm_w, dx_in, topk_idx, expert_offsets, expert_slot, num_experts, dx,
+                             dtopk_w=None, status=None, stream=None):
+    """Gradient of ep_dispatch_permuted: dx = dx_in + the token's rows of dperm_x, dtopk_w from dperm_w."""
+    R, max_rows, H = dperm_x.shape
+    T, k = topk_idx.shape
+    E = num_experts
+    _check("dperm_x", dperm_x, torch.bfloat16)
+    _check("dperm_w", dperm_w, torch.float32, (R, max_rows), optional=dtopk_w is None)
+    _check("dx_in", dx_in, torch.bfloat16, (T, H), optional=True)
+    _check("topk_idx", topk_idx, torch.int64)
+    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _check("expert_slot", expert_slot, torch.int32, (T, k))
+    _check("dx", dx, torch.bfloat16, (T, H))
+    _check("dtopk_w", dtopk_w, torch.float32, (T, k), optional=True)
+    _check("status", status, torch.int32, (1,), optional=True)
+    rc = lib().ep_dispatch_permuted_bwd(_ptr(dperm_x), _ptr(dperm_w), _ptr(dx_in), _ptr(topk_idx),
+                                        _ptr(expert_offsets), _ptr(expert_slot), T, H, k, E, R, max_rows, _ptr(dx),
+                                        _ptr(dtopk_w), _ptr(status), _stream(stream))
+    _done("ep_dispatch_permuted_bwd", rc)
+
+
+def ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, dy, dtopk_w=None,
+                            status=None, stream=None):
+    """Gradient of ep_combine_permuted: dy's rows = w * dout, dtopk_w = <dout, y's row>; y is read for dtopk_w only."""
+    R, max_rows, H = dy.shape
+    T, k = topk_idx.shape
+    E = num_experts
+    _check("dout", dout, torch.bfloat16, (T, H))
+    _check("y", y, torch.bfloat16, (R, max_rows, H), optional=dtopk_w is None)
+    _check("topk_idx", topk_idx, torch.int64)
+    _check("topk_w", topk_w, torch.float32, (T, k), optional=True)
+    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _check("expert_slot", expert_slot, torch.int32, (T, k))
+    _check("dy", dy, torch.bfloat16)
+    _check("dtopk_w", dtopk_w, torch.float32, (T, k), optional=True)
+    _check("status", status, torch.int32, (1,), optional=True)
+    rc = lib().ep_combine_permuted_bwd(_ptr(dout), _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(expert_offsets),
+                                       _ptr(expert_slot), T, H, k, E, R, max_rows, _ptr(dy), _ptr(dtopk_w),
+                                       _ptr(status), _stream(stream))
+    _done("ep_combine_permuted_bwd", rc)
+
+
+# --------------------------------------------------------------------------- norm
+
+_STREAM_TYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _stream_dtype(*tensors):
+    """The residual stream's type: that of the tensors given (they must agree), bf16 when there are none."""
+    types = {t.dtype for t in tensors if t is not None}
+    if len(types) > 1 or not types <= set(_STREAM_TYPES):
+        raise ValueError(f"the residual stream must be bfloat16 or float32 throughout, got {sorted(map(str, types))}")
+    return types.pop() if types else torch.bfloat16
+
+
+def _check_weight(weight, H):
+    _check("weight", weight, torch.float32 if weight is not None and weight.dtype == torch.float32 else torch.bfloat16,
+           (H,))
+    return _STREAM_TYPES[weight.dtype]
+
+
+def ep_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, y_q=None, y_scales=None, stream=None):
+    """z = x + residual; residual_out = z; y (bf16) and y_q / y_scales (E4M3, 1x128) = z / rms(z) * weight.
+    x or residual may be None; every output may be None, y_q and y_scales together."""
+    if x is None and residual is None:
+        raise ValueError("x or residual is required")
+    T, H = (x if x is not None else residual).shape
+    dtype = _stream_dtype(residual, residual_out)
+    _check("x", x, torch.bfloat16, (T, H), optional=True)
+    _check("residual", residual, dtype, (T, H), optional=True)
+    wtype = _check_weight(weight, H)
+    _check("residual_out", residual_out, dtype, (T, H), optional=True)
+    _check("y", y, torch.bfloat16, (T, H), optional=True)
+    if y_q is not None:
+        _check_codes("y_q", y_q, (T, H))
+    _check("y_scales", y_scales, torch.float32, (T, H // 128), optional=y_q is None)
+    rc = lib().ep_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _STREAM_TYPES[dtype], wtype, eps, T, H,
+                          _ptr(residual_out), _ptr(y), _ptr(y_q), _ptr(y_scales), _stream(stream))
+    _done("ep_rmsnorm", rc)
+
+
+def ep_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
+    return int(lib().ep_rmsnorm_bwd_workspace_size(T, H))
+
+
+def ep_rmsnorm_bwd(dy, z, weight, dz_in, eps, dz, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradient of ep_rmsnorm at z (its residual_out): dz = dz_in + d/dz, dx the same in bf16, dweight fp32."""
+    T, H = z.shape
+    dtype = _stream_dtype(z)
+    _check("dy", dy, torch.bfloat16, (T, H))
+    _check("z", z, dtype)
+    wtype = _check_weight(weight, H)
+    _check("dz_in", dz_in, dtype, (T, H), optional=True)
+    _check("dz", dz, dtype, (T, H))
+    _check("dx", dx, torch.bfloat16, (T, H), optional=True)
+    _check("dweight", dweight, torch.float32, (H,), optional=True)
+    _check("workspace", workspace, torch.uint8, optional=dweight is None)
+    rc = lib().ep_rmsnorm_bwd(_ptr(dy), _ptr(z), _ptr(weight), _ptr(dz_in), _STREAM_TYPES[dtype], wtype, eps, T, H,
+                              _ptr(dz), _ptr(dx), _ptr(dweight), _ptr(workspace),
+                              workspace.numel() if workspace is not None else 0, _stream(stream))
+    _done("ep_rmsnorm_bwd", rc)

@@ -20,9 +20,13 @@
 #include <algorithm>
 
 #include "ep_common.cuh"
+#include "ep_quant.cuh"
 #include "ep_scatter.cuh"
 
 namespace {
+
+using ep::quotient;
+using ep::scale_of;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -147,30 +151,6 @@ __global__ void __launch_bounds__(kThreads, 2) dispatch_bf16_kernel(DispatchArgs
         }
         __syncwarp();
     }
-}
-
-// x / scale correctly rounded to fp32, for a normal scale. The quotient is the product by
-// the correctly rounded reciprocal, corrected once by its residual (Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34,
-// 1990): with rcp = RN(1/scale) and q0 = RN(x * rcp) within an ulp of x / scale, the
-// residual x - q0 * scale is exact in one fused multiply-add and q0 + rcp * residual,
-// rounded once, is RN(x / scale). Quotients that fall below the fp32 normal range only
-// ever round to an E4M3 zero, whose sign is the sign of x; the correction turns a zero x
-// into +0, so x's sign bit is put back (for every other x it is already there).
-__device__ __forceinline__ float quotient(float x, float scale, float rcp) {
-    const float q0 = __fmul_rn(x, rcp);
-    const float e = __fmaf_rn(-q0, scale, x);
-    const float q1 = __fmaf_rn(e, rcp, q0);
-    return __uint_as_float(__float_as_uint(q1) | (__float_as_uint(x) & 0x80000000u));
-}
-
-// amax / 448 correctly rounded: the same correction with RN(1/448), valid while the
-// quotient is a normal fp32 (amax >= 2^-116); smaller amax take the IEEE division
-__device__ __forceinline__ float scale_of(float amax) {
-    constexpr float kInv448 = 1.0f / 448.0f;  // correctly rounded at compile time
-    if (amax < 0x1p-116f) return __fdiv_rn(amax, 448.0f);
-    const float q0 = __fmul_rn(amax, kInv448);
-    return __fmaf_rn(__fmaf_rn(-q0, 448.0f, amax), kInv448, q0);
 }
 
 // bf16 dispatch through the shared bulk-copy scatter (ep_scatter.cuh): source row t is

@@ -29,6 +29,7 @@ constexpr int kMaxTopk = 32;
 constexpr int kUnroll = 8;
 constexpr int kBatch = 8;
 constexpr int kLookbackBatch = 8;
+constexpr int kMaxFp8H = 65536;  // E4M3 rows: the scatter's row buffers hold any row up to this
 
 __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 inline int num_tiles_for(int T) { return T > 0 ? (T + kThreads - 1) / kThreads : 1; }
@@ -248,6 +249,23 @@ __device__ __forceinline__ int permuted_destinations(const int64_t* topk_idx, co
     return __popc(m);
 }
 
+// the nblk scales of token t to nd destination rows, by threads tid of nt
+__device__ __forceinline__ void copy_scales(const float* scales, float* perm_scales, int t, int nblk,
+                                            const long long* rows, int nd, int tid, int nt) {
+    const float* src = scales + static_cast<size_t>(t) * nblk;
+    if ((nblk & 3) == 0) {  // scale rows are whole 16-byte vectors
+        for (int v = tid; v < nblk / 4; v += nt) {
+            const uint4 s = ld_stream_v4(src + 4 * v);
+            for (int d = 0; d < nd; ++d) st_v4(perm_scales + static_cast<size_t>(rows[d]) * nblk + 4 * v, s);
+        }
+    } else {
+        for (int b = tid; b < nblk; b += nt) {
+            const float s = __ldg(src + b);
+            for (int d = 0; d < nd; ++d) perm_scales[static_cast<size_t>(rows[d]) * nblk + b] = s;
+        }
+    }
+}
+
 struct PermDispatchArgs {
     const uint16_t* x;
     const int64_t* topk_idx;
@@ -302,6 +320,33 @@ struct PermScatter {
             if (a.perm_src != nullptr) a.perm_src[row] = t;
             if (a.perm_w != nullptr) a.perm_w[row] = a.topk_w[static_cast<size_t>(t) * a.k + aux[lane]];
         }
+    }
+    __device__ void prologue() const {}
+};
+
+// E4M3 rows: H codes through the same scatter, and the row's H/128 scales beside them
+struct PermFp8Scatter {
+    PermDispatchArgs a;  // x and perm_x unused
+    const uint8_t* x_q;
+    const float* x_scales;
+    float* perm_scales;
+    char* dst;
+    uint32_t row_bytes;
+    int32_t* status;
+    __device__ int items() const { return a.T; }
+    __device__ const void* source(int t) const { return x_q + static_cast<size_t>(t) * a.H; }
+    __device__ int destinations(int t, long long* rows, int* aux) const {
+        return permuted_destinations(a.topk_idx, a.offsets, a.eslot, t, a.k, a.E, a.R, a.max_rows, rows, aux,
+                                     a.status);
+    }
+    __device__ void side_work(int t, int nd, const long long* rows, const int* aux) const {
+        const int lane = lane_id();
+        if (lane < nd) {
+            const size_t row = static_cast<size_t>(rows[lane]);
+            if (a.perm_src != nullptr) a.perm_src[row] = t;
+            if (a.perm_w != nullptr) a.perm_w[row] = a.topk_w[static_cast<size_t>(t) * a.k + aux[lane]];
+        }
+        copy_scales(x_scales, perm_scales, t, a.H / 128, rows, nd, lane, 32);
     }
     __device__ void prologue() const {}
 };
@@ -515,13 +560,16 @@ constexpr int kLLMaxTokens = 1024;
 constexpr int kLLMaxEntries = 8192;  // T * k
 
 struct LLArgs {
-    const uint16_t* x;
+    const void* x;  // rows of nvec 16-byte vectors: H bf16, or H E4M3 codes
+    int nvec;
+    const float* x_scales;  // E4M3 rows: [T][H/128]
+    float* perm_scales;
     const int64_t* topk_idx;
     const float* topk_w;
     int T, H, k, E, R, max_rows;
     int32_t* offsets;  // [E+1] out
     int32_t* eslot;    // [T][k] out
-    uint16_t* perm_x;
+    void* perm_x;
     int32_t* perm_src;
     float* perm_w;
     int32_t* status;
@@ -531,6 +579,7 @@ inline size_t ll_smem_bytes(int T, int k, int E) {
     return (static_cast<size_t>(2 * kWarps) * E + ((E + 1 + 3) & ~3) + static_cast<size_t>(T) * k) * sizeof(int32_t);
 }
 
+template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) dispatch_permuted_ll_kernel(LLArgs a) {
     // a decode batch's grid leaves most of every SM free: the next kernel (the expert work,
     // or the low-latency combine launched as a dependent launch) may settle its CTAs now and
@@ -550,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_permuted_ll_kernel(LLArg
     const int warp = tid >> 5;
     const int k = a.k;
     const int E = a.E;
-    const int nvec = a.H / 8;
+    const int nvec = a.nvec;
     const int per_warp = (nvec + kWarps - 1) / kWarps;  // 16-byte vectors of a row per warp
     const int v_lo = warp * per_warp;
     const int v_hi = v_lo + per_warp < nvec ? v_lo + per_warp : nvec;
@@ -559,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_permuted_ll_kernel(LLArg
     // that its memory latency overlaps it
     uint4 first[kUnroll];
     if (static_cast<int>(blockIdx.x) < a.T) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(blockIdx.x) * a.H);
+        const uint4* src = static_cast<const uint4*>(a.x) + static_cast<size_t>(blockIdx.x) * nvec;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int v = v_lo + u * 32 + lane;
@@ -688,8 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_permuted_ll_kernel(LLArg
         }
         __syncthreads();
         const int nd = s_nd;
-        const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.H);
-        uint4* base = reinterpret_cast<uint4*>(a.perm_x);
+        if constexpr (kFp8) copy_scales(a.x_scales, a.perm_scales, t, a.H / 128, s_row, nd, tid, kThreads);
+        const uint4* src = static_cast<const uint4*>(a.x) + static_cast<size_t>(t) * nvec;
+        uint4* base = static_cast<uint4*>(a.perm_x);
         for (int v0 = v_lo; v0 < v_hi; v0 += 32 * kUnroll) {
             uint4 buf[kUnroll];
             const bool prefetched = t == static_cast<int>(blockIdx.x) && v0 == v_lo;
@@ -1165,6 +1215,7 @@ std::atomic<int> g_send_per_sm[kMaxDevices];
 std::atomic<int> g_send_per_sm_w[kMaxDevices];
 
 std::atomic<int> g_ll_attr_set[kMaxDevices];
+std::atomic<int> g_ll_fp8_attr_set[kMaxDevices];
 std::atomic<int> g_attr_set[kMaxDevices];
 std::atomic<int> g_combine_per_sm[kMaxDevices];
 
@@ -1172,6 +1223,16 @@ int token_grid(long long work) {
     const long long want = (work + kWarps - 1) / kWarps;
     const long long cap = static_cast<long long>(sm_count()) * 8;
     return static_cast<int>(want < 1 ? 1 : (want < cap ? want : cap));
+}
+
+ep_status_t launch_ll(void (*kernel)(LLArgs), std::atomic<int>* attr_set, const LLArgs& a, cudaStream_t stream) {
+    const ep_status_t attr = ensure_dynamic_smem(
+        attr_set, kernel,
+        static_cast<int>(ll_smem_bytes(kLLMaxTokens, kLLMaxEntries / kLLMaxTokens, kMaxExpertsPerm)));
+    if (attr != EP_OK) return attr;
+    const int sms = sm_count();
+    const int grid = a.T < 1 ? 1 : (a.T < sms ? a.T : sms);
+    return launch_dependent(kernel, dim3(grid), dim3(kThreads), ll_smem_bytes(a.T, a.k, a.E), stream, a);
 }
 
 }  // namespace
@@ -1301,16 +1362,53 @@ extern "C" ep_status_t ep_dispatch_permuted_ll(const void* x, const int64_t* top
         !aligned16_or_null(topk_w) || !aligned16(expert_offsets) || !aligned16_or_null(expert_slot) ||
         !aligned16_or_null(perm_src) || !aligned16_or_null(perm_w))
         return EP_ERR_INVALID;
-    const ep_status_t attr = ensure_dynamic_smem(
-        g_ll_attr_set, dispatch_permuted_ll_kernel,
-        static_cast<int>(ll_smem_bytes(kLLMaxTokens, kLLMaxEntries / kLLMaxTokens, kMaxExpertsPerm)));
-    if (attr != EP_OK) return attr;
-    LLArgs a{static_cast<const uint16_t*>(x), topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets, expert_slot,
-             static_cast<uint16_t*>(perm_x), perm_src, perm_w, status};
-    const int sms = sm_count();
-    const int grid = T < 1 ? 1 : (T < sms ? T : sms);
-    return launch_dependent(dispatch_permuted_ll_kernel, dim3(grid), dim3(kThreads), ll_smem_bytes(T, k, E),
-                            as_stream(stream), a);
+    const LLArgs a{x, H / 8, nullptr, nullptr, topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets, expert_slot,
+                   perm_x, perm_src, perm_w, status};
+    return launch_ll(dispatch_permuted_ll_kernel<false>, g_ll_attr_set, a, as_stream(stream));
+}
+
+extern "C" ep_status_t ep_dispatch_permuted_fp8(const uint8_t* x_q, const float* x_scales, const int64_t* topk_idx,
+                                                const float* topk_w, const int32_t* expert_offsets,
+                                                const int32_t* expert_slot, int32_t T, int32_t H, int32_t k, int32_t E,
+                                                int32_t R, int32_t max_rows, uint8_t* perm_q, float* perm_scales,
+                                                int32_t* perm_src, float* perm_w, int32_t* status, void* stream) {
+    if (!perm_common_ok(T, H, k, E, R, max_rows) || H % 128 != 0 || H > kMaxFp8H) return EP_ERR_INVALID;
+    if (T == 0) return EP_OK;
+    if (x_q == nullptr || x_scales == nullptr || topk_idx == nullptr || expert_offsets == nullptr ||
+        expert_slot == nullptr || (max_rows > 0 && (perm_q == nullptr || perm_scales == nullptr)) ||
+        (perm_w != nullptr && topk_w == nullptr))
+        return EP_ERR_INVALID;
+    if (!aligned16(x_q) || !aligned16(x_scales) || !aligned16_or_null(perm_q) || !aligned16_or_null(perm_scales) ||
+        !aligned16(topk_idx) || !aligned16_or_null(topk_w) || !aligned16(expert_offsets) || !aligned16(expert_slot) ||
+        !aligned16_or_null(perm_src) || !aligned16_or_null(perm_w))
+        return EP_ERR_INVALID;
+    const PermDispatchArgs a{nullptr, topk_idx, topk_w, expert_offsets, expert_slot, T, H, k, E, R, max_rows, nullptr,
+                             perm_src, perm_w, status};
+    const PermFp8Scatter sp{a, x_q, x_scales, perm_scales, reinterpret_cast<char*>(perm_q), static_cast<uint32_t>(H),
+                            status};
+    return launch_scatter_rows(sp, T, as_stream(stream));
+}
+
+extern "C" ep_status_t ep_dispatch_permuted_fp8_ll(const uint8_t* x_q, const float* x_scales, const int64_t* topk_idx,
+                                                   const float* topk_w, int32_t T, int32_t H, int32_t k, int32_t E,
+                                                   int32_t R, int32_t max_rows, int32_t* expert_offsets,
+                                                   int32_t* expert_slot, uint8_t* perm_q, float* perm_scales,
+                                                   int32_t* perm_src, float* perm_w, int32_t* status, void* stream) {
+    if (!perm_common_ok(T, H, k, E, R, max_rows) || H % 128 != 0 || H > kMaxFp8H || T > kLLMaxTokens ||
+        T * k > kLLMaxEntries || E > kMaxExpertsPerm || expert_offsets == nullptr)
+        return EP_ERR_INVALID;
+    if (T > 0 && (x_q == nullptr || x_scales == nullptr || topk_idx == nullptr || expert_slot == nullptr ||
+                  (max_rows > 0 && (perm_q == nullptr || perm_scales == nullptr)) ||
+                  (perm_w != nullptr && topk_w == nullptr)))
+        return EP_ERR_INVALID;
+    if (!aligned16_or_null(x_q) || !aligned16_or_null(x_scales) || !aligned16_or_null(perm_q) ||
+        !aligned16_or_null(perm_scales) || !aligned16_or_null(topk_idx) || !aligned16_or_null(topk_w) ||
+        !aligned16(expert_offsets) || !aligned16_or_null(expert_slot) || !aligned16_or_null(perm_src) ||
+        !aligned16_or_null(perm_w))
+        return EP_ERR_INVALID;
+    const LLArgs a{x_q, H / 16, x_scales, perm_scales, topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets,
+                   expert_slot, perm_q, perm_src, perm_w, status};
+    return launch_ll(dispatch_permuted_ll_kernel<true>, g_ll_fp8_attr_set, a, as_stream(stream));
 }
 
 extern "C" ep_status_t ep_combine_send(const void* y_perm, const int32_t* recv_src_idx, const int32_t* recv_topk_idx,

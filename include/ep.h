@@ -65,6 +65,7 @@ typedef int32_t ep_status_t;
 typedef int32_t ep_dtype_t;
 #define EP_DTYPE_BF16 0 /* bfloat16 rows, 2 bytes per element */
 #define EP_DTYPE_E4M3 1 /* OCP E4M3 rows (1 byte per element) + one fp32 scale per 128 elements */
+#define EP_DTYPE_F32 2  /* fp32 (the norm's residual stream and weight) */
 
 typedef int32_t ep_node_mode_t;
 #define EP_NODES_DENSE 0  /* copy every chunk's whole token range to every node */
@@ -425,6 +426,117 @@ ep_status_t ep_combine_permuted_ll(const void* y, const int64_t* topk_idx, const
                                    const int32_t* expert_offsets, const int32_t* expert_slot,
                                    int32_t T, int32_t H, int32_t k, int32_t E, int32_t R,
                                    int32_t max_rows, void* out, int32_t* status, void* stream);
+
+/* ep_dispatch_permuted_fp8 -- ep_dispatch_permuted for rows that are already E4M3 (the
+ * FP8 row format of ep_dispatch: H codes and one fp32 scale per 128 channels, for
+ * instance ep_rmsnorm's y_q / y_scales): for every counted (t, j), at its row p,
+ *   perm_q[r][p] = x_q[t], perm_scales[r][p] = x_scales[t],
+ *   perm_src[r][p] = t, perm_w[r][p] = topk_w[t][j].
+ *   x_q uint8 [T][H], H % 128 == 0, H <= 65536; x_scales fp32 [T][H/128];
+ *   perm_q uint8 [R][max_rows][H]; perm_scales fp32 [R][max_rows][H/128];
+ *   other arguments, dropped rows and flags as ep_dispatch_permuted. Codes and scales
+ *   are copied bit for bit. */
+ep_status_t ep_dispatch_permuted_fp8(const uint8_t* x_q, const float* x_scales, const int64_t* topk_idx,
+                                     const float* topk_w, const int32_t* expert_offsets,
+                                     const int32_t* expert_slot, int32_t T, int32_t H, int32_t k,
+                                     int32_t E, int32_t R, int32_t max_rows, uint8_t* perm_q,
+                                     float* perm_scales, int32_t* perm_src, float* perm_w,
+                                     int32_t* status, void* stream);
+
+/* ep_dispatch_permuted_fp8_ll -- the low-latency (decode-sized) form: layout and rows in
+ * one launch, with the same results as ep_get_expert_layout followed by
+ * ep_dispatch_permuted_fp8. Limits and outputs as ep_dispatch_permuted_ll. */
+ep_status_t ep_dispatch_permuted_fp8_ll(const uint8_t* x_q, const float* x_scales, const int64_t* topk_idx,
+                                        const float* topk_w, int32_t T, int32_t H, int32_t k, int32_t E,
+                                        int32_t R, int32_t max_rows, int32_t* expert_offsets,
+                                        int32_t* expert_slot, uint8_t* perm_q, float* perm_scales,
+                                        int32_t* perm_src, float* perm_w, int32_t* status, void* stream);
+
+/* ep_dispatch_permuted_bwd -- gradient of ep_dispatch_permuted: what every copy of a token
+ * received, brought back to the token:
+ *   dx[t][h]     = bf16_rn(acc), acc = dx_in[t][h] (+0 when dx_in is NULL); for j = 0 .. k-1
+ *                  with a counted (t, j) at row p < max_rows: acc = acc + float(dperm_x[r][p][h])
+ *   dtopk_w[t][j] = dperm_w[r][p], or 0 for an entry that was not counted or was dropped
+ * accumulated in fp32 in exactly that order, one rounding at the end: deterministic.
+ *   dperm_x bf16 [R][max_rows][H] (gradient of perm_x; rows that hold no entry are not
+ *   read); dperm_w fp32 [R][max_rows] (gradient of perm_w) and dtopk_w fp32 [T][k]: both
+ *   or neither; dx_in bf16 [T][H] or NULL: another gradient of x to add (the router's, a
+ *   shared expert's; may be the same array as dx); topk_idx, expert_offsets, expert_slot
+ *   as ep_dispatch_permuted; dx bf16 [T][H], all of it written.
+ *   status: EP_FLAG_CAPACITY when an entry's row lies past max_rows. */
+ep_status_t ep_dispatch_permuted_bwd(const void* dperm_x, const float* dperm_w, const void* dx_in,
+                                     const int64_t* topk_idx, const int32_t* expert_offsets,
+                                     const int32_t* expert_slot, int32_t T, int32_t H, int32_t k,
+                                     int32_t E, int32_t R, int32_t max_rows, void* dx, float* dtopk_w,
+                                     int32_t* status, void* stream);
+
+/* ep_combine_permuted_bwd -- gradient of ep_combine_permuted: for every counted (t, j) at
+ * row p < max_rows
+ *   dy[r][p][h]   = bf16_rn(topk_w[t][j] * float(dout[t][h]))   (dout itself when topk_w is NULL)
+ *   dtopk_w[t][j] = sum over h of float(dout[t][h]) * float(y[r][p][h])   (fp32, fixed order)
+ * and dtopk_w[t][j] = 0 for an entry that was not counted or was dropped.
+ *   dout bf16 [T][H]; y bf16 [R][max_rows][H], the rows ep_combine_permuted combined (read
+ *   only when dtopk_w is given, else it may be NULL); dtopk_w fp32 [T][k] or NULL, NULL when
+ *   topk_w is; dy bf16 [R][max_rows][H]: rows that hold no entry are not written (a caller
+ *   that reads whole slabs zero-fills them first). dy may be the same array as y.
+ *   status: EP_FLAG_CAPACITY when an entry's row lies past max_rows. */
+ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, const int64_t* topk_idx,
+                                    const float* topk_w, const int32_t* expert_offsets,
+                                    const int32_t* expert_slot, int32_t T, int32_t H, int32_t k,
+                                    int32_t E, int32_t R, int32_t max_rows, void* dy, float* dtopk_w,
+                                    int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* The norm in front of an expert layer                                      */
+/* ------------------------------------------------------------------------- */
+
+/* ep_rmsnorm -- the residual's addition and the root-mean-square norm, to bf16 rows (what
+ * a router reads) and to E4M3 rows (what an FP8 dispatch sends), in one pass:
+ *   z[t][h] = float(x[t][h]) + float(residual[t][h])             (fp32)
+ *   residual_out[t][h] = z, rounded to the stream's type
+ *   v[t][h] = z[t][h] * rstd_t * float(weight[h]),  rstd_t = 1 / sqrt(mean over h of z^2 + eps)
+ *   y[t][h] = bf16_rn(v)
+ *   y_scales[t][b] = amax_b / 448, amax_b = max |v| over the 128 channels of block b
+ *   y_q[t][h] = e4m3(v / y_scales[t][b])   (one rounding to nearest even, saturated)
+ * in fp32 throughout; the norm and both outputs take the unrounded z. A block with amax 0
+ * has scale 0 and signed-zero codes; a NaN becomes the NaN code and takes no part in amax.
+ *   x            bf16 [T][H] or NULL (z = residual)
+ *   residual     stream_dtype [T][H] or NULL (z = x); x or residual is required
+ *   weight       weight_dtype [H]
+ *   stream_dtype EP_DTYPE_BF16 or EP_DTYPE_F32: the type of residual and residual_out
+ *   weight_dtype EP_DTYPE_BF16 or EP_DTYPE_F32
+ *   eps >= 0; H % 8 == 0, H <= 16384, and H % 128 == 0 when y_q is given
+ *   residual_out stream_dtype [T][H] or NULL; may be the same array as residual
+ *   y            bf16 [T][H] or NULL; may be the same array as x
+ *   y_q uint8 [T][H] and y_scales fp32 [T][H/128]: both or neither
+ *   at least one output. One launch, one thread block per row; T = 1 is an ordinary size. */
+ep_status_t ep_rmsnorm(const void* x, const void* residual, const void* weight,
+                       ep_dtype_t stream_dtype, ep_dtype_t weight_dtype, float eps, int32_t T,
+                       int32_t H, void* residual_out, void* y, uint8_t* y_q, float* y_scales,
+                       void* stream);
+
+/* Bytes of device workspace ep_rmsnorm_bwd needs when it returns dweight. */
+size_t ep_rmsnorm_bwd_workspace_size(int32_t T, int32_t H);
+
+/* ep_rmsnorm_bwd -- gradient of ep_rmsnorm's norm and addition (an 8-bit output is taken
+ * to pass its gradient straight through): with rstd_t as above, from z alone,
+ *   g[t][h]   = float(dy[t][h]) * float(weight[h])
+ *   d[t][h]   = rstd_t * (g - z * rstd_t^2 * mean over h of (g * z))  + dz_in[t][h]
+ *   dz[t][h]  = d rounded to the stream's type: the gradient of residual, and of x
+ *   dx[t][h]  = bf16_rn(d): the gradient of x where the stream is fp32
+ *   dweight[h] = sum over t of dy * z * rstd_t
+ * in fp32, sums in a fixed order for a given GPU: deterministic.
+ *   dy bf16 [T][H]; z stream_dtype [T][H], ep_rmsnorm's residual_out (its x where there is
+ *   no residual); dz_in stream_dtype [T][H] or NULL: the gradient that arrives along the
+ *   stream; dz stream_dtype [T][H] (may be the same array as dz_in or z); dx bf16 [T][H]
+ *   or NULL (may be the same array as dy); dweight fp32 [H] or NULL, overwritten (zeros when
+ *   T = 0); weight, types, eps and H as ep_rmsnorm
+ *   workspace: >= ep_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, contents
+ *   irrelevant; may be NULL when dweight is NULL. Two launches, one without dweight. */
+ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, const void* dz_in,
+                           ep_dtype_t stream_dtype, ep_dtype_t weight_dtype, float eps, int32_t T,
+                           int32_t H, void* dz, void* dx, float* dweight, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
