@@ -317,6 +317,9 @@ __device__ __forceinline__ void cp_async16_if(void* smem, const void* gmem, bool
         "l"(gmem), "r"(static_cast<int>(p))
         : "memory");
 }
+__device__ __forceinline__ void cp_async8(void* smem, const void* gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem)), "l"(gmem) : "memory");
+}
 __device__ __forceinline__ void cp_async4_if(void* smem, const void* gmem, bool p) {
     asm volatile(
         "{\n"
