@@ -129,6 +129,8 @@ def test_binding_refuses_host_tensors_wrong_types_and_shapes():
     with pytest.raises(ValueError, match="residual stream"):
         ep.ep_rmsnorm(bf(T, H), bf(T, H), bf(H), 1e-6, f32(T, H))
     with pytest.raises(ValueError, match="residual stream"):
+        ep.ep_rmsnorm(bf(T, H), torch.zeros((T, H), dtype=torch.float16), bf(H), 1e-6, None, bf(T, H))
+    with pytest.raises(ValueError, match="residual stream"):
         ep.ep_rmsnorm_bwd(bf(T, H), torch.zeros((T, H), dtype=torch.float16), bf(H), None, 1e-6, bf(T, H))
     with pytest.raises(ValueError, match="x must be a CUDA tensor"):
         ep.ep_rmsnorm(bf(T, H), None, bf(H), 1e-6, None, bf(T, H))
