@@ -38,7 +38,8 @@ from ._lib import (  # noqa: F401
     ep_combine_permuted_bwd, ep_rmsnorm, ep_rmsnorm_bwd, ep_rmsnorm_bwd_workspace_size,
 )
 from .api import (  # noqa: F401
-    Dispatched, Layout, alloc_dispatch, alloc_layout, combine, combine_fp8, combine_weights, dispatch, get_layout,
-    read_flags,
+    Dispatched, ExpertLayout, Layout, Normed, Permuted, alloc_dispatch, alloc_layout, alloc_permuted, combine,
+    combine_fp8, combine_permuted, combine_permuted_bwd, combine_weights, dispatch, dispatch_permuted,
+    dispatch_permuted_bwd, get_expert_layout, get_layout, read_flags, rmsnorm, rmsnorm_bwd,
 )
 from .build import LIB_PATH, build as build_library  # noqa: F401

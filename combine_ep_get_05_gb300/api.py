@@ -123,3 +123,128 @@ def combine_weights(recv_topk_w, layout: Layout, max_tokens: int, out=None, stat
     L.ep_combine_weights(recv_topk_w, layout.slot, max_tokens, out, status)
     return out
 
+
+
+# --------------------------------------------------------------------------- expert-major path
+
+@dataclass
+class ExpertLayout:
+    offsets: torch.Tensor    # int32 [E+1]: first row of every expert, all ranks' rows counted through
+    slot: torch.Tensor       # int32 [T][k]: place among the expert's rows, -1 where not counted
+    workspace: torch.Tensor  # uint8, zero-filled once, reusable
+    status: torch.Tensor     # int32 [1]
+    num_experts: int
+
+
+@dataclass
+class Permuted:
+    perm_x: torch.Tensor                  # bf16 rows or E4M3 codes [R][max_rows][H]
+    perm_scales: Optional[torch.Tensor]   # fp32 [R][max_rows][H/128] (E4M3 only)
+    perm_src: torch.Tensor                # int32 [R][max_rows]
+    perm_w: Optional[torch.Tensor]        # fp32 [R][max_rows]
+    status: torch.Tensor
+
+
+@dataclass
+class Normed:
+    residual: torch.Tensor                # x + residual (x itself where there is none)
+    y: Optional[torch.Tensor]             # bf16 [T][H]
+    y_q: Optional[torch.Tensor]           # float8_e4m3fn [T][H]
+    y_scales: Optional[torch.Tensor]      # fp32 [T][H/128]
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+            bf16: bool = True, fp8: bool = False, stream=None) -> Normed:
+    """x + residual and its RMS norm, as bf16 rows, as E4M3 rows with 1x128 scales, or both."""
+    T, H = x.shape
+    dev = x.device
+    z = torch.empty_like(residual) if residual is not None else None
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None
+    q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev) if fp8 else None
+    s = torch.empty((T, H // 128), dtype=torch.float32, device=dev) if fp8 else None
+    L.ep_rmsnorm(x, residual, weight, eps, z, y, q, s, stream)
+    return Normed(z if z is not None else x, y, q, s)
+
+
+def rmsnorm_bwd(dy: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, eps: float,
+                dz: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of rmsnorm at z = Normed.residual, with the gradient dz that arrives along the
+    stream: (gradient of residual in the stream's type, gradient of x in bf16, fp32 dweight)."""
+    T, H = z.shape
+    out = torch.empty_like(z)
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device=z.device) if z.dtype != torch.bfloat16 else None
+    dw = torch.empty(H, dtype=torch.float32, device=z.device)
+    ws = torch.empty(L.ep_rmsnorm_bwd_workspace_size(T, H), dtype=torch.uint8, device=z.device)
+    L.ep_rmsnorm_bwd(dy, z, weight, dz, eps, out, dx, dw, ws, stream)
+    return out, dx if dx is not None else out, dw
+
+
+def get_expert_layout(topk_idx: torch.Tensor, num_experts: int, stream=None) -> ExpertLayout:
+    T, k = topk_idx.shape
+    dev = topk_idx.device
+    i32 = dict(dtype=torch.int32, device=dev)
+    ws = torch.zeros(L.ep_expert_layout_workspace_size(T, num_experts), dtype=torch.uint8, device=dev)
+    lay = ExpertLayout(torch.empty(num_experts + 1, **i32), torch.empty((T, k), **i32), ws, torch.zeros(1, **i32),
+                       num_experts)
+    L.ep_get_expert_layout(topk_idx, num_experts, lay.offsets, lay.slot, ws, lay.status, stream)
+    return lay
+
+
+def alloc_permuted(num_ranks: int, max_rows: int, H: int, fp8: bool = False, weights: bool = True,
+                   device="cuda") -> Permuted:
+    """Zero-filled slabs: rows that no token is sent to stay zero."""
+    dev = torch.device(device)
+    x = torch.zeros((num_ranks, max_rows, H), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
+    return Permuted(
+        perm_x=x.view(torch.float8_e4m3fn) if fp8 else x,
+        perm_scales=torch.zeros((num_ranks, max_rows, H // 128), dtype=torch.float32, device=dev) if fp8 else None,
+        perm_src=torch.full((num_ranks, max_rows), -1, dtype=torch.int32, device=dev),
+        perm_w=torch.zeros((num_ranks, max_rows), dtype=torch.float32, device=dev) if weights else None,
+        status=torch.zeros(1, dtype=torch.int32, device=dev),
+    )
+
+
+def dispatch_permuted(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[torch.Tensor], layout: ExpertLayout,
+                      num_ranks: int, max_rows: int, scales: Optional[torch.Tensor] = None,
+                      out: Optional[Permuted] = None, stream=None) -> Permuted:
+    """Rows into expert order: bf16 rows, or E4M3 codes with their scales."""
+    p = out if out is not None else alloc_permuted(num_ranks, max_rows, x.shape[1], scales is not None,
+                                                   topk_w is not None, x.device)
+    if scales is None:
+        L.ep_dispatch_permuted(x, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, num_ranks,
+                               max_rows, p.perm_x, p.perm_src, p.perm_w, p.status, stream)
+    else:
+        L.ep_dispatch_permuted_fp8(x, scales, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts,
+                                   num_ranks, max_rows, p.perm_x, p.perm_scales, p.perm_src, p.perm_w, p.status,
+                                   stream)
+    return p
+
+
+def dispatch_permuted_bwd(dperm_x: torch.Tensor, topk_idx: torch.Tensor, layout: ExpertLayout,
+                          dperm_w: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                          status: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of dispatch_permuted, added to `dx` (another gradient of x) where given: (dx, dtopk_w or None)."""
+    T, k = topk_idx.shape
+    out = torch.empty((T, dperm_x.shape[2]), dtype=torch.bfloat16, device=dperm_x.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dperm_x.device) if dperm_w is not None else None
+    L.ep_dispatch_permuted_bwd(dperm_x, dperm_w, dx, topk_idx, layout.offsets, layout.slot, layout.num_experts, out,
+                               dw, status, stream)
+    return out, dw
+
+
+def combine_permuted(y: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[torch.Tensor], layout: ExpertLayout,
+                     status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows back to token order, weighted where topk_w is given."""
+    out = torch.empty((topk_idx.shape[0], y.shape[2]), dtype=torch.bfloat16, device=y.device)
+    L.ep_combine_permuted(y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, out, status, stream)
+    return out
+
+
+def combine_permuted_bwd(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                         layout: ExpertLayout, status: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of the weighted combine_permuted: (dy with zeros in rows that hold no entry, dtopk_w)."""
+    dy = torch.zeros_like(y)
+    dw = torch.empty_like(topk_w)
+    L.ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, dy, dw,
+                              status, stream)
+    return dy, dw
