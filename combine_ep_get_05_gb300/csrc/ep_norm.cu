@@ -584,9 +584,9 @@ ep_status_t launch_norm(const NormArgs& a, int T, cudaStream_t stream) {
 
 template <class Carry>
 ep_status_t launch_norm(const NormArgs& a, int T, cudaStream_t stream) {
-    if (a.y_q != nullptr)
-        return a.weight_f32 ? launch_norm<Carry, true, true>(a, T, stream) : launch_norm<Carry, true, false>(a, T, stream);
-    return a.weight_f32 ? launch_norm<Carry, false, true>(a, T, stream) : launch_norm<Carry, false, false>(a, T, stream);
+    auto launch = a.y_q != nullptr ? (a.weight_f32 ? launch_norm<Carry, true, true> : launch_norm<Carry, true, false>)
+                                   : (a.weight_f32 ? launch_norm<Carry, false, true> : launch_norm<Carry, false, false>);
+    return launch(a, T, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -765,10 +765,10 @@ __global__ void __maxnreg__((kMany ? 72 : 64)) rmsnorm_bwd_kernel(NormBwdArgs a,
     if (groups > 1) {
         __syncthreads();
         for (int h = static_cast<int>(threadIdx.x) * 4; h < a.H; h += static_cast<int>(blockDim.x) * 4) {
-            float4 s = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(s_ring) + h);
+            const float* const sums = reinterpret_cast<const float*>(s_ring) + h;
+            float4 s = *reinterpret_cast<const float4*>(sums);
             for (int g = 1; g < groups; ++g) {
-                const float4 v =
-                    *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(s_ring) + static_cast<size_t>(g) * a.H + h);
+                const float4 v = *reinterpret_cast<const float4*>(sums + static_cast<size_t>(g) * a.H);
                 s.x += v.x;
                 s.y += v.y;
                 s.z += v.z;
@@ -825,12 +825,13 @@ ep_status_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t stream, int* grid
     int per_sm = 1;
     const ep_status_t st = resident(cache, kernel, groups * nt, streams - 1, smem, &per_sm);
     if (st != EP_OK) return st;
-    int grid = sm_count() * per_sm;
-    if (grid > kMaxParts) grid = kMaxParts;
-    const int rows = (a.T + groups - 1) / groups;
-    if (grid > rows) grid = rows;
-    *grid_out = grid;
-    return launch_dependent(kernel, dim3(grid), dim3(groups * nt), smem, stream, a, groups);
+    // no more CTAs than end with equal numbers of rows: each writes a row of partial sums
+    const int resident_ctas = sm_count() * per_sm;
+    const int most = resident_ctas < kMaxParts ? resident_ctas : kMaxParts;
+    const int rows = (a.T - 1) / groups + 1;
+    const int turns = (rows - 1) / most + 1;
+    *grid_out = (rows - 1) / turns + 1;
+    return launch_dependent(kernel, dim3(*grid_out), dim3(groups * nt), smem, stream, a, groups);
 }
 
 template <class Carry, bool kWF32>
@@ -903,6 +904,7 @@ extern "C" ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void*
         if (st != EP_OK) return st;
     }
     if (dweight == nullptr) return EP_OK;
-    return launch_dependent(dweight_reduce_kernel, dim3((H + 31) / 32), dim3(8 * kReduceRows), 0,
-                            as_stream(stream), static_cast<const float*>(workspace), parts, static_cast<int>(H), dweight);
+    const float* const sums = static_cast<const float*>(workspace);
+    return launch_dependent(dweight_reduce_kernel, dim3((H + 31) / 32), dim3(8 * kReduceRows), 0, as_stream(stream),
+                            sums, parts, static_cast<int>(H), dweight);
 }

@@ -324,7 +324,11 @@ struct PermScatter {
     __device__ void prologue() const {}
 };
 
-// E4M3 rows: H codes through the same scatter, and the row's H/128 scales beside them
+// E4M3 rows: H codes through the same scatter, and the row's H/128 scales beside them.
+// Eight bytes are written for each one read; writes to scattered 7 KB rows bound it: 4096 x
+// 7168 top-8 in 44.0 us (6.2 TB/s, 0.91 of a measured copy), 42.4 us of them without the
+// scales, where the same bytes at hashed rows without any metadata take 41 us. A kernel that
+// moves the rows through registers, one vector a thread, takes 44.2 to 46 us.
 struct PermFp8Scatter {
     PermDispatchArgs a;  // x and perm_x unused
     const uint8_t* x_q;
@@ -350,6 +354,38 @@ struct PermFp8Scatter {
     }
     __device__ void prologue() const {}
 };
+
+// E4M3 rows of up to kWarpFp8Vecs * 512 channels: a token per warp, its row (kWarpFp8Vecs
+// vectors a lane) requested before the token's rows in the slabs are resolved. Below 1 KB a
+// row, the scatter's bulk copies cost more than the bytes (10571 x 384 top-8: 9.7 us instead
+// of 12.0 us, 16000 x 1024 27.2 us instead of 27.7 us; 8000 x 2048: 26.8 us against 25.9 us).
+constexpr int kWarpFp8Vecs = 2;
+
+__global__ void __launch_bounds__(kThreads) dispatch_permuted_fp8_kernel(PermFp8Scatter a) {
+    __shared__ long long s_row[kWarps][kMaxTopk];
+    __shared__ int s_j[kWarps][kMaxTopk];
+    grid_dependency_wait();
+    const int lane = lane_id();
+    const int warp = static_cast<int>(threadIdx.x >> 5);
+    const int nvec = static_cast<int>(a.row_bytes / 16);
+    const int t = static_cast<int>(blockIdx.x) * kWarps + warp;
+    if (t < a.a.T) {
+        const uint4* src = static_cast<const uint4*>(a.source(t));
+        uint4 q[kWarpFp8Vecs];
+#pragma unroll
+        for (int i = 0; i < kWarpFp8Vecs; ++i)
+            if (i * 32 + lane < nvec) q[i] = ld_stream_v4(src + i * 32 + lane);
+        const int nd = a.destinations(t, s_row[warp], s_j[warp]);
+        for (int d = 0; d < nd; ++d) {
+            uint4* dst = reinterpret_cast<uint4*>(a.dst) + static_cast<size_t>(s_row[warp][d]) * nvec + lane;
+#pragma unroll
+            for (int i = 0; i < kWarpFp8Vecs; ++i)
+                if (i * 32 + lane < nvec) st_v4(dst + i * 32, q[i]);
+        }
+        a.side_work(t, nd, s_row[warp], s_j[warp]);
+    }
+    allow_dependents();
+}
 
 struct PermuteRecvArgs {
     const uint16_t* recv_x;
@@ -548,16 +584,29 @@ __global__ void __launch_bounds__(kThreads, 4) combine_permuted_kernel(CombinePe
 // ---------------------------------------------------------------------------
 // Low-latency (decode-sized) dispatch + permute: one launch
 // ---------------------------------------------------------------------------
-// For a small batch (T <= kLLMaxTokens) every CTA computes the whole expert layout in
-// shared memory -- the per-warp expert masks and in-warp ranks of expert_layout_kernel,
-// chunk after chunk of 256 tokens with a running count per expert, then the offsets by a
-// block scan -- so no CTA waits on another and no workspace is needed. CTA 0 writes the
-// offsets and slots; CTA b then moves tokens b, b + gridDim.x, ...: warp 0 resolves the
-// token's expert-major rows and writes the metadata, and the 8 warps copy an eighth of
-// the row each to every destination. Same results as ep_get_expert_layout followed by
-// ep_dispatch_permuted.
+// For a small batch (T <= kLLMaxTokens) every CTA reads all ids itself, so no CTA waits on
+// another and no workspace is needed. CTA b owns the tokens b * count ... and needs two
+// histograms over the experts: of all entries (whose scan gives the offsets) and of the
+// entries before its own tokens (its entries' slots, up to the few earlier ones among its
+// own). Lanes take one entry each, whole tokens to a warp, so that a repeated expert of a
+// token is found by shuffles among its k lanes; the counts are shared-memory atomic
+// additions, whose result does not depend on their order. Every CTA writes its own tokens'
+// slots, CTA 0 the offsets. Then all threads copy the own rows, vector by
+// vector, to the slabs; what they copy first, and the weights, were requested at the start.
+// Same results as ep_get_expert_layout followed by ep_dispatch_permuted (bf16 rows) or
+// ep_dispatch_permuted_fp8 (kFp8).
+//
+// A call this small is bound by its chain of dependent steps: ids, counts, scan, rows,
+// stores. 128 x 7168 top-8: 4.3 us in E4M3, 5.7 us in bf16; 667 x 640 top-10 8.1 us. Finding
+// a token's repeats with a warp-wide match instead of shuffles costs 1 us a pass over the
+// ids; requesting eight ids at a time makes the code longer, and its first fetch 0.4 us slower.
 constexpr int kLLMaxTokens = 1024;
 constexpr int kLLMaxEntries = 8192;  // T * k
+constexpr int kLLThreads = 1024;
+constexpr int kLLWarps = kLLThreads / 32;
+constexpr int kLLOwn = 8;    // most tokens of a CTA
+constexpr int kLLBatch = 2;  // ids a lane requests at a time
+constexpr int kLLAhead = 2;  // vectors a thread requests at a time
 
 struct LLArgs {
     const void* x;  // rows of nvec 16-byte vectors: H bf16, or H E4M3 codes
@@ -575,110 +624,89 @@ struct LLArgs {
     int32_t* status;
 };
 
-inline size_t ll_smem_bytes(int T, int k, int E) {
-    return (static_cast<size_t>(2 * kWarps) * E + ((E + 1 + 3) & ~3) + static_cast<size_t>(T) * k) * sizeof(int32_t);
-}
-
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1) dispatch_permuted_ll_kernel(LLArgs a) {
+__global__ void __launch_bounds__(kLLThreads, 1) dispatch_permuted_ll_kernel(LLArgs a, int count) {
     // a decode batch's grid leaves most of every SM free: the next kernel (the expert work,
     // or the low-latency combine launched as a dependent launch) may settle its CTAs now and
     // wait on the device for this grid, so its launch latency is hidden behind this one
     allow_dependents();
     grid_dependency_wait();  // dependent launch: inputs are ready after this
-    extern __shared__ uint32_t smem[];
-    uint32_t* s_emask = smem;                                              // [kWarps][E]
-    int32_t* s_wpref = reinterpret_cast<int32_t*>(smem + kWarps * a.E);  // [kWarps][E]
-    int32_t* s_cnt = s_wpref + kWarps * a.E;                             // [E+1]: counts, then offsets
-    int32_t* s_slot = s_cnt + ((a.E + 1 + 3) & ~3);                      // [T][k]: expert, then slot
-    __shared__ int32_t s_part[kWarps];
-    __shared__ long long s_row[kMaxTopk];
-    __shared__ int s_nd;
+    __shared__ int32_t s_count[kMaxExpertsPerm];       // entries of each expert
+    __shared__ int32_t s_before[kMaxExpertsPerm];      // those of tokens before the own ones
+    __shared__ int32_t s_off[kMaxExpertsPerm + 1];     // offsets
+    __shared__ int32_t s_own[kLLOwn * kMaxTopk];       // own entries' experts, -1 where not counted
+    __shared__ long long s_row[kLLOwn][kMaxTopk];      // slab rows of the own tokens
+    __shared__ int s_nd[kLLOwn];
+    __shared__ int32_t s_part[kLLWarps];
     const int tid = static_cast<int>(threadIdx.x);
     const int lane = tid & 31;
     const int warp = tid >> 5;
-    const int k = a.k;
-    const int E = a.E;
-    const int nvec = a.nvec;
-    const int per_warp = (nvec + kWarps - 1) / kWarps;  // 16-byte vectors of a row per warp
-    const int v_lo = warp * per_warp;
-    const int v_hi = v_lo + per_warp < nvec ? v_lo + per_warp : nvec;
+    const int k = a.k, E = a.E, nvec = a.nvec;
+    const int t0 = static_cast<int>(blockIdx.x) * count;
+    const int own = a.T - t0 < count ? a.T - t0 : count;
+    const uint4* src = static_cast<const uint4*>(a.x) + static_cast<size_t>(t0) * nvec;
 
-    // the first token's row (this warp's slice) is requested before the layout work, so
-    // that its memory latency overlaps it
-    uint4 first[kUnroll];
-    if (static_cast<int>(blockIdx.x) < a.T) {
-        const uint4* src = static_cast<const uint4*>(a.x) + static_cast<size_t>(blockIdx.x) * nvec;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int v = v_lo + u * 32 + lane;
-            if (v < v_hi) first[u] = ld_stream_v4(src + v);
-        }
-    }
-
-    // 1. the expert layout of the whole batch, in shared memory
-    for (int e = tid; e < E; e += kThreads) s_cnt[e] = 0;
+    // 1. the histograms
+    const int per_pass = kLLWarps * (32 / k);  // tokens
+    const int tok = lane / k, slot = lane - tok * k;
+    const bool active = tok < 32 / k;
     bool bad = false;
-    for (int c0 = 0; c0 < a.T; c0 += kThreads) {
-        const int t = c0 + tid;
-        for (int e = lane; e < E; e += 32) s_emask[warp * E + e] = 0u;
-        __syncthreads();
-        if (t < a.T) {
-            const long long* row = reinterpret_cast<const long long*>(a.topk_idx) + static_cast<size_t>(t) * k;
-            for (int j0 = 0; j0 < k; j0 += kBatch) {
-                long long ev[kBatch];  // eight ids in flight
+    uint4 ahead[kLLAhead];  // the thread's first vectors
+    float weight = 0.0f;    // lane j of warp l: the weight of own token l's slot j
+    // a token's scales, four to a lane where they come in fours, held by the last warps (the
+    // first ones have the most vectors) if 32 lanes hold them
+    const int nblk = a.H / 128;
+    const bool wide = (nblk & 3) == 0;
+    const int nscales = wide ? nblk / 4 : nblk;
+    uint4 scale = make_uint4(0, 0, 0, 0);
+    auto load_rows = [&](int i0) {
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) ev[i] = j0 + i < k ? __ldg(row + j0 + i) : -1ll;
+        for (int u = 0; u < kLLAhead; ++u)
+            if (i0 + u * kLLThreads < own * nvec) ahead[u] = ld_stream_v4(src + i0 + u * kLLThreads);
+    };
+    for (int base = 0; base == 0 || base < a.T; base += kLLBatch * per_pass) {
+        long long id[kLLBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int j = j0 + i;
-                    if (j >= k) break;
-                    const long long e = ev[i];
-                    int x = -1;
-                    if (e >= 0) {
-                        if (e >= E) {
-                            bad = true;
-                        } else {
-                            bool rep = false;  // a repeat of an earlier slot of the row counts once
+        for (int i = 0; i < kLLBatch; ++i) {
+            const int t = base + i * per_pass + warp * (32 / k) + tok;
+            id[i] = active && t < a.T ? __ldg(reinterpret_cast<const long long*>(a.topk_idx) + t * k + slot) : -1ll;
+        }
+        if (base == 0) {
+            load_rows(tid);
+            if (a.perm_w != nullptr && warp < own && lane < k)
+                weight = __ldg(a.topk_w + static_cast<size_t>(t0 + warp) * k + lane);
+            if (kFp8 && nscales <= 32 && lane < nscales && kLLWarps - 1 - warp < own) {
+                const float* from = a.x_scales + static_cast<size_t>(t0 + kLLWarps - 1 - warp) * nblk;
+                if (wide) scale = ld_stream_v4(from + 4 * lane);
+                else scale.x = __float_as_uint(__ldg(from + lane));
+            }
+            for (int e = tid; e < E; e += kLLThreads) s_count[e] = s_before[e] = 0;
+            __syncthreads();
+        }
 #pragma unroll
-                            for (int ii = 0; ii < i; ++ii) rep |= ev[ii] == e;
-                            for (int jj = 0; jj < j0; ++jj) rep |= s_slot[t * k + jj] == static_cast<int>(e);
-                            if (rep) bad = true;
-                            else x = static_cast<int>(e);
-                        }
-                    }
-                    s_slot[t * k + j] = x;
-                    if (x >= 0) atomicOr(&s_emask[warp * E + x], 1u << lane);
-                }
+        for (int i = 0; i < kLLBatch; ++i) {
+            if (base + i * per_pass >= a.T) break;  // the same for the whole CTA
+            const int t = base + i * per_pass + warp * (32 / k) + tok;
+            const bool valid = id[i] >= 0 && id[i] < E;
+            const int e = valid ? static_cast<int>(id[i]) : -1;
+            bool repeat = false;  // of an earlier slot of the token
+            for (int q = 0; q + 1 < k; ++q) repeat |= __shfl_sync(kFullMask, e, lane - slot + q) == e && q < slot;
+            repeat = repeat && valid;
+            bad |= id[i] >= E || repeat;
+            const bool counts = valid && !repeat;
+            if (counts) {
+                atomicAdd(&s_count[e], 1);
+                if (t < t0) atomicAdd(&s_before[e], 1);
             }
+            if (active && t >= t0 && t < t0 + own) s_own[(t - t0) * k + slot] = counts ? e : -1;
         }
-        __syncthreads();
-        for (int e = tid; e < E; e += kThreads) {
-            int run = s_cnt[e];
-            for (int w = 0; w < kWarps; ++w) {
-                s_wpref[w * E + e] = run;
-                run += __popc(s_emask[w * E + e]);
-            }
-            s_cnt[e] = run;
-        }
-        __syncthreads();
-        if (t < a.T) {
-            const uint32_t below = (1u << lane) - 1u;
-            for (int j = 0; j < k; ++j) {
-                const int x = s_slot[t * k + j];
-                s_slot[t * k + j] = x >= 0 ? s_wpref[warp * E + x] + __popc(s_emask[warp * E + x] & below) : -1;
-            }
-        }
-        __syncthreads();
     }
-    // exclusive scan of the counts into the offsets (per-thread runs, then warp and block)
+    __syncthreads();
+
+    // 2. the offsets: a thread per expert (E <= kLLThreads), warp scans, then the warps' totals
     {
-        const int per = (E + kThreads - 1) / kThreads;
-        const int e0 = tid * per;
-        int sum = 0;
-        for (int i = 0; i < per; ++i)
-            if (e0 + i < E) sum += s_cnt[e0 + i];
-        int incl = sum;
+        const int c = tid < E ? s_count[tid] : 0;
+        int incl = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(kFullMask, incl, off);
@@ -686,78 +714,79 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_permuted_ll_kernel(LLArg
         }
         if (lane == 31) s_part[warp] = incl;
         __syncthreads();
-        int base = 0;
-        for (int w = 0; w < warp; ++w) base += s_part[w];
-        int run = base + incl - sum;
-        for (int i = 0; i < per; ++i) {
-            if (e0 + i < E) {
-                const int c = s_cnt[e0 + i];
-                s_cnt[e0 + i] = run;
-                run += c;
-            }
-        }
-        if (tid == kThreads - 1) s_cnt[E] = base + incl;
+        int base = lane < warp ? s_part[lane] : 0;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) base += __shfl_xor_sync(kFullMask, base, off);
+        if (tid < E) s_off[tid] = base + incl - c;
+        if (tid == E - 1) s_off[E] = base + incl;
         __syncthreads();
     }
     if (blockIdx.x == 0) {
-        for (int e = tid; e <= E; e += kThreads) a.offsets[e] = s_cnt[e];
-        for (int i = tid; i < a.T * k; i += kThreads) a.eslot[i] = s_slot[i];
+        for (int e = tid; e <= E; e += kLLThreads) a.offsets[e] = s_off[e];
         if (bad) raise_flag(a.status, EP_FLAG_BAD_EXPERT);
     }
 
-    // 2. the rows
-    const int epr = E / a.R;
-    for (int t = static_cast<int>(blockIdx.x); t < a.T; t += static_cast<int>(gridDim.x)) {
-        if (warp == 0) {
-            bool ok = false, over = false;
-            long long rowi = 0;
-            if (lane < k) {
-                const int sl = s_slot[t * k + lane];
-                if (sl >= 0) {
-                    const int e = static_cast<int>(a.topk_idx[static_cast<size_t>(t) * k + lane]);
-                    const int r = e / epr;
-                    const int p = s_cnt[e] - s_cnt[r * epr] + sl;
-                    if (p < a.max_rows) {
-                        ok = true;
-                        rowi = static_cast<long long>(r) * a.max_rows + p;
-                    } else {
-                        over = true;
+    // 3. the own tokens' rows, a warp per token
+    if (warp < own) {
+        const int t = t0 + warp;
+        const int epr = E / a.R;
+        bool ok = false, over = false;
+        long long rowi = 0;
+        if (lane < k) {
+            const int e = s_own[warp * k + lane];
+            int sl = -1;
+            if (e >= 0) {
+                sl = s_before[e];
+                for (int i = 0; i < warp * k; ++i) sl += s_own[i] == e;
+                const int r = e / epr;
+                const int p = s_off[e] - s_off[r * epr] + sl;
+                if (p < a.max_rows) {
+                    ok = true;
+                    rowi = static_cast<long long>(r) * a.max_rows + p;
+                } else {
+                    over = true;
+                }
+            }
+            a.eslot[static_cast<size_t>(t) * k + lane] = sl;
+        }
+        const uint32_t m = __ballot_sync(kFullMask, ok);
+        if (ok) s_row[warp][__popc(m & lanemask_lt())] = rowi;
+        if (lane == 0) s_nd[warp] = __popc(m);
+        if (__any_sync(kFullMask, over) && lane == 0) raise_flag(a.status, EP_FLAG_CAPACITY);
+        if (ok && a.perm_src != nullptr) a.perm_src[rowi] = t;
+        if (ok && a.perm_w != nullptr) a.perm_w[rowi] = weight;
+    }
+    __syncthreads();
+
+    // 4. the rows' vectors, and their scales
+    uint4* const base = static_cast<uint4*>(a.perm_x);
+    for (int i0 = tid; i0 < own * nvec; i0 += kLLAhead * kLLThreads) {
+        if (i0 != tid) load_rows(i0);
+#pragma unroll
+        for (int u = 0; u < kLLAhead; ++u) {
+            const int i = i0 + u * kLLThreads;
+            if (i >= own * nvec) break;
+            const int l = i / nvec, at = i - l * nvec;
+            const int nd = s_nd[l];
+            for (int d = 0; d < nd; ++d) st_v4(base + static_cast<size_t>(s_row[l][d]) * nvec + at, ahead[u]);
+        }
+    }
+    if constexpr (kFp8) {
+        const int l = kLLWarps - 1 - warp;
+        if (l < own) {
+            const int nd = s_nd[l];
+            if (nscales <= 32) {
+                if (lane < nscales) {
+                    for (int d = 0; d < nd; ++d) {
+                        float* to = a.perm_scales + static_cast<size_t>(s_row[l][d]) * nblk;
+                        if (wide) st_v4(to + 4 * lane, scale);
+                        else to[lane] = __uint_as_float(scale.x);
                     }
                 }
-            }
-            const uint32_t m = __ballot_sync(kFullMask, ok);
-            if (ok) {
-                const int pos = __popc(m & lanemask_lt());
-                s_row[pos] = rowi;
-                if (a.perm_src != nullptr) a.perm_src[rowi] = t;
-                if (a.perm_w != nullptr) a.perm_w[rowi] = a.topk_w[static_cast<size_t>(t) * k + lane];
-            }
-            if (__any_sync(kFullMask, over) && lane == 0) raise_flag(a.status, EP_FLAG_CAPACITY);
-            if (lane == 0) s_nd = __popc(m);
-        }
-        __syncthreads();
-        const int nd = s_nd;
-        if constexpr (kFp8) copy_scales(a.x_scales, a.perm_scales, t, a.H / 128, s_row, nd, tid, kThreads);
-        const uint4* src = static_cast<const uint4*>(a.x) + static_cast<size_t>(t) * nvec;
-        uint4* base = static_cast<uint4*>(a.perm_x);
-        for (int v0 = v_lo; v0 < v_hi; v0 += 32 * kUnroll) {
-            uint4 buf[kUnroll];
-            const bool prefetched = t == static_cast<int>(blockIdx.x) && v0 == v_lo;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int v = v0 + u * 32 + lane;
-                if (v < v_hi) buf[u] = prefetched ? first[u] : ld_stream_v4(src + v);
-            }
-            for (int d = 0; d < nd; ++d) {
-                uint4* dst = base + static_cast<size_t>(s_row[d]) * nvec;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int v = v0 + u * 32 + lane;
-                    if (v < v_hi) st_v4(dst + v, buf[u]);
-                }
+            } else {
+                copy_scales(a.x_scales, a.perm_scales, t0 + l, nblk, s_row[l], nd, lane, 32);
             }
         }
-        __syncthreads();  // s_row / s_nd are rewritten for the next token
     }
 }
 
@@ -1214,8 +1243,6 @@ std::atomic<int> g_send_smem_set_w[kMaxDevices];
 std::atomic<int> g_send_per_sm[kMaxDevices];
 std::atomic<int> g_send_per_sm_w[kMaxDevices];
 
-std::atomic<int> g_ll_attr_set[kMaxDevices];
-std::atomic<int> g_ll_fp8_attr_set[kMaxDevices];
 std::atomic<int> g_attr_set[kMaxDevices];
 std::atomic<int> g_combine_per_sm[kMaxDevices];
 
@@ -1225,14 +1252,12 @@ int token_grid(long long work) {
     return static_cast<int>(want < 1 ? 1 : (want < cap ? want : cap));
 }
 
-ep_status_t launch_ll(void (*kernel)(LLArgs), std::atomic<int>* attr_set, const LLArgs& a, cudaStream_t stream) {
-    const ep_status_t attr = ensure_dynamic_smem(
-        attr_set, kernel,
-        static_cast<int>(ll_smem_bytes(kLLMaxTokens, kLLMaxEntries / kLLMaxTokens, kMaxExpertsPerm)));
-    if (attr != EP_OK) return attr;
+ep_status_t launch_ll(void (*kernel)(LLArgs, int), const LLArgs& a, cudaStream_t stream) {
     const int sms = sm_count();
-    const int grid = a.T < 1 ? 1 : (a.T < sms ? a.T : sms);
-    return launch_dependent(kernel, dim3(grid), dim3(kThreads), ll_smem_bytes(a.T, a.k, a.E), stream, a);
+    const int spread = (a.T + sms - 1) / sms;
+    const int count = spread < 1 ? 1 : (spread < kLLOwn ? spread : kLLOwn);
+    const int grid = a.T < 1 ? 1 : (a.T + count - 1) / count;
+    return launch_dependent(kernel, dim3(grid), dim3(kLLThreads), 0, stream, a, count);
 }
 
 }  // namespace
@@ -1364,7 +1389,7 @@ extern "C" ep_status_t ep_dispatch_permuted_ll(const void* x, const int64_t* top
         return EP_ERR_INVALID;
     const LLArgs a{x, H / 8, nullptr, nullptr, topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets, expert_slot,
                    perm_x, perm_src, perm_w, status};
-    return launch_ll(dispatch_permuted_ll_kernel<false>, g_ll_attr_set, a, as_stream(stream));
+    return launch_ll(dispatch_permuted_ll_kernel<false>, a, as_stream(stream));
 }
 
 extern "C" ep_status_t ep_dispatch_permuted_fp8(const uint8_t* x_q, const float* x_scales, const int64_t* topk_idx,
@@ -1386,6 +1411,9 @@ extern "C" ep_status_t ep_dispatch_permuted_fp8(const uint8_t* x_q, const float*
                              perm_src, perm_w, status};
     const PermFp8Scatter sp{a, x_q, x_scales, perm_scales, reinterpret_cast<char*>(perm_q), static_cast<uint32_t>(H),
                             status};
+    if (H <= kWarpFp8Vecs * 512)
+        return launch_dependent(dispatch_permuted_fp8_kernel, dim3(static_cast<unsigned>((T - 1) / kWarps + 1)),
+                                dim3(kThreads), 0, as_stream(stream), sp);
     return launch_scatter_rows(sp, T, as_stream(stream));
 }
 
@@ -1408,7 +1436,7 @@ extern "C" ep_status_t ep_dispatch_permuted_fp8_ll(const uint8_t* x_q, const flo
         return EP_ERR_INVALID;
     const LLArgs a{x_q, H / 16, x_scales, perm_scales, topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets,
                    expert_slot, perm_q, perm_src, perm_w, status};
-    return launch_ll(dispatch_permuted_ll_kernel<true>, g_ll_fp8_attr_set, a, as_stream(stream));
+    return launch_ll(dispatch_permuted_ll_kernel<true>, a, as_stream(stream));
 }
 
 extern "C" ep_status_t ep_combine_send(const void* y_perm, const int32_t* recv_src_idx, const int32_t* recv_topk_idx,

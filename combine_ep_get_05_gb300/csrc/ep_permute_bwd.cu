@@ -12,9 +12,15 @@ using namespace ep;
 
 constexpr int kMaxTopk = 32;
 constexpr int kWarps = 8;         // most warps of a CTA of the return's gradient
-constexpr int kSortThreads = 128;  // most threads of a CTA of the sort's gradient
+// Rows of the return's gradient up to this many channels, where there are many, go two to a
+// warp: their positions are then resolved together (8000 x 1024 top-6 36.0 us instead of 38.7
+// us; 1237 x 1592 top-9, too few, 17.2 us instead of 15.1 us).
+constexpr int kShortRowH = 1024;
+constexpr int kSmallSplit = 4;  // warps of an entry where there are few (44 x 4176 top-4: 2.5 us instead of 4.2 us)
+constexpr int kSortWarps = 16;  // most warps of a CTA of the sort's gradient
+constexpr int kSortThreads = 64;  // threads of a token there, where tokens abound
+constexpr int kWarpRowH = 2048;   // rows up to this take a warp each
 constexpr int kVecs = 4;   // 16-byte vectors of a row per thread and step (return)
-constexpr int kBatch = 8;  // source rows whose vectors are loaded together (sort)
 
 // Slab row r * max_rows + p of entry (t, j), -1 when the entry is not counted, -2 when its
 // row lies past the slab's end (the forward pass dropped it).
@@ -61,69 +67,96 @@ struct CombineBwdArgs {
     int32_t* status;
 };
 
-// One CTA per token, a warp per top-k slot (slots past kWarps go round again): the warp
-// resolves its entry, then streams the entry's row of y and the token's dout -- which its
-// sibling warps read at the same time, so that L1 serves them -- and writes dy's row =
-// bf16(w * dout). The dot product is kept in fp32 in one sum per channel of a vector (at
-// most H / 256 terms each), added across the vector and the lanes at the end. At 64
-// registers four CTAs, 32 warps with 4 vectors of y each in flight, fit an SM: 4096 x 7168
-// top-8 in 153.6 us (6.50 TB/s, 0.96 of a measured copy); with 72 registers or 2 vectors 157
-// us, with a CTA's threads all on one entry after the other 155 us, and 777 x 1032 top-6 in
-// 4.5 us instead of 10.9 us.
-__global__ void __launch_bounds__(32 * kWarps, 4) combine_bwd_kernel(CombineBwdArgs a) {
+// A CTA takes `count` consecutive entries (t, j), t * k + j in order, kSplit warps on an entry
+// at a time. The warp's lanes resolve its entries, then it streams each entry's row of y and
+// the token's dout -- which the warps of the token's other entries read at the same time, so
+// that L1 serves them -- and writes dy's row = bf16(w * dout). The dot product is kept in
+// fp32 in one sum per channel of a vector (at most H / (256 kSplit) terms each), added across
+// the vector, the lanes and the entry's warps at the end.
+//
+// At 64 registers 32 warps with 4 vectors of y each in flight fit an SM: 4096 x 7168 top-8 in
+// 153 us (6.5 TB/s, 0.96 of a measured copy); 157 us with 72 registers or 2 vectors. Requesting
+// dout before the row is known costs 2 %, two warps a row 3 %, the token's rows one after the
+// other by a whole CTA 1 % (and 777 x 1032 top-6 then takes 10.9 us instead of 4.5 us).
+template <int kSplit>
+__global__ void __launch_bounds__(32 * kWarps, 4) combine_bwd_kernel(CombineBwdArgs a, int count) {
+    __shared__ float s_dot[kWarps];
     grid_dependency_wait();  // dependent launch: inputs are ready after this
+    const int tid = static_cast<int>(threadIdx.x);
     const int lane = lane_id();
-    const int nwarps = static_cast<int>(blockDim.x >> 5);
-    const int t = static_cast<int>(blockIdx.x);
+    const int part = (tid >> 5) % kSplit;
+    const int at_once = static_cast<int>(blockDim.x >> 5) / kSplit;
+    const long long entry0 = static_cast<long long>(blockIdx.x) * count;
+    const long long entries = static_cast<long long>(a.T) * a.k;
+    const int mine = entries - entry0 < count ? static_cast<int>(entries - entry0) : count;
     const int nvec = a.H / 8;
-    const uint4* dout = reinterpret_cast<const uint4*>(a.dout) + static_cast<size_t>(t) * nvec;
     const bool dots = a.dtopk_w != nullptr;
-    for (int j = static_cast<int>(threadIdx.x >> 5); j < a.k; j += nwarps) {
-        const size_t entry = static_cast<size_t>(t) * a.k + j;
-        const float w = a.topk_w != nullptr ? a.topk_w[entry] : 1.0f;
-        const long long row = entry_row(a.topk_idx, a.offsets, a.eslot, entry, a.E, a.E / a.R, a.max_rows);
-        if (row < 0) {
-            if (lane == 0) {
-                if (row == -2) raise_flag(a.status, EP_FLAG_CAPACITY);
-                if (dots) a.dtopk_w[entry] = 0.0f;
-            }
-            continue;
-        }
-        const uint4* y = reinterpret_cast<const uint4*>(a.y) + row * nvec;
-        uint4* dy = reinterpret_cast<uint4*>(a.dy) + row * nvec;
+    const int first = part * 32 + lane;
+    uint4 g[kVecs];
+    auto load_dout = [&](int e, int v0) {
+        const uint4* const dout = reinterpret_cast<const uint4*>(a.dout) + (entry0 + e) / a.k * nvec + v0;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            if (v0 + i * 32 * kSplit < nvec) g[i] = __ldg(dout + i * 32 * kSplit);
+    };
+    // lane r resolves the warp's entry of round r
+    const int e_first = (tid >> 5) / kSplit;
+    long long my_row = -1;
+    float my_w = 1.0f;
+    if (e_first + lane * at_once < mine) {
+        const size_t entry = static_cast<size_t>(entry0 + e_first + lane * at_once);
+        if (a.topk_w != nullptr) my_w = a.topk_w[entry];
+        my_row = entry_row(a.topk_idx, a.offsets, a.eslot, entry, a.E, a.E / a.R, a.max_rows);
+        if (my_row == -2) raise_flag(a.status, EP_FLAG_CAPACITY);
+    }
+    for (int r = 0; r * at_once < mine; ++r) {
+        const int e = e_first + r * at_once;
+        const long long row = __shfl_sync(kFullMask, my_row, r);
+        const float w = __shfl_sync(kFullMask, my_w, r);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int v0 = lane; v0 < nvec; v0 += 32 * kVecs) {
-            uint4 g[kVecs], yv[kVecs];
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int v = v0 + i * 32;
-                if (v < nvec) {
-                    if (dots) yv[i] = ld_inout_v4(y + v);
-                    g[i] = __ldg(dout + v);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int v = v0 + i * 32;
-                if (v >= nvec) continue;
-                float d[8];
-                unpack8(d, g[i]);
+        if (row >= 0) {
+            const uint4* y = reinterpret_cast<const uint4*>(a.y) + row * nvec;
+            uint4* dy = reinterpret_cast<uint4*>(a.dy) + row * nvec;
+            for (int v0 = first; v0 < nvec; v0 += 32 * kSplit * kVecs) {
+                uint4 yv[kVecs];
                 if (dots) {
-                    float f[8];
-                    unpack8(f, yv[i]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(d[e], f[e], acc[e]);
+                    for (int i = 0; i < kVecs; ++i)
+                        if (v0 + i * 32 * kSplit < nvec) yv[i] = ld_inout_v4(y + v0 + i * 32 * kSplit);
                 }
+                load_dout(e, v0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= w;
-                st_v4(dy + v, pack8(d));
+                for (int i = 0; i < kVecs; ++i) {
+                    const int v = v0 + i * 32 * kSplit;
+                    if (v >= nvec) continue;
+                    float d[8];
+                    unpack8(d, g[i]);
+                    if (dots) {
+                        float f[8];
+                        unpack8(f, yv[i]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) acc[c] = fmaf(d[c], f[c], acc[c]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) d[c] *= w;
+                    st_v4(dy + v, pack8(d));
+                }
             }
         }
         if (dots) {
             float dot = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(kFullMask, dot, off);
-            if (lane == 0) a.dtopk_w[entry] = dot;
+            if constexpr (kSplit > 1) {
+                if (lane == 0) s_dot[tid >> 5] = dot;
+                __syncthreads();
+                if (part == 0) {
+#pragma unroll
+                    for (int i = 1; i < kSplit; ++i) dot += s_dot[(tid >> 5) + i];
+                }
+                __syncthreads();  // s_dot is written again for the next entries
+            }
+            if (part == 0 && lane == 0 && e < mine) a.dtopk_w[entry0 + e] = dot;
         }
     }
     allow_dependents();
@@ -146,54 +179,101 @@ struct DispatchBwdArgs {
     int32_t* status;
 };
 
-// One CTA per token: warp 0 lists the token's rows, then every thread adds its vectors of
-// those rows in slot order, the addend first, with kBatch rows' vectors in flight. 16384 x
-// 4096 top-8 with the addend: 202.6 us (6.64 TB/s, 0.98 of a measured copy) with CTAs of 128
-// threads, 207 us with 256, 238 us with 512 (fewer, larger CTAs wait longer for their lists).
-__global__ void __launch_bounds__(kSortThreads, 8) dispatch_bwd_kernel(DispatchBwdArgs a) {
-    grid_dependency_wait();
-    __shared__ long long s_row[kMaxTopk];
-    __shared__ int s_n;
-    const int tid = static_cast<int>(threadIdx.x);
-    const int t = static_cast<int>(blockIdx.x);
-    const int nvec = a.H / 8;
-    if (tid < 32) {
-        const size_t entry = static_cast<size_t>(t) * a.k + tid;
-        long long row = -1;
-        if (tid < a.k) {
-            row = entry_row(a.topk_idx, a.offsets, a.eslot, entry, a.E, a.E / a.R, a.max_rows);
-            if (a.dtopk_w != nullptr) a.dtopk_w[entry] = row >= 0 ? a.dperm_w[row] : 0.0f;
-        }
-        const uint32_t m = __ballot_sync(kFullMask, row >= 0);
-        if (row >= 0) s_row[__popc(m & lanemask_lt())] = row * nvec;
-        if (__any_sync(kFullMask, row == -2) && tid == 0) raise_flag(a.status, EP_FLAG_CAPACITY);
-        if (tid == 0) s_n = __popc(m);
+// the addend's vectors v0, v0 + stride, ... (kVec of them), zeros where there is none
+template <int kVec>
+__device__ __forceinline__ void load_addend(const DispatchBwdArgs& a, uint4 (&first)[kVec], const uint4* in, int nvec,
+                                            int v0, int stride) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        first[i] = make_uint4(0, 0, 0, 0);
+        if (a.dx_in != nullptr && v0 + i * stride < nvec) first[i] = ld_inout_v4(in + v0 + i * stride);
     }
-    __syncthreads();
-    const int n = s_n;
+}
+
+// Adds the vectors tid, tid + stride, ... (kVec at a time) of a token's n rows, kRows rows at
+// a time in flight, in slot order, the addend first.
+template <int kVec, int kRows>
+__device__ __forceinline__ void add_rows(const DispatchBwdArgs& a, const long long* rows, int n, const uint4* in,
+                                         uint4* out, int nvec, uint4 (&first)[kVec], int tid, int stride) {
     const uint4* src = reinterpret_cast<const uint4*>(a.dperm_x);
-    const uint4* in = reinterpret_cast<const uint4*>(a.dx_in) + static_cast<size_t>(t) * nvec;
-    uint4* dx = reinterpret_cast<uint4*>(a.dx) + static_cast<size_t>(t) * nvec;
-    for (int v = tid; v < nvec; v += static_cast<int>(blockDim.x)) {
-        uint4 first = make_uint4(0, 0, 0, 0);
-        if (a.dx_in != nullptr) first = ld_inout_v4(in + v);
-        float acc[8];
-        unpack8(acc, first);
-        for (int d0 = 0; d0 < n; d0 += kBatch) {
-            uint4 buf[kBatch];
+    for (int v0 = tid; v0 < nvec; v0 += kVec * stride) {
+        if (v0 != tid) load_addend<kVec>(a, first, in, nvec, v0, stride);
+        float acc[kVec][8];
+        for (int d0 = 0; d0 == 0 || d0 < n; d0 += kRows) {
+            uint4 buf[kRows][kVec];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (d0 + i < n) buf[i] = ld_stream_v4(src + s_row[d0 + i] + v);
+            for (int r = 0; r < kRows; ++r)
+                if (d0 + r < n) {
+                    const uint4* row = src + rows[d0 + r] + v0;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (d0 + i >= n) continue;
-                float f[8];
-                unpack8(f, buf[i]);
+                    for (int i = 0; i < kVec; ++i)
+                        if (v0 + i * stride < nvec) buf[r][i] = ld_stream_v4(row + i * stride);
+                }
+            if (d0 == 0) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] += f[e];
+                for (int i = 0; i < kVec; ++i) unpack8(acc[i], first[i]);
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (d0 + r >= n) continue;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    float f[8];
+                    unpack8(f, buf[r][i]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[i][e] += f[e];
+                }
             }
         }
-        st_v4(dx + v, pack8(acc));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (v0 + i * stride < nvec) st_v4(out + v0 + i * stride, pack8(acc[i]));
+    }
+}
+
+// A token per CTA, or per warp where rows are short (per_warp): the first warp, or the token's,
+// lists the token's rows, then every thread adds its vectors of them. kVec and kRows follow
+// from k, so that about eight vectors are in flight per thread however few rows a token has
+// (2170 x 4752 top-2: 15.4 us instead of 20 us with one vector at a time). CTAs of 64 threads:
+// 16384 x 4096 top-8 with the addend in 202 us (6.67 TB/s, 0.98 of a measured copy), 207 us
+// with 256 threads and 238 us with 512, which wait longer for their lists; a warp per row up
+// to 2048 channels (8000 x 1024 top-6: 22.6 us instead of 24.9 us), not above (16384 x 4096:
+// 217 us). At most a token per SM: as many threads as there are vectors, up to 512.
+template <int kVec, int kRows>
+__global__ void __maxnreg__((kVec == 1 ? 64 : 72)) dispatch_bwd_kernel(DispatchBwdArgs a, int per_warp) {
+    grid_dependency_wait();
+    __shared__ long long s_row[kSortWarps][kMaxTopk];
+    __shared__ int s_n[kSortWarps];
+    const int lane = lane_id();
+    const int warp = static_cast<int>(threadIdx.x >> 5);
+    const int nvec = a.H / 8;
+    const int t = per_warp ? static_cast<int>(blockIdx.x * (blockDim.x >> 5)) + warp : static_cast<int>(blockIdx.x);
+    const int mine = per_warp ? warp : 0;
+    const uint4* const in = reinterpret_cast<const uint4*>(a.dx_in) + static_cast<size_t>(t) * nvec;
+    const int first_v = per_warp ? lane : static_cast<int>(threadIdx.x);
+    const int stride = per_warp ? 32 : static_cast<int>(blockDim.x);
+    uint4 first[kVec];  // the addend's first vectors, requested before the token's rows are known
+    load_addend<kVec>(a, first, in, t < a.T ? nvec : 0, first_v, stride);
+    float dw = 0.0f;
+    if (t < a.T && (per_warp || warp == 0)) {
+        const size_t entry = static_cast<size_t>(t) * a.k + lane;
+        long long row = -1;
+        if (lane < a.k) {
+            row = entry_row(a.topk_idx, a.offsets, a.eslot, entry, a.E, a.E / a.R, a.max_rows);
+            if (a.dtopk_w != nullptr && row >= 0) dw = __ldg(a.dperm_w + row);  // stored after the rows
+        }
+        const uint32_t m = __ballot_sync(kFullMask, row >= 0);
+        if (row >= 0) s_row[mine][__popc(m & lanemask_lt())] = row * nvec;
+        if (__any_sync(kFullMask, row == -2) && lane == 0) raise_flag(a.status, EP_FLAG_CAPACITY);
+        if (lane == 0) s_n[mine] = __popc(m);
+        __syncwarp();
+    }
+    if (!per_warp) __syncthreads();
+    if (t < a.T) {
+        add_rows<kVec, kRows>(a, s_row[mine], s_n[mine], in, reinterpret_cast<uint4*>(a.dx) + static_cast<size_t>(t) * nvec,
+                              nvec, first, first_v, stride);
+        if ((per_warp || warp == 0) && lane < a.k && a.dtopk_w != nullptr)
+            a.dtopk_w[static_cast<size_t>(t) * a.k + lane] = dw;
     }
     allow_dependents();
 }
@@ -223,8 +303,19 @@ extern "C" ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, 
     const CombineBwdArgs a{static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y), topk_idx, topk_w,
                            expert_offsets, expert_slot, T, H, k, E, R, max_rows, static_cast<uint16_t*>(dy), dtopk_w,
                            status};
-    return launch_dependent(combine_bwd_kernel, dim3(static_cast<unsigned>(T)), dim3(32 * (k < kWarps ? k : kWarps)),
-                            0, as_stream(stream), a);
+    const long long entries = static_cast<long long>(T) * k;
+    // few entries (an SM holds 4 CTAs): more warps on each row
+    const bool few = entries <= static_cast<long long>(sm_count()) * (4 * kWarps / kSmallSplit);
+    // otherwise a warp per entry and CTAs of a token's entries, or an even part of them
+    const int parts = (k + kWarps - 1) / kWarps;
+    const int warps = few ? kWarps : (k + parts - 1) / parts;
+    // many short rows: two rounds a CTA
+    const bool rounds = H <= kShortRowH && entries >= static_cast<long long>(sm_count()) * (4 * 4 * kWarps);
+    const int count = few ? kWarps / kSmallSplit : warps * (rounds ? 2 : 1);
+    const long long grid = (entries + count - 1) / count;
+    if (grid > 0x7fffffffLL) return EP_ERR_INVALID;
+    return launch_dependent(few ? combine_bwd_kernel<kSmallSplit> : combine_bwd_kernel<1>,
+                            dim3(static_cast<unsigned>(grid)), dim3(32 * warps), 0, as_stream(stream), a, count);
 }
 
 extern "C" ep_status_t ep_dispatch_permuted_bwd(const void* dperm_x, const float* dperm_w, const void* dx_in,
@@ -244,7 +335,13 @@ extern "C" ep_status_t ep_dispatch_permuted_bwd(const void* dperm_x, const float
     const DispatchBwdArgs a{static_cast<const uint16_t*>(dperm_x), dperm_w, static_cast<const uint16_t*>(dx_in),
                             topk_idx, expert_offsets, expert_slot, T, H, k, E, R, max_rows,
                             static_cast<uint16_t*>(dx), dtopk_w, status};
-    const int threads = H / 8 < kSortThreads ? (H / 8 + 31) / 32 * 32 : kSortThreads;
-    return launch_dependent(dispatch_bwd_kernel, dim3(static_cast<unsigned>(T)), dim3(threads), 0, as_stream(stream),
-                            a);
+    auto kernel = k == 1 ? dispatch_bwd_kernel<4, 1> : k <= 4 ? dispatch_bwd_kernel<2, 4> : dispatch_bwd_kernel<1, 8>;
+    const int vec = k == 1 ? 4 : k <= 4 ? 2 : 1;
+    if (H <= kWarpRowH && T > sm_count())
+        return launch_dependent(kernel, dim3(static_cast<unsigned>(T / 4 + (T % 4 != 0))), dim3(128), 0,
+                                as_stream(stream), a, 1);
+    const int most = T <= sm_count() ? 32 * kSortWarps : kSortThreads;
+    const int threads = (H / 8 + 32 * vec - 1) / (32 * vec) * 32;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(T)), dim3(threads < most ? threads : most), 0,
+                            as_stream(stream), a, 0);
 }

@@ -68,7 +68,10 @@ def rand_bf16(shape, seed, scale=1.0):
 CASES = [dict(T=1, H=128, E=4, k=2, R=2), dict(T=128, H=1024, E=16, k=4, R=4, bad=True),
          dict(T=77, H=640, E=24, k=5, R=8, empty=0.3), dict(T=300, H=7168, E=64, k=8, R=16),
          dict(T=200, H=384, E=32, k=6, R=4, max_rows=100, bad=True), dict(T=65, H=256, E=64, k=32, R=1),
-         dict(T=33, H=256, E=8, k=1, R=8, max_rows=0), dict(T=50, H=128, E=4, k=3, R=1, empty=1.0)]
+         dict(T=33, H=256, E=8, k=1, R=8, max_rows=0), dict(T=50, H=128, E=4, k=3, R=1, empty=1.0),
+         dict(T=1024, H=128, E=16, k=8, R=4, bad=True), dict(T=256, H=128, E=1024, k=32, R=8, bad=True),
+         dict(T=910, H=256, E=40, k=9, R=8, empty=0.2), dict(T=481, H=1152, E=32, k=17, R=2, bad=True),
+         dict(T=1024, H=16384, E=8, k=1, R=8), dict(T=3, H=16512, E=8, k=2, R=2)]
 
 
 # --------------------------------------------------------------------------- E4M3 sort
