@@ -1,4 +1,5 @@
-"""ctypes binding of libep_gb300.so (include/ep.h): argument marshalling only.
+"""Binding of libep_gb300.so (include/ep.h) by ctypes and, for its shortest calls, by the
+compiled module of csrc/ep_binding.cpp: argument marshalling only.
 
 Every function takes torch tensors, checks their device, dtype, shape and
 contiguity, passes raw device pointers and the current (or given) CUDA stream
@@ -9,12 +10,14 @@ no CPU path. If the library has not been built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 import torch
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 EP_OK = 0
 EP_ERR_INVALID = 1
@@ -440,144 +443,79 @@ def ep_combine_send(y_perm, recv_src_idx, recv_topk_idx, recv_topk_w, tokens_per
     _done("ep_combine_send", rc)
 
 
-# --------------------------------------------------------------------------- E4M3 rows and gradients
+# --------------------------------------------------------------------------- E4M3 rows, gradients, norm
+# Checks of arguments and calls in csrc/ep_binding.cpp: these are the calls whose GPU work is
+# shorter than their checks would be here. They refuse what _check refuses, in its words.
 
-_CODES = (torch.uint8, torch.float8_e4m3fn)  # E4M3 codes, as bytes or as torch's own type
+_binding = None
 
 
-def _check_codes(name, t, shape):
-    _check(name, t, t.dtype if t is not None and t.dtype in _CODES else torch.uint8, shape)
+def _native():
+    """The compiled binding, with the library's entry points; raises if either has not been built."""
+    global _binding
+    if _binding is None:
+        L = lib()
+        with _lock:
+            if _binding is None:
+                if not os.path.exists(BINDING_PATH):
+                    raise RuntimeError(
+                        f"{BINDING_PATH} is missing: build it first "
+                        "(python -m combine_ep_get_05_gb300.build or __graft_entry__.build())")
+                loader = importlib.machinery.ExtensionFileLoader("_ep_binding", BINDING_PATH)
+                spec = importlib.util.spec_from_file_location("_ep_binding", BINDING_PATH, loader=loader)
+                module = importlib.util.module_from_spec(spec)
+                loader.exec_module(module)
+                module.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+                    "ep_rmsnorm", "ep_rmsnorm_bwd", "ep_dispatch_permuted_fp8", "ep_dispatch_permuted_fp8_ll",
+                    "ep_dispatch_permuted_bwd", "ep_combine_permuted_bwd")})
+                _binding = module
+    return _binding
 
 
 def ep_dispatch_permuted_fp8(x_q, x_scales, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, num_ranks,
                              max_rows, perm_q, perm_scales, perm_src=None, perm_w=None, status=None, stream=None):
     """ep_dispatch_permuted for E4M3 rows: codes [T][H] (uint8 or float8_e4m3fn) and scales [T][H/128]."""
-    T, H = x_q.shape
-    k = topk_idx.shape[1]
-    E, R = num_experts, num_ranks
-    _check_codes("x_q", x_q, (T, H))
-    _check("x_scales", x_scales, torch.float32, (T, H // 128))
-    _check("topk_idx", topk_idx, torch.int64, (T, k))
-    _check("topk_w", topk_w, torch.float32, (T, k), optional=True)
-    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
-    _check("expert_slot", expert_slot, torch.int32, (T, k))
-    _check_codes("perm_q", perm_q, (R, max_rows, H))
-    _check("perm_scales", perm_scales, torch.float32, (R, max_rows, H // 128))
-    _check("perm_src", perm_src, torch.int32, (R, max_rows), optional=True)
-    _check("perm_w", perm_w, torch.float32, (R, max_rows), optional=True)
-    _check("status", status, torch.int32, (1,), optional=True)
-    rc = lib().ep_dispatch_permuted_fp8(x_q.data_ptr(), x_scales.data_ptr(), topk_idx.data_ptr(), _ptr(topk_w),
-                                        expert_offsets.data_ptr(), expert_slot.data_ptr(), T, H, k, E, R, max_rows,
-                                        perm_q.data_ptr(), perm_scales.data_ptr(), _ptr(perm_src), _ptr(perm_w),
-                                        _ptr(status), _stream(stream))
-    _done("ep_dispatch_permuted_fp8", rc)
+    rc = (_binding or _native()).dispatch_permuted_fp8(
+        x_q, x_scales, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, num_ranks, max_rows, perm_q,
+        perm_scales, perm_src, perm_w, status, stream)
+    if rc != EP_OK:
+        _done("ep_dispatch_permuted_fp8", rc)
 
 
 def ep_dispatch_permuted_fp8_ll(x_q, x_scales, topk_idx, topk_w, num_experts, num_ranks, max_rows, expert_offsets,
                                 expert_slot, perm_q, perm_scales, perm_src=None, perm_w=None, status=None, stream=None):
     """ep_dispatch_permuted_fp8 for a decode-sized batch (T <= 1024), expert layout included, in one launch."""
-    T, H = x_q.shape
-    k = topk_idx.shape[1]
-    E, R = num_experts, num_ranks
-    _check_codes("x_q", x_q, (T, H))
-    _check("x_scales", x_scales, torch.float32, (T, H // 128))
-    _check("topk_idx", topk_idx, torch.int64, (T, k))
-    _check("topk_w", topk_w, torch.float32, (T, k), optional=True)
-    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
-    _check("expert_slot", expert_slot, torch.int32, (T, k))
-    _check_codes("perm_q", perm_q, (R, max_rows, H))
-    _check("perm_scales", perm_scales, torch.float32, (R, max_rows, H // 128))
-    _check("perm_src", perm_src, torch.int32, (R, max_rows), optional=True)
-    _check("perm_w", perm_w, torch.float32, (R, max_rows), optional=True)
-    _check("status", status, torch.int32, (1,), optional=True)
-    rc = lib().ep_dispatch_permuted_fp8_ll(x_q.data_ptr(), x_scales.data_ptr(), topk_idx.data_ptr(), _ptr(topk_w), T,
-                                           H, k, E, R, max_rows, expert_offsets.data_ptr(), expert_slot.data_ptr(),
-                                           perm_q.data_ptr(), perm_scales.data_ptr(), _ptr(perm_src), _ptr(perm_w),
-                                           _ptr(status), _stream(stream))
-    _done("ep_dispatch_permuted_fp8_ll", rc)
+    rc = (_binding or _native()).dispatch_permuted_fp8_ll(
+        x_q, x_scales, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, num_ranks, max_rows, perm_q,
+        perm_scales, perm_src, perm_w, status, stream)
+    if rc != EP_OK:
+        _done("ep_dispatch_permuted_fp8_ll", rc)
 
 
 def ep_dispatch_permuted_bwd(dperm_x, dperm_w, dx_in, topk_idx, expert_offsets, expert_slot, num_experts, dx,
                              dtopk_w=None, status=None, stream=None):
     """Gradient of ep_dispatch_permuted: dx = dx_in + the token's rows of dperm_x, dtopk_w from dperm_w."""
-    R, max_rows, H = dperm_x.shape
-    T, k = topk_idx.shape
-    E = num_experts
-    _check("dperm_x", dperm_x, torch.bfloat16)
-    _check("dperm_w", dperm_w, torch.float32, (R, max_rows), optional=dtopk_w is None)
-    _check("dx_in", dx_in, torch.bfloat16, (T, H), optional=True)
-    _check("topk_idx", topk_idx, torch.int64)
-    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
-    _check("expert_slot", expert_slot, torch.int32, (T, k))
-    _check("dx", dx, torch.bfloat16, (T, H))
-    _check("dtopk_w", dtopk_w, torch.float32, (T, k), optional=True)
-    _check("status", status, torch.int32, (1,), optional=True)
-    rc = lib().ep_dispatch_permuted_bwd(dperm_x.data_ptr(), _ptr(dperm_w), _ptr(dx_in), topk_idx.data_ptr(),
-                                        expert_offsets.data_ptr(), expert_slot.data_ptr(), T, H, k, E, R, max_rows,
-                                        _ptr(dx), _ptr(dtopk_w), _ptr(status), _stream(stream))
-    _done("ep_dispatch_permuted_bwd", rc)
+    rc = (_binding or _native()).dispatch_permuted_bwd(dperm_x, dperm_w, dx_in, topk_idx, expert_offsets, expert_slot,
+                                                       num_experts, dx, dtopk_w, status, stream)
+    if rc != EP_OK:
+        _done("ep_dispatch_permuted_bwd", rc)
 
 
 def ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, dy, dtopk_w=None,
                             status=None, stream=None):
     """Gradient of ep_combine_permuted: dy's rows = w * dout, dtopk_w = <dout, y's row>; y is read for dtopk_w only."""
-    R, max_rows, H = dy.shape
-    T, k = topk_idx.shape
-    E = num_experts
-    _check("dout", dout, torch.bfloat16, (T, H))
-    _check("y", y, torch.bfloat16, (R, max_rows, H), optional=dtopk_w is None)
-    _check("topk_idx", topk_idx, torch.int64)
-    _check("topk_w", topk_w, torch.float32, (T, k), optional=True)
-    _check("expert_offsets", expert_offsets, torch.int32, (E + 1,))
-    _check("expert_slot", expert_slot, torch.int32, (T, k))
-    _check("dy", dy, torch.bfloat16)
-    _check("dtopk_w", dtopk_w, torch.float32, (T, k), optional=True)
-    _check("status", status, torch.int32, (1,), optional=True)
-    rc = lib().ep_combine_permuted_bwd(dout.data_ptr(), _ptr(y), topk_idx.data_ptr(), _ptr(topk_w),
-                                       expert_offsets.data_ptr(), expert_slot.data_ptr(), T, H, k, E, R, max_rows,
-                                       dy.data_ptr(), _ptr(dtopk_w), _ptr(status), _stream(stream))
-    _done("ep_combine_permuted_bwd", rc)
-
-
-# --------------------------------------------------------------------------- norm
-
-_STREAM_TYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
-
-
-def _stream_dtype(t):
-    """The residual stream's type, that of `t`; bf16 where there is no stream."""
-    dtype = torch.bfloat16 if t is None else t.dtype
-    if dtype not in _STREAM_TYPES:
-        raise ValueError(f"the residual stream must be bfloat16 or float32, got {dtype}")
-    return dtype
-
-
-def _check_weight(weight, H):
-    _check("weight", weight, torch.float32 if weight is not None and weight.dtype == torch.float32 else torch.bfloat16,
-           (H,))
-    return _STREAM_TYPES[weight.dtype]
+    rc = (_binding or _native()).combine_permuted_bwd(dout, y, topk_idx, topk_w, expert_offsets, expert_slot,
+                                                      num_experts, dy, dtopk_w, status, stream)
+    if rc != EP_OK:
+        _done("ep_combine_permuted_bwd", rc)
 
 
 def ep_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, y_q=None, y_scales=None, stream=None):
     """z = x + residual; residual_out = z; y (bf16) and y_q / y_scales (E4M3, 1x128) = z / rms(z) * weight.
     x or residual may be None; every output may be None, y_q and y_scales together."""
-    if x is None and residual is None:
-        raise ValueError("x or residual is required")
-    T, H = (x if x is not None else residual).shape
-    dtype = _stream_dtype(residual if residual is not None else residual_out)
-    if residual_out is not None and residual_out.dtype is not dtype:
-        raise ValueError(f"the residual stream must be of one type, got {dtype} and {residual_out.dtype}")
-    _check("x", x, torch.bfloat16, (T, H), optional=True)
-    _check("residual", residual, dtype, (T, H), optional=True)
-    wtype = _check_weight(weight, H)
-    _check("residual_out", residual_out, dtype, (T, H), optional=True)
-    _check("y", y, torch.bfloat16, (T, H), optional=True)
-    if y_q is not None:
-        _check_codes("y_q", y_q, (T, H))
-    _check("y_scales", y_scales, torch.float32, (T, H // 128), optional=y_q is None)
-    rc = lib().ep_rmsnorm(_ptr(x), _ptr(residual), weight.data_ptr(), _STREAM_TYPES[dtype], wtype, eps, T, H,
-                          _ptr(residual_out), _ptr(y), _ptr(y_q), _ptr(y_scales), _stream(stream))
-    _done("ep_rmsnorm", rc)
+    rc = (_binding or _native()).rmsnorm(x, residual, weight, eps, residual_out, y, y_q, y_scales, stream)
+    if rc != EP_OK:
+        _done("ep_rmsnorm", rc)
 
 
 def ep_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
@@ -586,17 +524,6 @@ def ep_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
 
 def ep_rmsnorm_bwd(dy, z, weight, dz_in, eps, dz, dx=None, dweight=None, workspace=None, stream=None):
     """Gradient of ep_rmsnorm at z (its residual_out): dz = dz_in + d/dz, dx the same in bf16, dweight fp32."""
-    T, H = z.shape
-    dtype = _stream_dtype(z)
-    _check("dy", dy, torch.bfloat16, (T, H))
-    _check("z", z, dtype)
-    wtype = _check_weight(weight, H)
-    _check("dz_in", dz_in, dtype, (T, H), optional=True)
-    _check("dz", dz, dtype, (T, H))
-    _check("dx", dx, torch.bfloat16, (T, H), optional=True)
-    _check("dweight", dweight, torch.float32, (H,), optional=True)
-    _check("workspace", workspace, torch.uint8, optional=dweight is None)
-    rc = lib().ep_rmsnorm_bwd(dy.data_ptr(), z.data_ptr(), weight.data_ptr(), _ptr(dz_in), _STREAM_TYPES[dtype],
-                              wtype, eps, T, H, dz.data_ptr(), _ptr(dx), _ptr(dweight), _ptr(workspace),
-                              workspace.numel() if workspace is not None else 0, _stream(stream))
-    _done("ep_rmsnorm_bwd", rc)
+    rc = (_binding or _native()).rmsnorm_bwd(dy, z, weight, dz_in, eps, dz, dx, dweight, workspace, stream)
+    if rc != EP_OK:
+        _done("ep_rmsnorm_bwd", rc)

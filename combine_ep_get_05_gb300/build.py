@@ -3,6 +3,9 @@
 Each translation unit is compiled in parallel (``nvcc -c``), then the objects
 are linked into one shared library with the C ABI of ``include/ep.h``. The
 CUDA runtime is linked statically, so the library needs only the driver.
+
+Beside it, csrc/ep_binding.cpp becomes the Python module _ep_binding, compiled
+by the host compiler against the installed torch.
 """
 from __future__ import annotations
 
@@ -10,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libep_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "ep_binding.cpp")
+BINDING_PATH = os.path.join(BUILD_DIR, "_ep_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -37,19 +43,51 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "ep.h")]
+def _older(target, inputs) -> bool:
+    if not os.path.exists(target):
+        return True
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(p) > t for p in inputs)
+
+
+def _library_is_stale() -> bool:
+    return _older(LIB_PATH, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "ep.h")])
+
+
+def _binding_is_stale() -> bool:
+    return _older(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "ep.h")])
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    return _library_is_stale() or _binding_is_stale()
+
+
+def host_compiler() -> str:
+    found = shutil.which("g++") or shutil.which("c++")
+    if not found:
+        raise RuntimeError("g++ not found: a host C++ compiler is needed to build _ep_binding.so")
+    return found
+
+
+def _build_binding() -> None:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    cmd = [host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp,
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"{host_compiler()} failed on {BINDING_SRC}:\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, ptxas_info: bool = False, jobs: int | None = None) -> str:
-    """Compile and link the library if any input changed (or force). Returns its path."""
+    """Compile and link the library and the binding if any input changed (or force). Returns the library's path."""
     if not (force or ptxas_info or is_stale()):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -64,7 +102,12 @@ def build(force: bool = False, ptxas_info: bool = False, jobs: int | None = None
         return obj, proc.stderr
 
     with ThreadPoolExecutor(max_workers=jobs or min(8, os.cpu_count() or 1)) as pool:
-        results = list(pool.map(compile_one, sources()))
+        binding = pool.submit(_build_binding) if force or _binding_is_stale() else None
+        results = list(pool.map(compile_one, sources())) if force or ptxas_info or _library_is_stale() else []
+        if binding is not None:
+            binding.result()
+    if not results:
+        return LIB_PATH
     if ptxas_info:
         with open(os.path.join(BUILD_DIR, "ptxas.txt"), "w") as f:
             for obj, log in results:

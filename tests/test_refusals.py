@@ -12,7 +12,7 @@ F = P(4096)      # a 16-byte aligned address
 ODD = P(4096 + 4)
 
 
-@pytest.fixture(scope="module")
+@pytest.fixture(scope="module", autouse=True)
 def L():
     from combine_ep_get_05_gb300 import _lib, build
 
