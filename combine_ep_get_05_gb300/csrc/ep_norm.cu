@@ -26,11 +26,12 @@ constexpr int kBlock = 128;         // channels per E4M3 scale
 constexpr int kMaxThreads = 1024;
 constexpr size_t kMaxRingSmem = 200 * 1024;
 // Rows that move fewer bytes than this, in and out, take the ring whatever they hold: a GPU
-// starts about one CTA a nanosecond, in which HBM moves 7 KB (16384 x 264: 8.1 us against
+// starts about one CTA a nanosecond, in which HBM moves 7 KB (16384 x 264: 5.7 us against
 // 16.9 us; 16384 x 1024, 8 KB a row: 22.1 us against 21.1 us).
 constexpr int kRingRowBytes = 6144;
 constexpr int kMaxParts = 512;      // rows of dweight partial sums
 constexpr int kBwdThreads = 448;    // threads of a gradient CTA: as many rows side by side as fit
+constexpr int kRingRows = 8;        // rows of a ring CTA where one warp holds a row
 constexpr int kMaxGroups = 15;      // rows side by side: a named barrier each
 constexpr int kReduceRows = 32;     // partial sums a dweight reduction CTA adds at a time
 
@@ -351,8 +352,8 @@ __device__ __forceinline__ float block_sum(float v, int nt, float* s_part) {
 // i of lane l being number i * 32 + l of them, so that a warp's accesses are whole lines and
 // all of a thread's vectors are at fixed distances from its first.
 template <class Carry, int kVecs>
-__device__ __forceinline__ int first_channel() {
-    return ((static_cast<int>(threadIdx.x) >> 5) * (kVecs * 32) + lane_id()) * Carry::kElems;
+__device__ __forceinline__ int first_channel(int thread) {
+    return ((thread >> 5) * (kVecs * 32) + (thread & 31)) * Carry::kElems;
 }
 
 // The row's outputs from its z (zero past the row's end) and reciprocal root mean square;
@@ -388,15 +389,15 @@ __device__ __forceinline__ void write_row(const NormArgs& a, size_t at, int h0, 
 
 // One CTA per row; the row stays in registers between the sum of squares and the outputs.
 // 4 vectors a thread at 72 registers keep four 7168-channel rows in flight on an SM; with 64 or
-// 80 registers, or 2 vectors a thread, 4096 x 7168 takes 41 to 44 us instead of 40.5. For at
-// most one row per SM every vector has a thread of its own (one row of 7168: 2.2 us).
+// 80 registers, or 2 vectors a thread, 4096 x 7168 takes 41 to 44 us instead of 40.5. One row
+// of 7168 takes 2.0 us (2.1 us with a thread for every vector), 128 rows of an fp32 stream 2.4 us.
 template <class Carry, int kVecs, bool kFp8, bool kWF32>
 __global__ void __maxnreg__((Carry::kElems == 8 && kVecs == 4 ? 72 : 64)) rmsnorm_kernel(NormArgs a) {
     constexpr int N = Carry::kElems, P = N / 2;
     __shared__ float s_part[32];
     grid_dependency_wait();  // dependent launch: inputs are ready after this
     allow_dependents();
-    const int h0 = first_channel<Carry, kVecs>();
+    const int h0 = first_channel<Carry, kVecs>(static_cast<int>(threadIdx.x));
     const size_t at = static_cast<size_t>(blockIdx.x) * a.H + h0;
     const char* const res = static_cast<const char*>(a.residual) + carry_bytes<Carry>(at);
     uint32_t xw[kVecs][P], rw[kVecs][4];
@@ -450,16 +451,20 @@ __device__ __forceinline__ void fill_ring(unsigned char* at, int stage_bytes, in
 // barrier guards the ring: a thread reads only what it copied itself. A missing input's
 // places hold -0 and those past the row's end 0, so the arithmetic has no cases. The weights
 // stay in registers over all rows.
-template <class Carry, int kVecs, int kStages, bool kFp8, bool kWF32>
+// A row that one warp holds (kMany) needs no barrier, and its CTA has kRingRows of them.
+template <class Carry, int kVecs, int kStages, bool kFp8, bool kWF32, bool kMany>
 __global__ void __maxnreg__(64) rmsnorm_ring_kernel(NormArgs a, int T) {
     constexpr int N = Carry::kElems, P = N / 2;
-    extern __shared__ __align__(16) unsigned char s_ring[];
+    extern __shared__ __align__(16) unsigned char s_all[];
     __shared__ float s_part[2][32];
-    const int nt = static_cast<int>(blockDim.x);
-    const int h0 = first_channel<Carry, kVecs>();
+    const int nt = kMany ? 32 : static_cast<int>(blockDim.x);  // threads of a row
+    const int rows = kMany ? kRingRows : 1;                   // of the CTA
+    const int group = kMany ? static_cast<int>(threadIdx.x) >> 5 : 0;
+    const int h0 = first_channel<Carry, kVecs>(kMany ? lane_id() : static_cast<int>(threadIdx.x));
     const bool has_x = a.x != nullptr, has_r = a.residual != nullptr;
     const int r_bytes = kVecs * nt * 16;  // of a stage
     const int stage_bytes = r_bytes + kVecs * nt * 2 * N;
+    unsigned char* const s_ring = s_all + group * (kStages * stage_bytes);
     unsigned char* const r_ring = s_ring + h0 * (16 / N);
     unsigned char* const x_ring = s_ring + r_bytes + h0 * 2;
     const int vectors_in = h0 < a.H ? (a.H - h0 + 32 * N - 1) / (32 * N) : 0;
@@ -489,13 +494,14 @@ __global__ void __maxnreg__(64) rmsnorm_ring_kernel(NormArgs a, int T) {
         }
         cp_async_commit();  // an empty group past the end keeps the waits uniform
     };
-    const uint32_t step = gridDim.x;  // T < 2^31: row numbers past the end stay below 2^32
+    const uint32_t first = blockIdx.x * rows + group;
+    const uint32_t step = gridDim.x * rows;  // T < 2^31: row numbers past the end stay below 2^32
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(blockIdx.x + s * step, s);
+    for (int s = 0; s < kStages - 1; ++s) issue(first + s * step, s);
     uint32_t w[kVecs][kWeightWords<kWF32, P>];
     load_weights<kWF32, P>(w, a.weight, h0, a.H);
     int st = 0, parity = 0;
-    for (uint32_t t = blockIdx.x; t < static_cast<uint32_t>(T); t += step, parity ^= 1) {
+    for (uint32_t t = first; t < static_cast<uint32_t>(T); t += step, parity ^= 1) {
         issue(t + (kStages - 1) * step, st == 0 ? kStages - 1 : st - 1);  // the stage read last time
         cp_async_wait<kStages - 1>();
         const size_t at = static_cast<size_t>(t) * a.H + h0;
@@ -546,17 +552,19 @@ ep_status_t resident(Residency& cache, Kernel* kernel, int nt, int kind, size_t 
     return EP_OK;
 }
 
-template <class Carry, int kVecs, int kStages, bool kFp8, bool kWF32>
+template <class Carry, int kVecs, int kStages, bool kFp8, bool kWF32, bool kMany>
 ep_status_t launch_norm_ring(const NormArgs& a, int T, cudaStream_t stream) {
     static Residency cache;
-    const int nt = row_threads(a.H / Carry::kElems, kVecs);
-    auto kernel = rmsnorm_ring_kernel<Carry, kVecs, kStages, kFp8, kWF32>;
-    const size_t smem = kStages * ring_row_bytes<Carry>(nt, kVecs, 1);
+    const int rows = kMany ? kRingRows : 1;
+    const int threads = rows * row_threads(a.H / Carry::kElems, kVecs);
+    auto kernel = rmsnorm_ring_kernel<Carry, kVecs, kStages, kFp8, kWF32, kMany>;
+    const size_t smem = kStages * ring_row_bytes<Carry>(threads, kVecs, 1);
     int per_sm = 1;
-    const ep_status_t st = resident(cache, kernel, nt, 0, smem, &per_sm);
+    const ep_status_t st = resident(cache, kernel, threads, 0, smem, &per_sm);
     if (st != EP_OK) return st;
     const int cap = sm_count() * per_sm;
-    return launch_dependent(kernel, dim3(T < cap ? T : cap), dim3(nt), smem, stream, a, T);
+    const int ctas = (T - 1) / rows + 1;
+    return launch_dependent(kernel, dim3(ctas < cap ? ctas : cap), dim3(threads), smem, stream, a, T);
 }
 
 template <class Carry, int kVecs, bool kFp8, bool kWF32>
@@ -568,25 +576,26 @@ ep_status_t launch_norm_rows(const NormArgs& a, int T, cudaStream_t stream) {
 template <class Carry, bool kFp8, bool kWF32>
 ep_status_t launch_norm(const NormArgs& a, int T, cudaStream_t stream) {
     const int vecs = a.H / Carry::kElems;
-    // a row per SM at most: as many threads on a row as it has vectors
-    if (T <= sm_count() && vecs <= kMaxThreads) return launch_norm_rows<Carry, 1, kFp8, kWF32>(a, T, stream);
     const int streams = (a.residual != nullptr) + (a.residual_out != nullptr);
     const int row_bytes = a.H * (streams * (16 / Carry::kElems) + (a.x != nullptr ? 2 : 0) + (a.y != nullptr ? 2 : 0) +
                                  (kFp8 ? 1 : 0));
     if (T > sm_count() && (row_bytes < kRingRowBytes || a.x == nullptr || a.residual == nullptr)) {
         if constexpr (Carry::kElems == 4) {  // 4 channels a vector: 1024 threads of 2 vectors cover 8192
-            if (row_threads(vecs, 2) > kMaxThreads) return launch_norm_ring<Carry, 4, 2, kFp8, kWF32>(a, T, stream);
+            if (row_threads(vecs, 2) > kMaxThreads)
+                return launch_norm_ring<Carry, 4, 2, kFp8, kWF32, false>(a, T, stream);
         }
-        return launch_norm_ring<Carry, 2, 2, kFp8, kWF32>(a, T, stream);
+        if (row_threads(vecs, 2) == 32) return launch_norm_ring<Carry, 2, 2, kFp8, kWF32, true>(a, T, stream);
+        return launch_norm_ring<Carry, 2, 2, kFp8, kWF32, false>(a, T, stream);
     }
     return launch_norm_rows<Carry, 4, kFp8, kWF32>(a, T, stream);
 }
 
 template <class Carry>
 ep_status_t launch_norm(const NormArgs& a, int T, cudaStream_t stream) {
-    auto launch = a.y_q != nullptr ? (a.weight_f32 ? launch_norm<Carry, true, true> : launch_norm<Carry, true, false>)
-                                   : (a.weight_f32 ? launch_norm<Carry, false, true> : launch_norm<Carry, false, false>);
-    return launch(a, T, stream);
+    const bool f32 = a.weight_f32 != 0;
+    if (a.y_q != nullptr)
+        return f32 ? launch_norm<Carry, true, true>(a, T, stream) : launch_norm<Carry, true, false>(a, T, stream);
+    return f32 ? launch_norm<Carry, false, true>(a, T, stream) : launch_norm<Carry, false, false>(a, T, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -622,7 +631,7 @@ __global__ void __maxnreg__((kMany ? 72 : 64)) rmsnorm_bwd_kernel(NormBwdArgs a,
     const int nt = static_cast<int>(blockDim.x) / groups;  // threads of a row
     const int group = kMany ? static_cast<int>(threadIdx.x) / nt : 0;
     const int tid = static_cast<int>(threadIdx.x) - group * nt;
-    const int h0 = ((tid >> 5) * (kVecs * 32) + lane_id()) * N;
+    const int h0 = first_channel<Carry, kVecs>(tid);
     const bool has_in = a.dz_in != nullptr;
     const int z_bytes = kVecs * nt * 16;  // of a stage
     const int in_bytes = has_in ? z_bytes : 0;

@@ -361,28 +361,46 @@ struct PermFp8Scatter {
 // of 12.0 us, 16000 x 1024 27.2 us instead of 27.7 us; 8000 x 2048: 26.8 us against 25.9 us).
 constexpr int kWarpFp8Vecs = 2;
 
+// Where tokens are few, a CTA takes one (kAlone) and its threads the row's vectors.
+template <bool kAlone>
 __global__ void __launch_bounds__(kThreads) dispatch_permuted_fp8_kernel(PermFp8Scatter a) {
     __shared__ long long s_row[kWarps][kMaxTopk];
     __shared__ int s_j[kWarps][kMaxTopk];
+    __shared__ int s_nd;
     grid_dependency_wait();
-    const int lane = lane_id();
     const int warp = static_cast<int>(threadIdx.x >> 5);
     const int nvec = static_cast<int>(a.row_bytes / 16);
-    const int t = static_cast<int>(blockIdx.x) * kWarps + warp;
+    const int t = kAlone ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kWarps + warp;
+    const int first = kAlone ? static_cast<int>(threadIdx.x) : lane_id();
+    constexpr int kStride = kAlone ? kThreads : 32;
+    const int mine = kAlone ? 0 : warp;
     if (t < a.a.T) {
         const uint4* src = static_cast<const uint4*>(a.source(t));
         uint4 q[kWarpFp8Vecs];
 #pragma unroll
         for (int i = 0; i < kWarpFp8Vecs; ++i)
-            if (i * 32 + lane < nvec) q[i] = ld_stream_v4(src + i * 32 + lane);
-        const int nd = a.destinations(t, s_row[warp], s_j[warp]);
-        for (int d = 0; d < nd; ++d) {
-            uint4* dst = reinterpret_cast<uint4*>(a.dst) + static_cast<size_t>(s_row[warp][d]) * nvec + lane;
-#pragma unroll
-            for (int i = 0; i < kWarpFp8Vecs; ++i)
-                if (i * 32 + lane < nvec) st_v4(dst + i * 32, q[i]);
+            if (i * kStride + first < nvec) q[i] = ld_stream_v4(src + i * kStride + first);
+        int nd = 0;
+        if (!kAlone || warp == 0) nd = a.destinations(t, s_row[mine], s_j[mine]);
+        if constexpr (kAlone) {
+            if (threadIdx.x == 0) s_nd = nd;
+            __syncthreads();
+            nd = s_nd;
         }
-        a.side_work(t, nd, s_row[warp], s_j[warp]);
+        for (int v0 = first; v0 < nvec; v0 += kWarpFp8Vecs * kStride) {
+            if (kAlone && v0 != first) {
+#pragma unroll
+                for (int i = 0; i < kWarpFp8Vecs; ++i)
+                    if (i * kStride + v0 < nvec) q[i] = ld_stream_v4(src + i * kStride + v0);
+            }
+            for (int d = 0; d < nd; ++d) {
+                uint4* dst = reinterpret_cast<uint4*>(a.dst) + static_cast<size_t>(s_row[mine][d]) * nvec + v0;
+#pragma unroll
+                for (int i = 0; i < kWarpFp8Vecs; ++i)
+                    if (i * kStride + v0 < nvec) st_v4(dst + i * kStride, q[i]);
+            }
+        }
+        if (!kAlone || warp == kWarps - 1) a.side_work(t, nd, s_row[mine], s_j[mine]);
     }
     allow_dependents();
 }
@@ -597,13 +615,16 @@ __global__ void __launch_bounds__(kThreads, 4) combine_permuted_kernel(CombinePe
 // ep_dispatch_permuted_fp8 (kFp8).
 //
 // A call this small is bound by its chain of dependent steps: ids, counts, scan, rows,
-// stores. 128 x 7168 top-8: 4.3 us in E4M3, 5.7 us in bf16; 667 x 640 top-10 8.1 us. Finding
-// a token's repeats with a warp-wide match instead of shuffles costs 1 us a pass over the
-// ids; requesting eight ids at a time makes the code longer, and its first fetch 0.4 us slower.
+// stores. 128 x 7168 top-8 in E4M3: 3.9 us with 512 threads a CTA (4.3 us with 1024), in bf16,
+// twice the vectors, 7.1 us (5.7 us with 1024); 667 x 640 top-10 9.0 us (8.1 us). Finding a
+// token's repeats with a warp-wide match instead of shuffles costs 1 us a pass over the ids;
+// requesting eight ids at a time makes the code longer, and its first fetch 0.4 us slower.
 constexpr int kLLMaxTokens = 1024;
 constexpr int kLLMaxEntries = 8192;  // T * k
-constexpr int kLLThreads = 1024;
-constexpr int kLLWarps = kLLThreads / 32;
+// 512 threads a CTA up to so many entries where they copy a vector each, or the whole batch
+// has so few vectors; else 1024
+constexpr int kLLFewEntries = 2048;
+constexpr int kLLFewVectors = 32768;
 constexpr int kLLOwn = 8;    // most tokens of a CTA
 constexpr int kLLBatch = 2;  // ids a lane requests at a time
 constexpr int kLLAhead = 2;  // vectors a thread requests at a time
@@ -624,8 +645,9 @@ struct LLArgs {
     int32_t* status;
 };
 
-template <bool kFp8>
+template <bool kFp8, int kLLThreads>
 __global__ void __launch_bounds__(kLLThreads, 1) dispatch_permuted_ll_kernel(LLArgs a, int count) {
+    constexpr int kLLWarps = kLLThreads / 32;
     // a decode batch's grid leaves most of every SM free: the next kernel (the expert work,
     // or the low-latency combine launched as a dependent launch) may settle its CTAs now and
     // wait on the device for this grid, so its launch latency is hidden behind this one
@@ -703,10 +725,16 @@ __global__ void __launch_bounds__(kLLThreads, 1) dispatch_permuted_ll_kernel(LLA
     }
     __syncthreads();
 
-    // 2. the offsets: a thread per expert (E <= kLLThreads), warp scans, then the warps' totals
+    // 2. the offsets: kPer experts a thread, warp scans, then the warps' totals
     {
-        const int c = tid < E ? s_count[tid] : 0;
-        int incl = c;
+        constexpr int kPer = kMaxExpertsPerm / kLLThreads;
+        int c[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            c[i] = tid * kPer + i < E ? s_count[tid * kPer + i] : 0;
+            sum += c[i];
+        }
+        int incl = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(kFullMask, incl, off);
@@ -714,11 +742,17 @@ __global__ void __launch_bounds__(kLLThreads, 1) dispatch_permuted_ll_kernel(LLA
         }
         if (lane == 31) s_part[warp] = incl;
         __syncthreads();
-        int base = lane < warp ? s_part[lane] : 0;
+        int run = lane < warp ? s_part[lane] : 0;
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) base += __shfl_xor_sync(kFullMask, base, off);
-        if (tid < E) s_off[tid] = base + incl - c;
-        if (tid == E - 1) s_off[E] = base + incl;
+        for (int off = 16; off >= 1; off >>= 1) run += __shfl_xor_sync(kFullMask, run, off);
+        run += incl - sum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i;
+            if (e < E) s_off[e] = run;
+            run += c[i];
+            if (e == E - 1) s_off[E] = run;
+        }
         __syncthreads();
     }
     if (blockIdx.x == 0) {
@@ -1252,12 +1286,17 @@ int token_grid(long long work) {
     return static_cast<int>(want < 1 ? 1 : (want < cap ? want : cap));
 }
 
-ep_status_t launch_ll(void (*kernel)(LLArgs, int), const LLArgs& a, cudaStream_t stream) {
+template <bool kFp8>
+ep_status_t launch_ll(const LLArgs& a, cudaStream_t stream) {
     const int sms = sm_count();
     const int spread = (a.T + sms - 1) / sms;
     const int count = spread < 1 ? 1 : (spread < kLLOwn ? spread : kLLOwn);
     const int grid = a.T < 1 ? 1 : (a.T + count - 1) / count;
-    return launch_dependent(kernel, dim3(grid), dim3(kLLThreads), 0, stream, a, count);
+    const bool few = a.T * a.k <= kLLFewEntries &&
+                     (count * a.nvec <= 512 || static_cast<long long>(a.T) * a.nvec <= kLLFewVectors);
+    const int threads = few ? 512 : 1024;
+    auto kernel = few ? dispatch_permuted_ll_kernel<kFp8, 512> : dispatch_permuted_ll_kernel<kFp8, 1024>;
+    return launch_dependent(kernel, dim3(grid), dim3(threads), 0, stream, a, count);
 }
 
 }  // namespace
@@ -1389,7 +1428,7 @@ extern "C" ep_status_t ep_dispatch_permuted_ll(const void* x, const int64_t* top
         return EP_ERR_INVALID;
     const LLArgs a{x, H / 8, nullptr, nullptr, topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets, expert_slot,
                    perm_x, perm_src, perm_w, status};
-    return launch_ll(dispatch_permuted_ll_kernel<false>, a, as_stream(stream));
+    return launch_ll<false>(a, as_stream(stream));
 }
 
 extern "C" ep_status_t ep_dispatch_permuted_fp8(const uint8_t* x_q, const float* x_scales, const int64_t* topk_idx,
@@ -1411,8 +1450,11 @@ extern "C" ep_status_t ep_dispatch_permuted_fp8(const uint8_t* x_q, const float*
                              perm_src, perm_w, status};
     const PermFp8Scatter sp{a, x_q, x_scales, perm_scales, reinterpret_cast<char*>(perm_q), static_cast<uint32_t>(H),
                             status};
+    if (T <= sm_count())
+        return launch_dependent(dispatch_permuted_fp8_kernel<true>, dim3(static_cast<unsigned>(T)), dim3(kThreads), 0,
+                                as_stream(stream), sp);
     if (H <= kWarpFp8Vecs * 512)
-        return launch_dependent(dispatch_permuted_fp8_kernel, dim3(static_cast<unsigned>((T - 1) / kWarps + 1)),
+        return launch_dependent(dispatch_permuted_fp8_kernel<false>, dim3(static_cast<unsigned>((T - 1) / kWarps + 1)),
                                 dim3(kThreads), 0, as_stream(stream), sp);
     return launch_scatter_rows(sp, T, as_stream(stream));
 }
@@ -1436,7 +1478,7 @@ extern "C" ep_status_t ep_dispatch_permuted_fp8_ll(const uint8_t* x_q, const flo
         return EP_ERR_INVALID;
     const LLArgs a{x_q, H / 16, x_scales, perm_scales, topk_idx, topk_w, T, H, k, E, R, max_rows, expert_offsets,
                    expert_slot, perm_q, perm_src, perm_w, status};
-    return launch_ll(dispatch_permuted_ll_kernel<true>, a, as_stream(stream));
+    return launch_ll<true>(a, as_stream(stream));
 }
 
 extern "C" ep_status_t ep_combine_send(const void* y_perm, const int32_t* recv_src_idx, const int32_t* recv_topk_idx,

@@ -13,12 +13,15 @@ using namespace ep;
 constexpr int kMaxTopk = 32;
 constexpr int kWarps = 8;         // most warps of a CTA of the return's gradient
 // Rows of the return's gradient up to this many channels, where there are many, go two to a
-// warp: their positions are then resolved together (8000 x 1024 top-6 36.0 us instead of 38.7
-// us; 1237 x 1592 top-9, too few, 17.2 us instead of 15.1 us).
+// warp: their positions are then resolved together (8000 x 1024 top-6 37.0 us instead of 38.7
+// us; 1237 x 1592 top-9, too few, 17.2 us instead of 15.5 us).
 constexpr int kShortRowH = 1024;
-constexpr int kSmallSplit = 4;  // warps of an entry where there are few (44 x 4176 top-4: 2.5 us instead of 4.2 us)
+// Entries an SM below which the return's gradient puts four warps on each row (44 x 4176
+// top-4: 2.6 us instead of 4.2 us; 777 x 1032 top-6, 31 an SM, 8.6 us instead of 4.6 us)
+constexpr int kFewEntries = 8;
 constexpr int kSortWarps = 16;  // most warps of a CTA of the sort's gradient
 constexpr int kSortThreads = 64;  // threads of a token there, where tokens abound
+constexpr int kSortFill = 768;    // threads an SM that fill the GPU
 constexpr int kWarpRowH = 2048;   // rows up to this take a warp each
 constexpr int kVecs = 4;   // 16-byte vectors of a row per thread and step (return)
 
@@ -67,67 +70,64 @@ struct CombineBwdArgs {
     int32_t* status;
 };
 
-// A CTA takes `count` consecutive entries (t, j), t * k + j in order, kSplit warps on an entry
-// at a time. The warp's lanes resolve its entries, then it streams each entry's row of y and
-// the token's dout -- which the warps of the token's other entries read at the same time, so
-// that L1 serves them -- and writes dy's row = bf16(w * dout). The dot product is kept in
-// fp32 in one sum per channel of a vector (at most H / (256 kSplit) terms each), added across
-// the vector, the lanes and the entry's warps at the end.
+// A CTA takes `count` consecutive entries (t, j), t * k + j in order, kLanes threads on an
+// entry at a time. They resolve its row, then stream the row of y and the token's dout --
+// which the warps of the token's other entries read at the same time, so that L1 serves them
+// -- and write dy's row = bf16(w * dout). The dot product is kept in fp32 in one sum per
+// channel of a vector (at most H / (8 kLanes) terms each), added across the vector, the lanes
+// and the entry's warps at the end.
 //
 // At 64 registers 32 warps with 4 vectors of y each in flight fit an SM: 4096 x 7168 top-8 in
 // 153 us (6.5 TB/s, 0.96 of a measured copy); 157 us with 72 registers or 2 vectors. Requesting
 // dout before the row is known costs 2 %, two warps a row 3 %, the token's rows one after the
 // other by a whole CTA 1 % (and 777 x 1032 top-6 then takes 10.9 us instead of 4.5 us).
-template <int kSplit>
+template <int kLanes>
 __global__ void __launch_bounds__(32 * kWarps, 4) combine_bwd_kernel(CombineBwdArgs a, int count) {
+    constexpr int kSub = kLanes < 32 ? kLanes : 32;  // lanes of an entry in a warp
+    constexpr int kSplit = kLanes / kSub;            // warps of an entry
     __shared__ float s_dot[kWarps];
     grid_dependency_wait();  // dependent launch: inputs are ready after this
     const int tid = static_cast<int>(threadIdx.x);
-    const int lane = lane_id();
-    const int part = (tid >> 5) % kSplit;
-    const int at_once = static_cast<int>(blockDim.x >> 5) / kSplit;
+    const int first = tid % kLanes;
+    const int at_once = static_cast<int>(blockDim.x) / kLanes;
     const long long entry0 = static_cast<long long>(blockIdx.x) * count;
     const long long entries = static_cast<long long>(a.T) * a.k;
     const int mine = entries - entry0 < count ? static_cast<int>(entries - entry0) : count;
     const int nvec = a.H / 8;
     const bool dots = a.dtopk_w != nullptr;
-    const int first = part * 32 + lane;
-    uint4 g[kVecs];
-    auto load_dout = [&](int e, int v0) {
-        const uint4* const dout = reinterpret_cast<const uint4*>(a.dout) + (entry0 + e) / a.k * nvec + v0;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-            if (v0 + i * 32 * kSplit < nvec) g[i] = __ldg(dout + i * 32 * kSplit);
-    };
-    // lane r resolves the warp's entry of round r
-    const int e_first = (tid >> 5) / kSplit;
+    // the entries of rounds 0, 1, ... of these lanes are resolved together, a lane each
+    const int e_first = tid / kLanes;
+    const int sub = tid % kSub;
     long long my_row = -1;
     float my_w = 1.0f;
-    if (e_first + lane * at_once < mine) {
-        const size_t entry = static_cast<size_t>(entry0 + e_first + lane * at_once);
+    if (e_first + sub * at_once < mine) {
+        const size_t entry = static_cast<size_t>(entry0 + e_first + sub * at_once);
         if (a.topk_w != nullptr) my_w = a.topk_w[entry];
         my_row = entry_row(a.topk_idx, a.offsets, a.eslot, entry, a.E, a.E / a.R, a.max_rows);
         if (my_row == -2) raise_flag(a.status, EP_FLAG_CAPACITY);
     }
-    for (int r = 0; r * at_once < mine; ++r) {
+    for (int r = 0; r * at_once < mine; ++r) {  // the same number of rounds for all threads
         const int e = e_first + r * at_once;
-        const long long row = __shfl_sync(kFullMask, my_row, r);
-        const float w = __shfl_sync(kFullMask, my_w, r);
+        const long long row = __shfl_sync(kFullMask, my_row, r, kSub);
+        const float w = __shfl_sync(kFullMask, my_w, r, kSub);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (row >= 0) {
+            const uint4* dout = reinterpret_cast<const uint4*>(a.dout) + (entry0 + e) / a.k * nvec;
             const uint4* y = reinterpret_cast<const uint4*>(a.y) + row * nvec;
             uint4* dy = reinterpret_cast<uint4*>(a.dy) + row * nvec;
-            for (int v0 = first; v0 < nvec; v0 += 32 * kSplit * kVecs) {
-                uint4 yv[kVecs];
+            for (int v0 = first; v0 < nvec; v0 += kLanes * kVecs) {
+                uint4 g[kVecs], yv[kVecs];
                 if (dots) {
 #pragma unroll
                     for (int i = 0; i < kVecs; ++i)
-                        if (v0 + i * 32 * kSplit < nvec) yv[i] = ld_inout_v4(y + v0 + i * 32 * kSplit);
+                        if (v0 + i * kLanes < nvec) yv[i] = ld_inout_v4(y + v0 + i * kLanes);
                 }
-                load_dout(e, v0);
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+                    if (v0 + i * kLanes < nvec) g[i] = __ldg(dout + v0 + i * kLanes);
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    const int v = v0 + i * 32 * kSplit;
+                    const int v = v0 + i * kLanes;
                     if (v >= nvec) continue;
                     float d[8];
                     unpack8(d, g[i]);
@@ -146,17 +146,17 @@ __global__ void __launch_bounds__(32 * kWarps, 4) combine_bwd_kernel(CombineBwdA
         if (dots) {
             float dot = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(kFullMask, dot, off);
+            for (int off = kSub / 2; off >= 1; off >>= 1) dot += __shfl_xor_sync(kFullMask, dot, off);
             if constexpr (kSplit > 1) {
-                if (lane == 0) s_dot[tid >> 5] = dot;
+                if (sub == 0) s_dot[tid >> 5] = dot;
                 __syncthreads();
-                if (part == 0) {
+                if (first == 0) {
 #pragma unroll
                     for (int i = 1; i < kSplit; ++i) dot += s_dot[(tid >> 5) + i];
                 }
-                __syncthreads();  // s_dot is written again for the next entries
+                __syncthreads();  // s_dot is written again in the next round
             }
-            if (part == 0 && lane == 0 && e < mine) a.dtopk_w[entry0 + e] = dot;
+            if (first == 0 && e < mine) a.dtopk_w[entry0 + e] = dot;
         }
     }
     allow_dependents();
@@ -238,7 +238,8 @@ __device__ __forceinline__ void add_rows(const DispatchBwdArgs& a, const long lo
 // 16384 x 4096 top-8 with the addend in 202 us (6.67 TB/s, 0.98 of a measured copy), 207 us
 // with 256 threads and 238 us with 512, which wait longer for their lists; a warp per row up
 // to 2048 channels (8000 x 1024 top-6: 22.6 us instead of 24.9 us), not above (16384 x 4096:
-// 217 us). At most a token per SM: as many threads as there are vectors, up to 512.
+// 217 us). Few tokens: more threads each (281 x 6320 top-9 9.4 us instead of 32.6 us; 20 x
+// 4024 top-10 3.2 us instead of 6.2 us).
 template <int kVec, int kRows>
 __global__ void __maxnreg__((kVec == 1 ? 64 : 72)) dispatch_bwd_kernel(DispatchBwdArgs a, int per_warp) {
     grid_dependency_wait();
@@ -270,8 +271,8 @@ __global__ void __maxnreg__((kVec == 1 ? 64 : 72)) dispatch_bwd_kernel(DispatchB
     }
     if (!per_warp) __syncthreads();
     if (t < a.T) {
-        add_rows<kVec, kRows>(a, s_row[mine], s_n[mine], in, reinterpret_cast<uint4*>(a.dx) + static_cast<size_t>(t) * nvec,
-                              nvec, first, first_v, stride);
+        uint4* const out = reinterpret_cast<uint4*>(a.dx) + static_cast<size_t>(t) * nvec;
+        add_rows<kVec, kRows>(a, s_row[mine], s_n[mine], in, out, nvec, first, first_v, stride);
         if ((per_warp || warp == 0) && lane < a.k && a.dtopk_w != nullptr)
             a.dtopk_w[static_cast<size_t>(t) * a.k + lane] = dw;
     }
@@ -304,18 +305,29 @@ extern "C" ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, 
                            expert_offsets, expert_slot, T, H, k, E, R, max_rows, static_cast<uint16_t*>(dy), dtopk_w,
                            status};
     const long long entries = static_cast<long long>(T) * k;
-    // few entries (an SM holds 4 CTAs): more warps on each row
-    const bool few = entries <= static_cast<long long>(sm_count()) * (4 * kWarps / kSmallSplit);
-    // otherwise a warp per entry and CTAs of a token's entries, or an even part of them
-    const int parts = (k + kWarps - 1) / kWarps;
-    const int warps = few ? kWarps : (k + parts - 1) / parts;
+    // Few entries: enough warps on each row to fill the GPU (an SM holds 32 warps). Many: short
+    // rows take part of a warp, so that its 4 vectors a lane are all of use (6933 x 192 top-7
+    // 9.4 us instead of 17.6 us, 8000 x 512 top-6 20.1 us instead of 24.7 us). Otherwise a warp a
+    // row, and CTAs of a token's entries or an even part of them.
+    const long long per_sm = entries / sm_count();
+    auto kernel = combine_bwd_kernel<32>;
+    int lanes = 32, threads = 32 * kWarps;
+    if (per_sm < kFewEntries) {
+        kernel = combine_bwd_kernel<128>, lanes = 128;
+    } else if (H <= 256) {
+        kernel = combine_bwd_kernel<8>, lanes = 8;
+    } else if (H <= 512) {
+        kernel = combine_bwd_kernel<16>, lanes = 16;
+    } else {
+        const int parts = (k + kWarps - 1) / kWarps;
+        threads = 32 * ((k + parts - 1) / parts);
+    }
     // many short rows: two rounds a CTA
-    const bool rounds = H <= kShortRowH && entries >= static_cast<long long>(sm_count()) * (4 * 4 * kWarps);
-    const int count = few ? kWarps / kSmallSplit : warps * (rounds ? 2 : 1);
+    const int rounds = H <= kShortRowH && entries * lanes >= 32LL * sm_count() * (4 * 4 * kWarps) ? 2 : 1;
+    const int count = threads / lanes * rounds;
     const long long grid = (entries + count - 1) / count;
     if (grid > 0x7fffffffLL) return EP_ERR_INVALID;
-    return launch_dependent(few ? combine_bwd_kernel<kSmallSplit> : combine_bwd_kernel<1>,
-                            dim3(static_cast<unsigned>(grid)), dim3(32 * warps), 0, as_stream(stream), a, count);
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, as_stream(stream), a, count);
 }
 
 extern "C" ep_status_t ep_dispatch_permuted_bwd(const void* dperm_x, const float* dperm_w, const void* dx_in,
@@ -337,11 +349,13 @@ extern "C" ep_status_t ep_dispatch_permuted_bwd(const void* dperm_x, const float
                             static_cast<uint16_t*>(dx), dtopk_w, status};
     auto kernel = k == 1 ? dispatch_bwd_kernel<4, 1> : k <= 4 ? dispatch_bwd_kernel<2, 4> : dispatch_bwd_kernel<1, 8>;
     const int vec = k == 1 ? 4 : k <= 4 ? 2 : 1;
-    if (H <= kWarpRowH && T > sm_count())
+    if (H <= kWarpRowH && T >= 16 * sm_count())
         return launch_dependent(kernel, dim3(static_cast<unsigned>(T / 4 + (T % 4 != 0))), dim3(128), 0,
                                 as_stream(stream), a, 1);
-    const int most = T <= sm_count() ? 32 * kSortWarps : kSortThreads;
-    const int threads = (H / 8 + 32 * vec - 1) / (32 * vec) * 32;
-    return launch_dependent(kernel, dim3(static_cast<unsigned>(T)), dim3(threads < most ? threads : most), 0,
-                            as_stream(stream), a, 0);
+    // as many threads as the row has vectors, no fewer than fill the GPU
+    const int fill = (kSortFill * sm_count() / T + 31) / 32 * 32;
+    const int most = fill < kSortThreads ? kSortThreads : fill < 32 * kSortWarps ? fill : 32 * kSortWarps;
+    const int steps = (H / 8 - 1) / (vec * most) + 1;  // all steps with as many threads
+    const int threads = ((H / 8 - 1) / (vec * steps) + 32) / 32 * 32;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(T)), dim3(threads), 0, as_stream(stream), a, 0);
 }
