@@ -681,10 +681,11 @@ __global__ void __launch_bounds__(kLLThreads, 1) dispatch_permuted_ll_kernel(LLA
     const bool wide = (nblk & 3) == 0;
     const int nscales = wide ? nblk / 4 : nblk;
     uint4 scale = make_uint4(0, 0, 0, 0);
-    auto load_rows = [&](int i0) {
+    const uint32_t vectors = static_cast<uint32_t>(own) * nvec;  // below 2^31: own <= 8, nvec < 2^28
+    auto load_rows = [&](uint32_t i0) {
 #pragma unroll
         for (int u = 0; u < kLLAhead; ++u)
-            if (i0 + u * kLLThreads < own * nvec) ahead[u] = ld_stream_v4(src + i0 + u * kLLThreads);
+            if (i0 + u * kLLThreads < vectors) ahead[u] = ld_stream_v4(src + i0 + u * kLLThreads);
     };
     for (int base = 0; base == 0 || base < a.T; base += kLLBatch * per_pass) {
         long long id[kLLBatch];
@@ -794,13 +795,13 @@ __global__ void __launch_bounds__(kLLThreads, 1) dispatch_permuted_ll_kernel(LLA
 
     // 4. the rows' vectors, and their scales
     uint4* const base = static_cast<uint4*>(a.perm_x);
-    for (int i0 = tid; i0 < own * nvec; i0 += kLLAhead * kLLThreads) {
-        if (i0 != tid) load_rows(i0);
+    for (uint32_t i0 = threadIdx.x; i0 < vectors; i0 += kLLAhead * kLLThreads) {
+        if (i0 != threadIdx.x) load_rows(i0);
 #pragma unroll
         for (int u = 0; u < kLLAhead; ++u) {
-            const int i = i0 + u * kLLThreads;
-            if (i >= own * nvec) break;
-            const int l = i / nvec, at = i - l * nvec;
+            const uint32_t i = i0 + u * kLLThreads;
+            if (i >= vectors) break;
+            const uint32_t l = i / static_cast<uint32_t>(nvec), at = i - l * nvec;
             const int nd = s_nd[l];
             for (int d = 0; d < nd; ++d) st_v4(base + static_cast<size_t>(s_row[l][d]) * nvec + at, ahead[u]);
         }

@@ -509,7 +509,7 @@ ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, const int64
  *   residual_out stream_dtype [T][H] or NULL; may be the same array as residual
  *   y            bf16 [T][H] or NULL; may be the same array as x
  *   y_q uint8 [T][H] and y_scales fp32 [T][H/128]: both or neither
- *   at least one output. One launch, one thread block per row; T = 1 is an ordinary size. */
+ *   at least one output. One launch; T = 1 is an ordinary size. */
 ep_status_t ep_rmsnorm(const void* x, const void* residual, const void* weight,
                        ep_dtype_t stream_dtype, ep_dtype_t weight_dtype, float eps, int32_t T,
                        int32_t H, void* residual_out, void* y, uint8_t* y_q, float* y_scales,
