@@ -104,6 +104,35 @@ def test_norm_against_definition(T, H, carry, wdt):
         check_guards(sback, T * H // 128, SENT_F32)
 
 
+@pytest.mark.parametrize("T,H", [(20000, 8), (12000, 264), (12001, 512), (5000, 1032), (1500, 4104), (1200, 7168),
+                                 (400, 16384), (153, 128)])
+@pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inputs", ["x", "residual", "both"])
+def test_norm_of_many_rows(T, H, carry, inputs):
+    """More rows than fit the GPU at once: every form of the kernel takes several rows a CTA."""
+    x = rand((T, H), 61) if inputs != "residual" else None
+    residual = rand((T, H), 62, 3.0, carry) if inputs != "x" else None
+    weight = weights(H, torch.float32 if T % 2 else torch.bfloat16)
+    fp8 = H % 128 == 0
+    sent = SENT_BF16 if carry == torch.bfloat16 else SENT_F32
+    rout, rback = guarded((T, H), carry, sent)
+    y, yback = guarded((T, H), torch.bfloat16, SENT_BF16)
+    q, qback = guarded((T, H), torch.uint8, 0x7E) if fp8 else (None, None)
+    sc, sback = guarded((T, H // 128), torch.float32, SENT_F32) if fp8 else (None, None)
+    ep.ep_rmsnorm(x, residual, weight, EPS, rout, y, q, sc)
+    torch.cuda.synchronize()
+    z, v = definition(x, residual, weight)
+    assert torch.equal(rout, (x.float() + residual.float() if inputs == "both" else
+                              x.float() if inputs == "x" else residual.float()).to(carry))
+    assert rounds_from(y, v, v.abs() * 2.0 ** -18)
+    check_guards(rback, T * H, sent)
+    check_guards(yback, T * H, SENT_BF16)
+    if fp8:
+        check_quantised(q, sc, v)
+        check_guards(qback, T * H, 0x7E)
+        check_guards(sback, T * H // 128, SENT_F32)
+
+
 @pytest.mark.parametrize("H", [128, 1024, 7168])
 @pytest.mark.parametrize("case", ["x only", "residual only", "fp8 only", "y only", "residual_out of x"])
 def test_norm_subsets_of_inputs_and_outputs(H, case):
@@ -222,6 +251,28 @@ def test_norm_quantises_as_the_fp8_dispatch_does():
     assert torch.equal(d.recv_x[0], q) and torch.equal(d.recv_scales[0], sc)
 
 
+@pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
+def test_norm_quantises_blocks_whose_scale_is_subnormal(carry):
+    """Blocks around 2^-130, whose scale has no finite reciprocal, next to ordinary ones: the
+    division itself, as the FP8 dispatch makes it of the same bf16 values."""
+    T, H = 9, 1024
+    x = torch.where(rand((T, H), 14).float() > 0, 2.0, -2.0)
+    weight = torch.ones(H, device="cuda")
+    weight[::3] = 0.375
+    weight[::5] = 0.5
+    weight[128:384] *= 2.0 ** -130
+    weight[640:768] *= 2.0 ** -118
+    y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    sc = torch.empty((T, H // 128), device="cuda")
+    ep.ep_rmsnorm(None, x.to(carry), weight, 0.0, None, y, q, sc)
+    topk = torch.zeros((T, 1), dtype=torch.int64, device="cuda")
+    lay = ep.get_layout(topk, 1, 1)
+    d = ep.dispatch(y, topk, torch.ones((T, 1), device="cuda"), lay, T, fp8=True)
+    assert torch.all(sc[:, 1:3] < 2.0 ** -126) and torch.all(sc[:, 1:3] > 0)
+    assert torch.equal(d.recv_scales[0], sc) and torch.equal(d.recv_x[0], q)
+
+
 def test_norm_offsets_past_32_bits():
     T, H = 140_000, 16384
     x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
@@ -281,7 +332,7 @@ def run_bwd(dy, z, weight, dz_in, dx=True, dweight=True):
     return dz, dxt, dw
 
 
-@pytest.mark.parametrize("T,H", SIZES + [(1500, 264), (700, 7168)])
+@pytest.mark.parametrize("T,H", SIZES + [(1500, 264), (700, 7168), (20000, 264), (3000, 1032), (9000, 8), (400, 16384)])
 @pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("wdt", [torch.bfloat16, torch.float32])
 def test_norm_gradient_against_formula(T, H, carry, wdt):

@@ -183,7 +183,11 @@ def sort_bwd_expected(b, dperm_x, dperm_w, dx_in):
 
 
 GRAD_CASES = CASES + [dict(T=130, H=1000, E=16, k=4, R=4, empty=0.2), dict(T=1, H=8, E=1, k=1, R=1),
-                      dict(T=9, H=16392, E=8, k=3, R=2), dict(T=40, H=8200, E=16, k=9, R=2)]
+                      dict(T=9, H=16392, E=8, k=3, R=2), dict(T=40, H=8200, E=16, k=9, R=2),
+                      dict(T=700, H=392, E=16, k=4, R=4, bad=True), dict(T=5000, H=1024, E=32, k=5, R=4, empty=0.1),
+                      dict(T=10000, H=64, E=16, k=8, R=2, max_rows=36000), dict(T=2600, H=264, E=16, k=3, R=4),
+                      dict(T=2500, H=2048, E=8, k=1, R=8, bad=True), dict(T=400, H=4104, E=8, k=2, R=1),
+                      dict(T=3000, H=2056, E=16, k=1, R=4), dict(T=500, H=7168, E=16, k=10, R=2, empty=0.3)]
 
 
 @pytest.mark.parametrize("case", GRAD_CASES, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
