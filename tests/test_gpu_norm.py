@@ -273,6 +273,38 @@ def test_norm_quantises_blocks_whose_scale_is_subnormal(carry):
     assert torch.equal(d.recv_scales[0], sc) and torch.equal(d.recv_x[0], q)
 
 
+def test_norm_rounds_codes_once_where_scales_are_small():
+    """Values at and beside the midpoints of codes, with scales from 2^-126 to 2^-80: a quotient whose
+    correction underflows is off by an fp32 ulp, which shows here. The codes are those of the IEEE division."""
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    mids = (codes[:-1] + codes[1:]) / 2
+    r = np.random.default_rng(31)
+    blocks = 127
+    H = 128 * (blocks + 1)
+    w = np.full(H, 448.0, dtype=np.float32)  # the first block shows that the root mean square is exactly 1
+    for b in range(blocks):
+        keep = r.integers(4, 24)  # leading bits of the scale
+        m = 1.0 + np.floor(r.random() * 2.0 ** keep) / 2.0 ** keep
+        amax = np.float32(448.0 * m * 2.0 ** (-126 + b % 47))
+        scale = amax / np.float32(448.0)
+        v = (r.choice(mids, 127) * np.float64(scale)).astype(np.float32)
+        beside = np.nextafter(v, np.float32(1)), np.nextafter(v, np.float32(0))
+        v = np.where(np.arange(127) % 4 < 2, v, np.where(np.arange(127) % 4 == 2, beside[0], beside[1]))
+        w[128 * (b + 1):128 * (b + 2)] = np.append(v, amax)
+    x = torch.where(rand((3, H), 32).float() > 0, 1.0, -1.0).bfloat16()
+    for carry in (torch.bfloat16, torch.float32):
+        q = torch.empty((3, H), dtype=torch.uint8, device="cuda")
+        sc = torch.empty((3, H // 128), device="cuda")
+        ep.ep_rmsnorm(None, x.to(carry), torch.from_numpy(w).cuda(), 0.0, None, None, q, sc)
+        sc = sc.cpu()
+        assert torch.all(sc[:, 0] == 1.0)
+        want = w.reshape(-1, 128) / sc[0].numpy()[:, None]
+        want = torch.from_numpy(want.reshape(H)).to(torch.float8_e4m3fn).view(torch.uint8)
+        sign = (x < 0).to(torch.uint8).cpu() << 7
+        assert torch.equal(q.cpu(), want[None] | sign)
+        assert torch.equal(sc[0], sc[1]) and torch.equal(sc[0], sc[2])
+
+
 def test_norm_offsets_past_32_bits():
     T, H = 140_000, 16384
     x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
