@@ -31,7 +31,13 @@ constexpr size_t kMaxRingSmem = 200 * 1024;
 constexpr int kRingRowBytes = 6144;
 constexpr int kRingRows = 8;      // rows of a ring CTA where one warp holds a row
 constexpr int kMaxParts = 512;    // rows of dweight partial sums
-constexpr int kBwdThreads = 448;  // threads of a gradient CTA: as many rows side by side as fit
+// Threads of a gradient CTA that has rows side by side: as many rows as fit, a CTA per SM
+// (16384 x 4096 bf16: 84.0 us instead of 87.7 us with 448 threads, whose CTAs hold one such row;
+// 16384 x 2048 with an fp32 stream 82.5 us instead of 100.5 us)
+constexpr int kBwdThreads = 704;
+// but fewer rows side by side where that leaves CTAs with less than a row for each of them:
+// one per so many rows (127 x 1024, fp32 stream: 3.5 us instead of 4.4 us)
+constexpr int kBwdRowsPerGroup = 64;
 constexpr int kBwdRows = 6;       // rows of a gradient CTA that are worth its partial sums
 constexpr int kMaxGroups = 15;    // rows side by side: a named barrier each
 constexpr int kReduceRows = 32;   // partial sums a dweight reduction CTA adds at a time
@@ -622,11 +628,12 @@ struct NormBwdArgs {
 // registers over all rows of a thread, and each CTA writes one row of partial sums (resident
 // CTAs, because every further CTA would add one). Where rows are short (kMany), a CTA has
 // several rows side by side, each with its own threads and named barrier, whose sums it adds
-// before it writes: 16384 x 1024 in 26.5 us against 46.8 us with a CTA per row. Both passes
+// before it writes: 16384 x 1024 in 25.5 us against 46.8 us with a CTA per row. Both passes
 // over a row read it from the ring, so it costs no registers between them. 4096 x 7168 bf16
-// with dz_in: 40.0 us (5.87 TB/s), 36.0 us of them without dweight.
+// with dz_in: 40.0 us (5.87 TB/s), 36.0 us of them without dweight. At 72 registers instead of
+// 80, a CTA with rows side by side takes 1 to 3 % longer.
 template <class Carry, int kVecs, int kStages, bool kWF32, bool kMany>
-__global__ void __maxnreg__((kMany ? 72 : 64)) rmsnorm_bwd_kernel(NormBwdArgs a, int rows_at_once) {
+__global__ void __maxnreg__((kMany ? 80 : 64)) rmsnorm_bwd_kernel(NormBwdArgs a, int rows_at_once) {
     constexpr int N = Carry::kElems, P = N / 2;
     extern __shared__ __align__(16) unsigned char s_ring[];
     __shared__ float2 s_part[2][32];  // [parity][warp of the CTA]
@@ -831,7 +838,9 @@ ep_status_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t stream, int* grid
     static Residency cache;
     auto kernel = rmsnorm_bwd_kernel<Carry, kVecs, kStages, kWF32, kMany>;
     const int nt = row_threads(a.H / Carry::kElems, kVecs);
-    const int groups = !kMany ? 1 : kBwdThreads / nt < kMaxGroups ? kBwdThreads / nt : kMaxGroups;
+    int groups = !kMany ? 1 : kBwdThreads / nt < kMaxGroups ? kBwdThreads / nt : kMaxGroups;
+    const int useful = (a.T - 1) / kBwdRowsPerGroup + 1;
+    if (useful < groups) groups = useful;
     const int streams = a.dz_in != nullptr ? 2 : 1;
     const size_t smem = groups * kStages * ring_row_bytes<Carry>(nt, kVecs, streams);
     int per_sm = 1;
