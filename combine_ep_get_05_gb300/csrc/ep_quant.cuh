@@ -6,14 +6,22 @@
 
 namespace ep {
 
-// x / scale correctly rounded to fp32, for a normal scale. The quotient is the product by
-// the correctly rounded reciprocal, corrected once by its residual (Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34,
-// 1990): with rcp = RN(1/scale) and q0 = RN(x * rcp) within an ulp of x / scale, the
-// residual x - q0 * scale is exact in one fused multiply-add and q0 + rcp * residual,
-// rounded once, is RN(x / scale). Quotients that fall below the fp32 normal range only
-// ever round to an E4M3 zero, whose sign is the sign of x; the correction turns a zero x
-// into +0, so x's sign bit is put back (for every other x it is already there).
+// Smallest scale whose quotients are corrected. The residual below is exact only where fp32 holds
+// it: a quotient that is not a zero code (from 2^-11 on) and the scale have 24 bits each, so the
+// residual is a multiple of the scale's exponent times 2^-57, an fp32 number from scale 2^-92 on.
+// Smaller scales take the division itself (bf16 values whose corrected quotient is an fp32 ulp off
+// are found in blocks with amax 2^-105 and below; beside a midpoint of codes it is the other code).
+constexpr float kMinCorrectedScale = 0x1p-92f;
+
+// x / scale correctly rounded to fp32, for a scale from kMinCorrectedScale on and a quotient
+// from 2^-11 on. The quotient is the product by the correctly rounded reciprocal, corrected
+// once by its residual (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. Res. Dev. 34, 1990): with rcp = RN(1/scale) and
+// q0 = RN(x * rcp) within an ulp of x / scale, the residual x - q0 * scale is exact in one
+// fused multiply-add and q0 + rcp * residual, rounded once, is RN(x / scale). Smaller
+// quotients, corrected well or not, only ever round to an E4M3 zero, whose sign is the sign
+// of x; the correction turns a zero x into +0, so x's sign bit is put back (for every other
+// x it is already there).
 __device__ __forceinline__ float quotient(float x, float scale, float rcp) {
     const float q0 = __fmul_rn(x, rcp);
     const float e = __fmaf_rn(-q0, scale, x);
