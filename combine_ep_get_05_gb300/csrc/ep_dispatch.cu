@@ -197,7 +197,7 @@ __device__ __forceinline__ void quantize16(const uint4& a, const uint4& b, uint4
             c[i] = (__float_as_uint(f[4 * i]) >> 31) << 7 | (__float_as_uint(f[4 * i + 1]) >> 31) << 15 |
                    (__float_as_uint(f[4 * i + 2]) >> 31) << 23 | (__float_as_uint(f[4 * i + 3]) >> 31) << 31;
         q = make_uint4(c[0], c[1], c[2], c[3]);
-    } else if (scale >= ep::kMinCorrectedScale) {  // the corrected product
+    } else if (ep::corrected(scale)) {  // the corrected product
         const float rcp = __frcp_rn(scale);
         q.x = ep::pack_e4m3x4_rn_sat(quotient(f[0], scale, rcp), quotient(f[1], scale, rcp),
                                      quotient(f[2], scale, rcp), quotient(f[3], scale, rcp));

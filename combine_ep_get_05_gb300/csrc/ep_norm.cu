@@ -241,7 +241,7 @@ struct NormArgs {
 // The quotient is the one of ep_quant.cuh, v / scale correctly rounded, with its sign turned:
 // with n = -1 / scale rounded, p = RN(v n), e = RN(p scale + v) and RN(e n + p) =
 // -RN(v / scale), zeros and their signs included, so the codes' sign bits are flipped at the end.
-// Scales below kMinCorrectedScale, and infinite ones, take the division.
+// Scales that are not `corrected` take the division.
 // Returns the scale of the lane's vector; `leads` is set in the lane that stores it, `mine`
 // names the vector.
 template <int kVecs, int P>
@@ -280,7 +280,7 @@ __device__ __forceinline__ float quantise(const f2 (&v)[kVecs][P], uint32_t (&co
     // a zero block: n = -1 and s = 1 return every value's own code
     const bool zero = amax[0] == 0.0f;
     const float n1 = zero ? -1.0f : -__frcp_rn(scale), s1 = zero ? 1.0f : scale;
-    const bool odd = !zero && !(scale >= kMinCorrectedScale && scale < __int_as_float(0x7f800000));
+    const bool odd = !zero && !corrected(scale);
     const bool any_odd = __any_sync(kFullMask, odd);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {

@@ -11,9 +11,13 @@ namespace ep {
 // residual is a multiple of the scale's exponent times 2^-57, an fp32 number from scale 2^-92 on.
 // Smaller scales take the division itself (bf16 values whose corrected quotient is an fp32 ulp off
 // are found in blocks with amax 2^-105 and below; beside a midpoint of codes it is the other code).
+// So do infinite scales (a block with an infinity: zeros for its finite values, NaN for infinities).
 constexpr float kMinCorrectedScale = 0x1p-92f;
 
-// x / scale correctly rounded to fp32, for a scale from kMinCorrectedScale on and a quotient
+__device__ __forceinline__ bool below_infinity(float v) { return v < __int_as_float(0x7f800000); }
+__device__ __forceinline__ bool corrected(float scale) { return scale >= kMinCorrectedScale && below_infinity(scale); }
+
+// x / scale correctly rounded to fp32, for a scale that is `corrected` and a quotient
 // from 2^-11 on. The quotient is the product by the correctly rounded reciprocal, corrected
 // once by its residual (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", IBM J. Res. Dev. 34, 1990): with rcp = RN(1/scale) and
@@ -30,10 +34,10 @@ __device__ __forceinline__ float quotient(float x, float scale, float rcp) {
 }
 
 // amax / 448 correctly rounded: the same correction with RN(1/448), valid while the
-// quotient is a normal fp32 (amax >= 2^-116); smaller amax take the IEEE division
+// quotient is a normal fp32 (amax >= 2^-116) and finite; other amax take the IEEE division
 __device__ __forceinline__ float scale_of(float amax) {
     constexpr float kInv448 = 1.0f / 448.0f;  // correctly rounded at compile time
-    if (amax < 0x1p-116f) return __fdiv_rn(amax, 448.0f);
+    if (!(amax >= 0x1p-116f && below_infinity(amax))) return __fdiv_rn(amax, 448.0f);
     const float q0 = __fmul_rn(amax, kInv448);
     return __fmaf_rn(__fmaf_rn(-q0, 448.0f, amax), kInv448, q0);
 }

@@ -173,7 +173,9 @@ ep_status_t ep_get_layout_noalloc(const int64_t* topk_idx, int32_t T, int32_t k,
  *                            128 elements of block b (fp32, correctly rounded
  *                            division; q rounded once to nearest-even and
  *                            saturated to +-448; a block with amax 0 stores
- *                            scale 0 and the signed zero code of each element)
+ *                            scale 0 and the signed zero code of each element,
+ *                            one with an infinity stores scale infinity, zeros
+ *                            for its finite elements and NaN for infinities)
  *   recv_src_idx[r][s]     = t
  *   recv_topk_idx[r][s][j] = e_j - r*(E/R) when expert e_j lives on r, else -1
  *   recv_topk_w[r][s][j]   = topk_w[t][j] when expert e_j lives on r, else 0
@@ -499,7 +501,9 @@ ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, const int64
  *   y_scales[t][b] = amax_b / 448, amax_b = max |v| over the 128 channels of block b
  *   y_q[t][h] = e4m3(v / y_scales[t][b])   (one rounding to nearest even, saturated)
  * in fp32 throughout; the norm and both outputs take the unrounded z. A block with amax 0
- * has scale 0 and signed-zero codes; a NaN becomes the NaN code and takes no part in amax.
+ * has scale 0 and signed-zero codes; one with an infinite amax has scale infinity, zeros for
+ * its finite values and NaN for the infinities; a NaN becomes the NaN code and takes no part
+ * in amax.
  *   x            bf16 [T][H] or NULL (z = residual)
  *   residual     stream_dtype [T][H] or NULL (z = x); x or residual is required
  *   weight       weight_dtype [H]

@@ -56,3 +56,62 @@ def test_fp8_dispatch_rounds_codes_once_where_scales_are_small(H):
     want_q, want_s = quantised_by_oracle(bits)
     assert np.array_equal(s, want_s)
     assert np.array_equal(q, want_q)
+
+
+@pytest.mark.parametrize("H", [1024, 1152])  # through shared memory; through registers
+def test_fp8_dispatch_of_infinite_values(H):
+    """A block with an infinity has an infinite scale: 0 for its finite values, NaN for infinities."""
+    x = np.random.default_rng(41).standard_normal((5, H)).astype(np.float32)
+    x[1, 3], x[2, 200], x[2, 201], x[3, H - 1] = np.inf, -np.inf, np.inf, -np.inf
+    bits = bf16_bits(x)
+    q, s = dispatched(bits)
+    with np.errstate(invalid="ignore"):
+        want_q, want_s = quantised_by_oracle(bits)
+    assert np.isinf(want_s).sum() == 3
+    assert np.array_equal(s, want_s)
+    nan = (want_q & 0x7F) == 0x7F
+    assert nan.sum() == 4 and np.all((q[nan] & 0x7F) == 0x7F)
+    assert np.array_equal(q[~nan], want_q[~nan])
+
+
+def normed(weight, carry, T=3, quarter=False):
+    """Codes and scales of v = +-weight, or of v in {0, +-2 weight} (a quarter of the channels is
+    2, the others 0), and v itself in fp32."""
+    H = weight.size
+    rng = np.random.default_rng(42)
+    z = np.where(rng.random((T, H)) < 0.5, -1.0, 1.0).astype(np.float32)
+    if quarter:
+        z *= np.where(np.arange(H) % 4 == 1, 2.0, 0.0).astype(np.float32)
+    q = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    s = torch.empty((T, H // 128), device="cuda")
+    ep.ep_rmsnorm(None, torch.from_numpy(z).cuda().to(carry), torch.from_numpy(weight).cuda(), 0.0, None, None, q, s)
+    with np.errstate(over="ignore", invalid="ignore"):
+        v = z * weight
+    return host_bits(q), host_bits(s), v
+
+
+def by_division(v):
+    """The stated format: scale = amax / 448, code = e4m3(v / scale), saturated; where the scale is 0
+    every value's own code; NaN takes no part in amax and becomes the code 0x7F."""
+    blocks = v.reshape(v.shape[0], -1, 128)
+    with np.errstate(invalid="ignore", over="ignore"):
+        s = np.fmax.reduce(np.abs(blocks), axis=2, initial=np.float32(0)) / np.float32(448.0)
+        quotient = blocks / np.where(s > 0, s, np.float32(1.0))[:, :, None]
+    q = torch.from_numpy(np.clip(quotient, -448.0, 448.0)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    return np.where(np.isnan(quotient), np.uint8(0x7F), q).reshape(v.shape), s
+
+
+@pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [1024, 7168])
+def test_norm_of_blocks_that_overflow(carry, H):
+    """Products above the largest fp32 number: scale infinity, 0 for the block's finite values."""
+    weight = np.random.default_rng(43).uniform(0.5, 1.0, H).astype(np.float32)
+    weight[130], weight[133], weight[300], weight[641] = 3e38, 3e38, -3e38, np.inf
+    weight[H - 127] = 1e38  # twice that is finite
+    q, s, v = normed(weight, carry, quarter=True)
+    want_q, want_s = by_division(v)
+    assert np.isinf(want_s).any(0).sum() == 2  # channels 133 and 641 are among the quarter, 130 and 300 are not
+    assert np.array_equal(s, want_s)
+    nan = (want_q & 0x7F) == 0x7F
+    assert nan.any() and np.all((q[nan] & 0x7F) == 0x7F)
+    assert np.array_equal(q[~nan], want_q[~nan])
