@@ -230,8 +230,9 @@ struct NormArgs {
 };
 
 // The E4M3 codes of a thread's vectors; G = kBlock / (2 P) lanes hold a block. A block whose
-// largest magnitude is 0 has scale 0 and every value's own code (a signed zero, or NaN);
-// NaNs do not take part in the maximum. Lanes past the row's end pass zeros.
+// scale is 0 (the largest magnitude is 0, or at most 224 * 2^-149, which over 448 rounds to 0)
+// has every value's own code (a signed zero, or NaN); NaNs do not take part in the maximum.
+// Lanes past the row's end pass zeros.
 //
 // The maxima of the kVecs vectors are reduced together: at each of the first log2(kVecs)
 // steps a lane keeps half of its vectors and hands the other half to its partner, so that
@@ -278,7 +279,7 @@ __device__ __forceinline__ float quantise(const f2 (&v)[kVecs][P], uint32_t (&co
     for (; off >= 1; off >>= 1) amax[0] = fmaxf(amax[0], __shfl_xor_sync(kFullMask, amax[0], off));
     const float scale = scale_of(amax[0]);
     // a zero block: n = -1 and s = 1 return every value's own code
-    const bool zero = amax[0] == 0.0f;
+    const bool zero = scale == 0.0f;
     const float n1 = zero ? -1.0f : -__frcp_rn(scale), s1 = zero ? 1.0f : scale;
     const bool odd = !zero && !corrected(scale);
     const bool any_odd = __any_sync(kFullMask, odd);

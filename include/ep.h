@@ -500,10 +500,10 @@ ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, const int64
  *   y[t][h] = bf16_rn(v)
  *   y_scales[t][b] = amax_b / 448, amax_b = max |v| over the 128 channels of block b
  *   y_q[t][h] = e4m3(v / y_scales[t][b])   (one rounding to nearest even, saturated)
- * in fp32 throughout; the norm and both outputs take the unrounded z. A block with amax 0
- * has scale 0 and signed-zero codes; one with an infinite amax has scale infinity, zeros for
- * its finite values and NaN for the infinities; a NaN becomes the NaN code and takes no part
- * in amax.
+ * in fp32 throughout; the norm and both outputs take the unrounded z. A block whose
+ * scale rounds to 0 (amax up to 224 * 2^-149) has signed-zero codes; one with an infinite
+ * amax has scale infinity, zeros for its finite values and NaN for the infinities; a NaN
+ * becomes the NaN code and takes no part in amax.
  *   x            bf16 [T][H] or NULL (z = residual)
  *   residual     stream_dtype [T][H] or NULL (z = x); x or residual is required
  *   weight       weight_dtype [H]

@@ -115,3 +115,22 @@ def test_norm_of_blocks_that_overflow(carry, H):
     nan = (want_q & 0x7F) == 0x7F
     assert nan.any() and np.all((q[nan] & 0x7F) == 0x7F)
     assert np.array_equal(q[~nan], want_q[~nan])
+
+
+@pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [1024, 7168])
+def test_norm_of_blocks_whose_scale_rounds_to_zero(carry, H):
+    """amax up to 224 * 2^-149 over 448 is 0 in fp32: the values' own codes (signed zeros), no
+    division by 0; one step above it the scale is 2^-149."""
+    rng = np.random.default_rng(44)
+    weight = rng.uniform(0.5, 1.0, H).astype(np.float32)
+    for b, most in ((1, 1), (2, 224), (4, 225), (5, 2000), (6, 3)):
+        steps = rng.integers(0, most + 1, 128)
+        steps[::7] = 0
+        steps[3] = most
+        weight[128 * b:128 * (b + 1)] = np.ldexp(steps.astype(np.float64), -149).astype(np.float32)
+    q, s, v = normed(weight, carry)
+    want_q, want_s = by_division(v)
+    assert np.all(want_s[:, [1, 2, 6]] == 0) and np.all(want_s[:, 4] == np.float32(2.0 ** -149))
+    assert np.array_equal(s, want_s)
+    assert np.array_equal(q, want_q)
