@@ -242,6 +242,9 @@ struct NormArgs {
 // The quotient is the one of ep_quant.cuh, v / scale correctly rounded, with its sign turned:
 // with n = -1 / scale rounded, p = RN(v n), e = RN(p scale + v) and RN(e n + p) =
 // -RN(v / scale), zeros and their signs included, so the codes' sign bits are flipped at the end.
+// The conversion's code of any NaN is 0x7F, so it leaves as 0xFF; turning the signs before the
+// conversion instead gives 0x7F and takes longer (4096 x 7168 without a residual, E4M3 only,
+// 23.9 us instead of 23.1 us; one token 2.11 us instead of 2.06 us).
 // Scales that are not `corrected` take the division.
 // Returns the scale of the lane's vector; `leads` is set in the lane that stores it, `mine`
 // names the vector.

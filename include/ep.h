@@ -503,7 +503,8 @@ ep_status_t ep_combine_permuted_bwd(const void* dout, const void* y, const int64
  * in fp32 throughout; the norm and both outputs take the unrounded z. A block whose
  * scale rounds to 0 (amax up to 224 * 2^-149) has signed-zero codes; one with an infinite
  * amax has scale infinity, zeros for its finite values and NaN for the infinities; a NaN
- * becomes the NaN code and takes no part in amax.
+ * becomes the code 0xFF (a NaN, as 0x7F, which ep_dispatch writes, is) and takes no part in
+ * amax.
  *   x            bf16 [T][H] or NULL (z = residual)
  *   residual     stream_dtype [T][H] or NULL (z = x); x or residual is required
  *   weight       weight_dtype [H]

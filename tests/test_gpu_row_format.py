@@ -92,7 +92,7 @@ def normed(weight, carry, T=3, quarter=False):
 
 def by_division(v):
     """The stated format: scale = amax / 448, code = e4m3(v / scale), saturated; where the scale is 0
-    every value's own code; NaN takes no part in amax and becomes the code 0x7F."""
+    every value's own code; NaN takes no part in amax (its code stands as 0x7F here)."""
     blocks = v.reshape(v.shape[0], -1, 128)
     with np.errstate(invalid="ignore", over="ignore"):
         s = np.fmax.reduce(np.abs(blocks), axis=2, initial=np.float32(0)) / np.float32(448.0)
@@ -134,3 +134,20 @@ def test_norm_of_blocks_whose_scale_rounds_to_zero(carry, H):
     assert np.all(want_s[:, [1, 2, 6]] == 0) and np.all(want_s[:, 4] == np.float32(2.0 ** -149))
     assert np.array_equal(s, want_s)
     assert np.array_equal(q, want_q)
+
+
+@pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(4, 128), (4, 7168), (2000, 256), (1000, 1024)])  # a row per CTA; the ring
+def test_norm_writes_one_nan_code(carry, T, H):
+    """0xFF for a NaN of either sign; the FP8 dispatch writes 0x7F."""
+    weight = np.random.default_rng(45).uniform(0.5, 1.0, H).astype(np.float32)
+    weight[5::11], weight[7::11] = np.nan, -np.nan
+    q, s, v = normed(weight, carry, T)
+    want_q, want_s = by_division(v)
+    nan = np.isnan(v)
+    assert nan.any() and np.all(q[nan] == 0xFF)
+    assert np.array_equal(q[~nan], want_q[~nan]) and np.array_equal(s, want_s)
+    bits = np.full((2, 512), 0x3F80, np.uint16)
+    bits[0, 3], bits[1, 9] = 0x7FC0, 0xFFC0
+    codes, _ = dispatched(bits)
+    assert codes[0, 3] == 0x7F and codes[1, 9] == 0x7F
