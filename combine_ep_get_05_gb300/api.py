@@ -1,14 +1,49 @@
 """Convenience layer over the C ABI: allocate the caller-owned buffers with torch
 and chain the entry points. It adds no computation: every step still runs in
-the library's kernels (see _lib.py)."""
+the library's kernels (see _lib.py).
+
+A helper with `stream` allocates, zero-fills and frees on that stream, where its kernels run,
+and what it returns may also be used and freed on the stream that was current (once that has
+been made to wait for `stream`, as for any work there). Inputs are the caller's: they have to
+be ready on `stream` and to live until its work is done."""
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import Optional
 
 import torch
 
 from . import _lib as L
+
+
+class _On:
+    """with _On(stream) as on: `stream` is the current one (None: the current one stays).
+    on.made(m): m, a tensor or a dataclass of tensors that was allocated there and goes to the
+    caller; its memory is taken back only after the caller's stream is done with it too."""
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        if self.stream is not None:
+            s = self.stream
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(s.cuda_stream)
+            self.callers = torch.cuda.current_stream()
+            self.inside = torch.cuda.stream(s)
+            self.inside.__enter__()
+        return self
+
+    def __exit__(self, *exception):
+        if self.stream is not None:
+            self.inside.__exit__(*exception)
+
+    def made(self, m):
+        if self.stream is not None:
+            for t in [m] if isinstance(m, torch.Tensor) else [getattr(m, f.name) for f in fields(m)]:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(self.callers)
+        return m
 
 
 @dataclass
@@ -73,10 +108,12 @@ def alloc_dispatch(num_ranks: int, max_tokens: int, H: int, k: int, fp8: bool = 
 def get_layout(topk_idx: torch.Tensor, num_experts: int, num_ranks: int, ranks_per_node: int = 0,
                out: Optional[Layout] = None, stream=None) -> Layout:
     T = topk_idx.shape[0]
-    lay = out if out is not None else alloc_layout(T, num_experts, num_ranks, ranks_per_node, topk_idx.device)
-    L.ep_get_layout(topk_idx, num_experts, num_ranks, ranks_per_node, lay.tokens_per_expert, lay.tokens_per_rank,
-                    lay.tokens_per_node, lay.is_token_in_rank, lay.is_token_in_node, lay.slot, lay.workspace,
-                    lay.status, stream)
+    with _On(stream) as on:
+        lay = out if out is not None else on.made(
+            alloc_layout(T, num_experts, num_ranks, ranks_per_node, topk_idx.device))
+        L.ep_get_layout(topk_idx, num_experts, num_ranks, ranks_per_node, lay.tokens_per_expert, lay.tokens_per_rank,
+                        lay.tokens_per_node, lay.is_token_in_rank, lay.is_token_in_node, lay.slot, lay.workspace,
+                        lay.status, stream)
     return lay
 
 
@@ -84,10 +121,12 @@ def dispatch(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, layo
              fp8: bool = False, out: Optional[Dispatched] = None, stream=None) -> Dispatched:
     T, H = x.shape
     k = topk_idx.shape[1]
-    d = out if out is not None else alloc_dispatch(layout.num_ranks, max_tokens, H, k, fp8, device=x.device)
-    L.ep_dispatch(x, L.DTYPE_E4M3 if fp8 else L.DTYPE_BF16, topk_idx, topk_w, layout.slot, layout.num_experts,
-                  layout.num_ranks, max_tokens, d.recv_x, d.recv_scales, d.recv_src_idx, d.recv_topk_idx,
-                  d.recv_topk_w, d.status, stream)
+    with _On(stream) as on:
+        d = out if out is not None else on.made(
+            alloc_dispatch(layout.num_ranks, max_tokens, H, k, fp8, device=x.device))
+        L.ep_dispatch(x, L.DTYPE_E4M3 if fp8 else L.DTYPE_BF16, topk_idx, topk_w, layout.slot, layout.num_experts,
+                      layout.num_ranks, max_tokens, d.recv_x, d.recv_scales, d.recv_src_idx, d.recv_topk_idx,
+                      d.recv_topk_w, d.status, stream)
     return d
 
 
@@ -95,8 +134,9 @@ def combine(y: torch.Tensor, layout: Layout, max_tokens: int, out: Optional[torc
             status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     T = layout.slot.shape[0]
     H = y.shape[2]
-    o = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-    L.ep_combine(y, layout.slot, max_tokens, o, status, stream)
+    with _On(stream) as on:
+        o = out if out is not None else on.made(torch.empty((T, H), dtype=torch.bfloat16, device=y.device))
+        L.ep_combine(y, layout.slot, max_tokens, o, status, stream)
     return o
 
 
@@ -158,12 +198,16 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optiona
     """x + residual and its RMS norm, as bf16 rows, as E4M3 rows with 1x128 scales, or both."""
     T, H = x.shape
     dev = x.device
-    z = torch.empty_like(residual) if residual is not None else None
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None
-    q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev) if fp8 else None
-    s = torch.empty((T, H // 128), dtype=torch.float32, device=dev) if fp8 else None
-    L.ep_rmsnorm(x, residual, weight, eps, z, y, q, s, stream)
-    return Normed(z if z is not None else x, y, q, s)
+    with _On(stream) as on:
+        n = on.made(Normed(
+            residual=torch.empty_like(residual) if residual is not None else None,
+            y=torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
+            y_q=torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev) if fp8 else None,
+            y_scales=torch.empty((T, H // 128), dtype=torch.float32, device=dev) if fp8 else None))
+        L.ep_rmsnorm(x, residual, weight, eps, n.residual, n.y, n.y_q, n.y_scales, stream)
+    if n.residual is None:
+        n.residual = x
+    return n
 
 
 def rmsnorm_bwd(dy: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, eps: float,
@@ -171,22 +215,26 @@ def rmsnorm_bwd(dy: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, eps: fl
     """Gradient of rmsnorm at z = Normed.residual, with the gradient dz that arrives along the
     stream: (gradient of residual in the stream's type, gradient of x in bf16, fp32 dweight)."""
     T, H = z.shape
-    out = torch.empty_like(z)
-    dx = torch.empty((T, H), dtype=torch.bfloat16, device=z.device) if z.dtype != torch.bfloat16 else None
-    dw = torch.empty(H, dtype=torch.float32, device=z.device)
-    ws = torch.empty(L.ep_rmsnorm_bwd_workspace_size(T, H), dtype=torch.uint8, device=z.device)
-    L.ep_rmsnorm_bwd(dy, z, weight, dz, eps, out, dx, dw, ws, stream)
-    return out, dx if dx is not None else out, dw
+    with _On(stream) as on:
+        out = on.made(torch.empty_like(z))
+        dx = out
+        if z.dtype != torch.bfloat16:
+            dx = on.made(torch.empty((T, H), dtype=torch.bfloat16, device=z.device))
+        dw = on.made(torch.empty(H, dtype=torch.float32, device=z.device))
+        ws = torch.empty(L.ep_rmsnorm_bwd_workspace_size(T, H), dtype=torch.uint8, device=z.device)
+        L.ep_rmsnorm_bwd(dy, z, weight, dz, eps, out, dx if dx is not out else None, dw, ws, stream)
+    return out, dx, dw
 
 
 def get_expert_layout(topk_idx: torch.Tensor, num_experts: int, stream=None) -> ExpertLayout:
     T, k = topk_idx.shape
     dev = topk_idx.device
     i32 = dict(dtype=torch.int32, device=dev)
-    ws = torch.zeros(L.ep_expert_layout_workspace_size(T, num_experts), dtype=torch.uint8, device=dev)
-    lay = ExpertLayout(torch.empty(num_experts + 1, **i32), torch.empty((T, k), **i32), ws, torch.zeros(1, **i32),
-                       num_experts)
-    L.ep_get_expert_layout(topk_idx, num_experts, lay.offsets, lay.slot, ws, lay.status, stream)
+    with _On(stream) as on:
+        ws = torch.zeros(L.ep_expert_layout_workspace_size(T, num_experts), dtype=torch.uint8, device=dev)
+        lay = on.made(ExpertLayout(torch.empty(num_experts + 1, **i32), torch.empty((T, k), **i32), ws,
+                                   torch.zeros(1, **i32), num_experts))
+        L.ep_get_expert_layout(topk_idx, num_experts, lay.offsets, lay.slot, ws, lay.status, stream)
     return lay
 
 
@@ -208,15 +256,16 @@ def dispatch_permuted(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[
                       num_ranks: int, max_rows: int, scales: Optional[torch.Tensor] = None,
                       out: Optional[Permuted] = None, stream=None) -> Permuted:
     """Rows into expert order: bf16 rows, or E4M3 codes with their scales."""
-    p = out if out is not None else alloc_permuted(num_ranks, max_rows, x.shape[1], scales is not None,
-                                                   topk_w is not None, x.device)
-    if scales is None:
-        L.ep_dispatch_permuted(x, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, num_ranks,
-                               max_rows, p.perm_x, p.perm_src, p.perm_w, p.status, stream)
-    else:
-        L.ep_dispatch_permuted_fp8(x, scales, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts,
-                                   num_ranks, max_rows, p.perm_x, p.perm_scales, p.perm_src, p.perm_w, p.status,
-                                   stream)
+    with _On(stream) as on:
+        p = out if out is not None else on.made(
+            alloc_permuted(num_ranks, max_rows, x.shape[1], scales is not None, topk_w is not None, x.device))
+        if scales is None:
+            L.ep_dispatch_permuted(x, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, num_ranks,
+                                   max_rows, p.perm_x, p.perm_src, p.perm_w, p.status, stream)
+        else:
+            L.ep_dispatch_permuted_fp8(x, scales, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts,
+                                       num_ranks, max_rows, p.perm_x, p.perm_scales, p.perm_src, p.perm_w, p.status,
+                                       stream)
     return p
 
 
@@ -225,26 +274,31 @@ def dispatch_permuted_bwd(dperm_x: torch.Tensor, topk_idx: torch.Tensor, layout:
                           status: Optional[torch.Tensor] = None, stream=None):
     """Gradient of dispatch_permuted, added to `dx` (another gradient of x) where given: (dx, dtopk_w or None)."""
     T, k = topk_idx.shape
-    out = torch.empty((T, dperm_x.shape[2]), dtype=torch.bfloat16, device=dperm_x.device)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dperm_x.device) if dperm_w is not None else None
-    L.ep_dispatch_permuted_bwd(dperm_x, dperm_w, dx, topk_idx, layout.offsets, layout.slot, layout.num_experts, out,
-                               dw, status, stream)
+    dev = dperm_x.device
+    with _On(stream) as on:
+        out = on.made(torch.empty((T, dperm_x.shape[2]), dtype=torch.bfloat16, device=dev))
+        dw = on.made(torch.empty((T, k), dtype=torch.float32, device=dev)) if dperm_w is not None else None
+        L.ep_dispatch_permuted_bwd(dperm_x, dperm_w, dx, topk_idx, layout.offsets, layout.slot, layout.num_experts,
+                                   out, dw, status, stream)
     return out, dw
 
 
 def combine_permuted(y: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[torch.Tensor], layout: ExpertLayout,
                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows back to token order, weighted where topk_w is given."""
-    out = torch.empty((topk_idx.shape[0], y.shape[2]), dtype=torch.bfloat16, device=y.device)
-    L.ep_combine_permuted(y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, out, status, stream)
+    with _On(stream) as on:
+        out = on.made(torch.empty((topk_idx.shape[0], y.shape[2]), dtype=torch.bfloat16, device=y.device))
+        L.ep_combine_permuted(y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, out, status,
+                              stream)
     return out
 
 
 def combine_permuted_bwd(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                          layout: ExpertLayout, status: Optional[torch.Tensor] = None, stream=None):
     """Gradient of the weighted combine_permuted: (dy with zeros in rows that hold no entry, dtopk_w)."""
-    dy = torch.zeros_like(y)
-    dw = torch.empty_like(topk_w)
-    L.ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, dy, dw,
-                              status, stream)
+    with _On(stream) as on:
+        dy = on.made(torch.zeros_like(y))
+        dw = on.made(torch.empty_like(topk_w))
+        L.ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, dy, dw,
+                                  status, stream)
     return dy, dw
