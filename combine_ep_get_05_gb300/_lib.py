@@ -1,7 +1,7 @@
 """Binding of libep_gb300.so (include/ep.h) by ctypes and, for its shortest calls, by the
 compiled module of csrc/ep_binding.cpp: argument marshalling only.
 
-Every function takes torch tensors, checks their device, dtype, shape and
+Every function takes torch tensors, checks their device (the current one), dtype, shape and
 contiguity, passes raw device pointers and the current (or given) CUDA stream
 to the C entry point of the same name, and raises ``EpError`` on a non-OK
 synchronous status. All work happens in the library's CUDA kernels; there is
@@ -138,13 +138,22 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_g
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+_only_device = False  # set once CUDA is known to show this process one device
+
+
+def _on_current_device(t):
+    global _only_device
+    _only_device = torch.cuda.device_count() == 1
+    return t.get_device() == torch.cuda.current_device()
+
+
 def _stream(stream):
     return _raw_current_stream() if stream is None else stream.cuda_stream
 
 
 def _check(name, t, dtype, shape=None, optional=False):
-    if (t is not None and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape)
-            and t.is_contiguous()):
+    if (t is not None and t.dtype is dtype and t.is_cuda and (_only_device or _on_current_device(t))
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
     if t is None:
         if optional:
@@ -152,6 +161,9 @@ def _check(name, t, dtype, shape=None, optional=False):
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if not (_only_device or _on_current_device(t)):  # kernels are launched on the current device
+        raise ValueError(f"{name} must be on the current device, cuda:{torch.cuda.current_device()}, "
+                         f"got cuda:{t.get_device()}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():

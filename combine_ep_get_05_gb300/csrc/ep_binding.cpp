@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -85,8 +86,15 @@ int32_t integer(PyObject* o, const char* name) {
     return static_cast<int32_t>(v);
 }
 
+// the device that the call of this thread launches on, asked for once a call
+thread_local int t_device = -1;
+
 void* address(const at::Tensor& t, const char* name, at::ScalarType dtype, Shape shape) {
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    if (t.get_device() != t_device)
+        refuse("%s must be on the current device, cuda:%d, got cuda:%d", name, t_device,
+               static_cast<int>(t.get_device()));
     if (t.scalar_type() != dtype)
         refuse("%s must be %s, got %s", name, dtype_name(dtype).c_str(), dtype_name(t.scalar_type()).c_str());
     if (!t.is_contiguous()) refuse("%s must be contiguous", name);
@@ -291,6 +299,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", kArgs, n);
         return nullptr;
     }
+    t_device = -1;
     try {
         return PyLong_FromLong(kCall(args));
     } catch (const Refused&) {
