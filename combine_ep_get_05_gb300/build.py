@@ -103,20 +103,20 @@ def build(force: bool = False, ptxas_info: bool = False, jobs: int | None = None
 
     with ThreadPoolExecutor(max_workers=jobs or min(8, os.cpu_count() or 1)) as pool:
         binding = pool.submit(_build_binding) if force or _binding_is_stale() else None
-        results = list(pool.map(compile_one, sources())) if force or ptxas_info or _library_is_stale() else []
+        if force or ptxas_info or _library_is_stale():
+            results = list(pool.map(compile_one, sources()))
+            if ptxas_info:
+                with open(os.path.join(BUILD_DIR, "ptxas.txt"), "w") as f:
+                    for obj, log in results:
+                        f.write(f"== {os.path.basename(obj)}\n{log}\n")
+            tmp = LIB_PATH + f".tmp{os.getpid()}"
+            proc = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]], capture_output=True,
+                                  text=True)
+            if proc.returncode != 0:
+                raise RuntimeError(f"nvcc link failed:\n{proc.stdout}\n{proc.stderr}")
+            os.replace(tmp, LIB_PATH)
         if binding is not None:
-            binding.result()
-    if not results:
-        return LIB_PATH
-    if ptxas_info:
-        with open(os.path.join(BUILD_DIR, "ptxas.txt"), "w") as f:
-            for obj, log in results:
-                f.write(f"== {os.path.basename(obj)}\n{log}\n")
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    proc = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]], capture_output=True, text=True)
-    if proc.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{proc.stdout}\n{proc.stderr}")
-    os.replace(tmp, LIB_PATH)
+            binding.result()  # what fails here leaves the library, which does not need it, in place
     return LIB_PATH
 
 
