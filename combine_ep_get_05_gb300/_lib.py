@@ -17,7 +17,7 @@ import threading
 
 import torch
 
-from .build import BINDING_PATH, LIB_PATH
+from .build import BINDING_PATH, LIB_PATH, check_binding
 
 EP_OK = 0
 EP_ERR_INVALID = 1
@@ -469,10 +469,7 @@ def _native():
         L = lib()
         with _lock:
             if _binding is None:
-                if not os.path.exists(BINDING_PATH):
-                    raise RuntimeError(
-                        f"{BINDING_PATH} is missing: build it first "
-                        "(python -m combine_ep_get_05_gb300.build or __graft_entry__.build())")
+                check_binding()
                 loader = importlib.machinery.ExtensionFileLoader("_ep_binding", BINDING_PATH)
                 spec = importlib.util.spec_from_file_location("_ep_binding", BINDING_PATH, loader=loader)
                 module = importlib.util.module_from_spec(spec)

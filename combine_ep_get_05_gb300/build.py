@@ -9,6 +9,7 @@ by the host compiler against the installed torch.
 """
 from __future__ import annotations
 
+import contextlib
 import glob
 import os
 import shutil
@@ -55,7 +56,33 @@ def _library_is_stale() -> bool:
 
 
 def _binding_is_stale() -> bool:
-    return _older(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "ep.h")])
+    return _older(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "ep.h")]) or binding_built_for() != _installed()
+
+
+def _installed() -> str:
+    """The interpreter and the torch whose C++ interfaces a binding is compiled against."""
+    import torch
+
+    return f"{sysconfig.get_config_var('EXT_SUFFIX')} torch {torch.__version__} {torch.version.git_version}"
+
+
+def binding_built_for() -> str:
+    """What _installed() was when the binding was compiled, "" if that is not known."""
+    try:
+        with open(BINDING_PATH + ".for") as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
+
+
+def check_binding() -> None:
+    """Raises unless the binding that is there was built, and for this interpreter and this torch."""
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is missing: build it first "
+                           "(python -m combine_ep_get_05_gb300.build or __graft_entry__.build())")
+    if binding_built_for() != _installed():
+        raise RuntimeError(f"{BINDING_PATH} was built for [{binding_built_for()}] and this is [{_installed()}]: build it "
+                           "again (python -m combine_ep_get_05_gb300.build)")
 
 
 def is_stale() -> bool:
@@ -83,7 +110,11 @@ def _build_binding() -> None:
     proc = subprocess.run(cmd, capture_output=True, text=True)
     if proc.returncode != 0:
         raise RuntimeError(f"{host_compiler()} failed on {BINDING_SRC}:\n{proc.stdout}\n{proc.stderr}")
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(BINDING_PATH + ".for")  # whatever happens next, the old origin does not stay with the new file
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_PATH + ".for", "w") as f:
+        f.write(_installed())
 
 
 def build(force: bool = False, ptxas_info: bool = False, jobs: int | None = None) -> str:

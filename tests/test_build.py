@@ -25,3 +25,36 @@ def test_a_binding_that_does_not_compile_leaves_the_library(elsewhere, monkeypat
         build.build()
     assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
     assert build.is_stale() and not build._library_is_stale()
+
+
+def test_a_binding_of_another_torch_or_python_is_stale_and_not_loaded(monkeypatch):
+    from combine_ep_get_05_gb300 import _lib
+
+    build.build()
+    assert not build.is_stale()
+    _lib._native()
+    monkeypatch.setattr(_lib, "_binding", None)
+    for attribute, value in (("__version__", "1.0.0"), ("version.git_version", "0" * 40)):
+        with monkeypatch.context() as m:
+            m.setattr(f"torch.{attribute}", value)
+            assert build.is_stale() and not build._library_is_stale()
+            with pytest.raises(RuntimeError, match="was built for .* and this is .*build it again"):
+                _lib._native()
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_config_var", lambda name: ".cpython-399.so")
+        assert build.is_stale()
+        with pytest.raises(RuntimeError, match="build it again"):
+            _lib._native()
+    _lib._native()
+
+
+def test_a_binding_whose_origin_is_unknown_is_stale(elsewhere):
+    with open(build.BINDING_PATH, "w"):
+        pass
+    assert build._binding_is_stale()
+    with open(build.BINDING_PATH + ".for", "w") as f:
+        f.write(build._installed())
+    assert not build._binding_is_stale()
+    os.remove(build.BINDING_PATH)
+    with pytest.raises(RuntimeError, match="missing"):
+        build.check_binding()
