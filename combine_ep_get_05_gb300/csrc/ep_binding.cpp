@@ -168,6 +168,16 @@ ep_status_t bind(PyObject* const* a) {
     return EP_OK;
 }
 
+// The library's call itself, with other Python threads let through: a launch waits while the
+// stream's queue is full. Its arguments are C values by then; `launch` touches no Python object.
+template <typename Launch>
+ep_status_t launched(Launch launch) {
+    PyThreadState* const state = PyEval_SaveThread();
+    const ep_status_t status = launch();
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // the residual stream's type, that of `t`; bf16 where there is no stream
 at::ScalarType stream_type(const at::Tensor* t) {
     const at::ScalarType type = t == nullptr ? at::kBFloat16 : t->scalar_type();
@@ -203,8 +213,12 @@ ep_status_t rmsnorm(PyObject* const* a) {
     } else {
         ps = address_or_null(a[7], "y_scales", at::kFloat, {T, H / 128});
     }
-    return g_ep.rmsnorm(px, pr, pw, ep_type(type), ep_type(wtype), number(a[3]), T, H, po, py, as<uint8_t>(pq),
-                        as<float>(ps), stream_of(a[8]));
+    const float eps = number(a[3]);
+    void* const stream = stream_of(a[8]);
+    return launched([&] {
+        return g_ep.rmsnorm(px, pr, pw, ep_type(type), ep_type(wtype), eps, T, H, po, py, as<uint8_t>(pq),
+                            as<float>(ps), stream);
+    });
 }
 
 // dy, z, weight, dz_in, eps, dz, dx, dweight, workspace, stream
@@ -224,8 +238,12 @@ ep_status_t rmsnorm_bwd(PyObject* const* a) {
     const at::Tensor* ws = pdw != nullptr ? &required(a[8], "workspace") : tensor_of(a[8], "workspace");
     const int64_t bytes = ws == nullptr ? 0 : ws->numel();
     void* const pws = ws == nullptr ? nullptr : address(*ws, "workspace", at::kByte, {bytes});
-    return g_ep.rmsnorm_bwd(pdy, pz, pw, pin, ep_type(type), ep_type(wtype), number(a[4]), T, H, pdz, pdx,
-                            as<float>(pdw), pws, static_cast<size_t>(bytes), stream_of(a[9]));
+    const float eps = number(a[4]);
+    void* const stream = stream_of(a[9]);
+    return launched([&] {
+        return g_ep.rmsnorm_bwd(pdy, pz, pw, pin, ep_type(type), ep_type(wtype), eps, T, H, pdz, pdx, as<float>(pdw),
+                                pws, static_cast<size_t>(bytes), stream);
+    });
 }
 
 // x_q, x_scales, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, num_ranks, max_rows,
@@ -247,10 +265,13 @@ ep_status_t sort_fp8(PyObject* const* a, bool one_launch) {
     auto* const pw = as<float>(address_or_null(a[12], "perm_w", at::kFloat, {R, M}));
     auto* const status = as<int32_t>(address_or_null(a[13], "status", at::kInt, {1}));
     void* const stream = stream_of(a[14]);
-    if (one_launch)
-        return g_ep.dispatch_permuted_fp8_ll(pq, ps, idx, w, T, H, k, E, R, M, off, slot, oq, os, src, pw, status,
-                                             stream);
-    return g_ep.dispatch_permuted_fp8(pq, ps, idx, w, off, slot, T, H, k, E, R, M, oq, os, src, pw, status, stream);
+    return launched([&] {
+        if (one_launch)
+            return g_ep.dispatch_permuted_fp8_ll(pq, ps, idx, w, T, H, k, E, R, M, off, slot, oq, os, src, pw, status,
+                                                 stream);
+        return g_ep.dispatch_permuted_fp8(pq, ps, idx, w, off, slot, T, H, k, E, R, M, oq, os, src, pw, status,
+                                          stream);
+    });
 }
 
 ep_status_t dispatch_permuted_fp8(PyObject* const* a) { return sort_fp8(a, false); }
@@ -271,7 +292,10 @@ ep_status_t dispatch_permuted_bwd(PyObject* const* a) {
     void* const dx = address(a[7], "dx", at::kBFloat16, {T, H});
     auto* const dw = as<float>(address_or_null(a[8], "dtopk_w", at::kFloat, {T, k}));
     auto* const status = as<int32_t>(address_or_null(a[9], "status", at::kInt, {1}));
-    return g_ep.dispatch_permuted_bwd(pd, pw, in, idx, off, slot, T, H, k, E, R, M, dx, dw, status, stream_of(a[10]));
+    void* const stream = stream_of(a[10]);
+    return launched([&] {
+        return g_ep.dispatch_permuted_bwd(pd, pw, in, idx, off, slot, T, H, k, E, R, M, dx, dw, status, stream);
+    });
 }
 
 // dout, y, topk_idx, topk_w, expert_offsets, expert_slot, num_experts, dy, dtopk_w, status, stream
@@ -289,7 +313,10 @@ ep_status_t combine_permuted_bwd(PyObject* const* a) {
     void* const dy = address(d, "dy", at::kBFloat16, {R, M, H});
     auto* const dw = as<float>(address_or_null(a[8], "dtopk_w", at::kFloat, {T, k}));
     auto* const status = as<int32_t>(address_or_null(a[9], "status", at::kInt, {1}));
-    return g_ep.combine_permuted_bwd(dout, y, idx, w, off, slot, T, H, k, E, R, M, dy, dw, status, stream_of(a[10]));
+    void* const stream = stream_of(a[10]);
+    return launched([&] {
+        return g_ep.combine_permuted_bwd(dout, y, idx, w, off, slot, T, H, k, E, R, M, dy, dw, status, stream);
+    });
 }
 
 // A call: the number of arguments, then the function; no C++ exception leaves it.
