@@ -89,7 +89,7 @@ int32_t integer(PyObject* o, const char* name) {
 // the device that the call of this thread launches on, asked for once a call
 thread_local int t_device = -1;
 
-void* address(const at::Tensor& t, const char* name, at::ScalarType dtype, Shape shape) {
+void check(const at::Tensor& t, const char* name, at::ScalarType dtype, Shape shape) {
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
     if (t_device < 0) t_device = c10::cuda::current_device();
     if (t.get_device() != t_device)
@@ -101,22 +101,41 @@ void* address(const at::Tensor& t, const char* name, at::ScalarType dtype, Shape
     const c10::IntArrayRef want(shape.begin(), shape.size());
     if (t.sizes() != want)
         refuse("%s must have shape %s, got %s", name, shape_name(want).c_str(), shape_name(t.sizes()).c_str());
+}
+
+// The address of a tensor that the call reads, or writes: asking to write copies the
+// memory of a lazily cloned tensor, asking to read does not.
+const void* reads(const at::Tensor& t, const char* name, at::ScalarType dtype, Shape shape) {
+    check(t, name, dtype, shape);
+    return t.const_data_ptr();
+}
+
+const void* reads(PyObject* o, const char* name, at::ScalarType dtype, Shape shape) {
+    return reads(required(o, name), name, dtype, shape);
+}
+
+const void* reads_or_null(PyObject* o, const char* name, at::ScalarType dtype, Shape shape) {
+    const at::Tensor* t = tensor_of(o, name);
+    return t == nullptr ? nullptr : reads(*t, name, dtype, shape);
+}
+
+void* writes(const at::Tensor& t, const char* name, at::ScalarType dtype, Shape shape) {
+    check(t, name, dtype, shape);
     return t.mutable_data_ptr();
 }
 
-void* address(PyObject* o, const char* name, at::ScalarType dtype, Shape shape) {
-    return address(required(o, name), name, dtype, shape);
+void* writes(PyObject* o, const char* name, at::ScalarType dtype, Shape shape) {
+    return writes(required(o, name), name, dtype, shape);
 }
 
-void* address_or_null(PyObject* o, const char* name, at::ScalarType dtype, Shape shape) {
+void* writes_or_null(PyObject* o, const char* name, at::ScalarType dtype, Shape shape) {
     const at::Tensor* t = tensor_of(o, name);
-    return t == nullptr ? nullptr : address(*t, name, dtype, shape);
+    return t == nullptr ? nullptr : writes(*t, name, dtype, shape);
 }
 
-// E4M3 codes: bytes, or torch's own type
-void* codes(PyObject* o, const char* name, Shape shape) {
-    const at::Tensor& t = required(o, name);
-    return address(t, name, t.scalar_type() == at::kFloat8_e4m3fn ? at::kFloat8_e4m3fn : at::kByte, shape);
+// the type of E4M3 codes: bytes, or torch's own
+at::ScalarType code_type(PyObject* o, const char* name) {
+    return required(o, name).scalar_type() == at::kFloat8_e4m3fn ? at::kFloat8_e4m3fn : at::kByte;
 }
 
 void* stream_of(PyObject* o) {
@@ -138,6 +157,11 @@ float number(PyObject* o) {
 template <typename T>
 T* as(void* p) {
     return static_cast<T*>(p);
+}
+
+template <typename T>
+const T* as(const void* p) {
+    return static_cast<const T*>(p);
 }
 
 // the library's entry points
@@ -199,19 +223,19 @@ ep_status_t rmsnorm(PyObject* const* a) {
     if (out != nullptr && out->scalar_type() != type)
         refuse("the residual stream must be of one type, got %s and %s", dtype_name(type).c_str(),
                dtype_name(out->scalar_type()).c_str());
-    void* const px = address_or_null(a[0], "x", at::kBFloat16, {T, H});
-    void* const pr = address_or_null(a[1], "residual", type, {T, H});
+    const void* const px = reads_or_null(a[0], "x", at::kBFloat16, {T, H});
+    const void* const pr = reads_or_null(a[1], "residual", type, {T, H});
     const at::Tensor& w = required(a[2], "weight");
     const at::ScalarType wtype = w.scalar_type() == at::kFloat ? at::kFloat : at::kBFloat16;
-    void* const pw = address(w, "weight", wtype, {H});
-    void* const po = address_or_null(a[4], "residual_out", type, {T, H});
-    void* const py = address_or_null(a[5], "y", at::kBFloat16, {T, H});
+    const void* const pw = reads(w, "weight", wtype, {H});
+    void* const po = writes_or_null(a[4], "residual_out", type, {T, H});
+    void* const py = writes_or_null(a[5], "y", at::kBFloat16, {T, H});
     void *pq = nullptr, *ps = nullptr;
     if (a[6] != Py_None) {
-        pq = codes(a[6], "y_q", {T, H});
-        ps = address(a[7], "y_scales", at::kFloat, {T, H / 128});
+        pq = writes(a[6], "y_q", code_type(a[6], "y_q"), {T, H});
+        ps = writes(a[7], "y_scales", at::kFloat, {T, H / 128});
     } else {
-        ps = address_or_null(a[7], "y_scales", at::kFloat, {T, H / 128});
+        ps = writes_or_null(a[7], "y_scales", at::kFloat, {T, H / 128});
     }
     const float eps = number(a[3]);
     void* const stream = stream_of(a[8]);
@@ -226,18 +250,18 @@ ep_status_t rmsnorm_bwd(PyObject* const* a) {
     const at::Tensor& z = required(a[1], "z");
     const int32_t T = dim(z, "z", 2, 0), H = dim(z, "z", 2, 1);
     const at::ScalarType type = stream_type(&z);
-    void* const pdy = address(a[0], "dy", at::kBFloat16, {T, H});
-    void* const pz = address(z, "z", type, {T, H});
+    const void* const pdy = reads(a[0], "dy", at::kBFloat16, {T, H});
+    const void* const pz = reads(z, "z", type, {T, H});
     const at::Tensor& w = required(a[2], "weight");
     const at::ScalarType wtype = w.scalar_type() == at::kFloat ? at::kFloat : at::kBFloat16;
-    void* const pw = address(w, "weight", wtype, {H});
-    void* const pin = address_or_null(a[3], "dz_in", type, {T, H});
-    void* const pdz = address(a[5], "dz", type, {T, H});
-    void* const pdx = address_or_null(a[6], "dx", at::kBFloat16, {T, H});
-    void* const pdw = address_or_null(a[7], "dweight", at::kFloat, {H});
+    const void* const pw = reads(w, "weight", wtype, {H});
+    const void* const pin = reads_or_null(a[3], "dz_in", type, {T, H});
+    void* const pdz = writes(a[5], "dz", type, {T, H});
+    void* const pdx = writes_or_null(a[6], "dx", at::kBFloat16, {T, H});
+    void* const pdw = writes_or_null(a[7], "dweight", at::kFloat, {H});
     const at::Tensor* ws = pdw != nullptr ? &required(a[8], "workspace") : tensor_of(a[8], "workspace");
     const int64_t bytes = ws == nullptr ? 0 : ws->numel();
-    void* const pws = ws == nullptr ? nullptr : address(*ws, "workspace", at::kByte, {bytes});
+    void* const pws = ws == nullptr ? nullptr : writes(*ws, "workspace", at::kByte, {bytes});
     const float eps = number(a[4]);
     void* const stream = stream_of(a[9]);
     return launched([&] {
@@ -253,22 +277,30 @@ ep_status_t sort_fp8(PyObject* const* a, bool one_launch) {
     const int32_t T = dim(q, "x_q", 2, 0), H = dim(q, "x_q", 2, 1);
     const int32_t k = dim(required(a[2], "topk_idx"), "topk_idx", 2, 1);
     const int32_t E = integer(a[6], "num_experts"), R = integer(a[7], "num_ranks"), M = integer(a[8], "max_rows");
-    auto* const pq = as<uint8_t>(codes(a[0], "x_q", {T, H}));
-    auto* const ps = as<float>(address(a[1], "x_scales", at::kFloat, {T, H / 128}));
-    auto* const idx = as<int64_t>(address(a[2], "topk_idx", at::kLong, {T, k}));
-    auto* const w = as<float>(address_or_null(a[3], "topk_w", at::kFloat, {T, k}));
-    auto* const off = as<int32_t>(address(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
-    auto* const slot = as<int32_t>(address(a[5], "expert_slot", at::kInt, {T, k}));
-    auto* const oq = as<uint8_t>(codes(a[9], "perm_q", {R, M, H}));
-    auto* const os = as<float>(address(a[10], "perm_scales", at::kFloat, {R, M, H / 128}));
-    auto* const src = as<int32_t>(address_or_null(a[11], "perm_src", at::kInt, {R, M}));
-    auto* const pw = as<float>(address_or_null(a[12], "perm_w", at::kFloat, {R, M}));
-    auto* const status = as<int32_t>(address_or_null(a[13], "status", at::kInt, {1}));
+    auto* const pq = as<uint8_t>(reads(a[0], "x_q", code_type(a[0], "x_q"), {T, H}));
+    auto* const ps = as<float>(reads(a[1], "x_scales", at::kFloat, {T, H / 128}));
+    auto* const idx = as<int64_t>(reads(a[2], "topk_idx", at::kLong, {T, k}));
+    auto* const w = as<float>(reads_or_null(a[3], "topk_w", at::kFloat, {T, k}));
+    // the layout: written by the one-launch form, read by the other
+    const int32_t *off = nullptr, *slot = nullptr;
+    int32_t *off_out = nullptr, *slot_out = nullptr;
+    if (one_launch) {
+        off_out = as<int32_t>(writes(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
+        slot_out = as<int32_t>(writes(a[5], "expert_slot", at::kInt, {T, k}));
+    } else {
+        off = as<int32_t>(reads(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
+        slot = as<int32_t>(reads(a[5], "expert_slot", at::kInt, {T, k}));
+    }
+    auto* const oq = as<uint8_t>(writes(a[9], "perm_q", code_type(a[9], "perm_q"), {R, M, H}));
+    auto* const os = as<float>(writes(a[10], "perm_scales", at::kFloat, {R, M, H / 128}));
+    auto* const src = as<int32_t>(writes_or_null(a[11], "perm_src", at::kInt, {R, M}));
+    auto* const pw = as<float>(writes_or_null(a[12], "perm_w", at::kFloat, {R, M}));
+    auto* const status = as<int32_t>(writes_or_null(a[13], "status", at::kInt, {1}));
     void* const stream = stream_of(a[14]);
     return launched([&] {
         if (one_launch)
-            return g_ep.dispatch_permuted_fp8_ll(pq, ps, idx, w, T, H, k, E, R, M, off, slot, oq, os, src, pw, status,
-                                                 stream);
+            return g_ep.dispatch_permuted_fp8_ll(pq, ps, idx, w, T, H, k, E, R, M, off_out, slot_out, oq, os, src, pw,
+                                                 status, stream);
         return g_ep.dispatch_permuted_fp8(pq, ps, idx, w, off, slot, T, H, k, E, R, M, oq, os, src, pw, status,
                                           stream);
     });
@@ -282,19 +314,19 @@ ep_status_t dispatch_permuted_bwd(PyObject* const* a) {
     const at::Tensor &d = required(a[0], "dperm_x"), &ids = required(a[3], "topk_idx");
     const int32_t R = dim(d, "dperm_x", 3, 0), M = dim(d, "dperm_x", 3, 1), H = dim(d, "dperm_x", 3, 2);
     const int32_t T = dim(ids, "topk_idx", 2, 0), k = dim(ids, "topk_idx", 2, 1), E = integer(a[6], "num_experts");
-    void* const pd = address(d, "dperm_x", at::kBFloat16, {R, M, H});
-    auto* const pw = as<float>(a[8] != Py_None ? address(a[1], "dperm_w", at::kFloat, {R, M})
-                                               : address_or_null(a[1], "dperm_w", at::kFloat, {R, M}));
-    void* const in = address_or_null(a[2], "dx_in", at::kBFloat16, {T, H});
-    auto* const idx = as<int64_t>(address(ids, "topk_idx", at::kLong, {T, k}));
-    auto* const off = as<int32_t>(address(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
-    auto* const slot = as<int32_t>(address(a[5], "expert_slot", at::kInt, {T, k}));
-    void* const dx = address(a[7], "dx", at::kBFloat16, {T, H});
-    auto* const dw = as<float>(address_or_null(a[8], "dtopk_w", at::kFloat, {T, k}));
-    auto* const status = as<int32_t>(address_or_null(a[9], "status", at::kInt, {1}));
+    const void* const pd = reads(d, "dperm_x", at::kBFloat16, {R, M, H});
+    auto* const pw = as<float>(a[8] != Py_None ? reads(a[1], "dperm_w", at::kFloat, {R, M})
+                                               : reads_or_null(a[1], "dperm_w", at::kFloat, {R, M}));
+    const void* const add = reads_or_null(a[2], "dx_in", at::kBFloat16, {T, H});
+    auto* const idx = as<int64_t>(reads(ids, "topk_idx", at::kLong, {T, k}));
+    auto* const off = as<int32_t>(reads(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
+    auto* const slot = as<int32_t>(reads(a[5], "expert_slot", at::kInt, {T, k}));
+    void* const dx = writes(a[7], "dx", at::kBFloat16, {T, H});
+    auto* const dw = as<float>(writes_or_null(a[8], "dtopk_w", at::kFloat, {T, k}));
+    auto* const status = as<int32_t>(writes_or_null(a[9], "status", at::kInt, {1}));
     void* const stream = stream_of(a[10]);
     return launched([&] {
-        return g_ep.dispatch_permuted_bwd(pd, pw, in, idx, off, slot, T, H, k, E, R, M, dx, dw, status, stream);
+        return g_ep.dispatch_permuted_bwd(pd, pw, add, idx, off, slot, T, H, k, E, R, M, dx, dw, status, stream);
     });
 }
 
@@ -303,16 +335,16 @@ ep_status_t combine_permuted_bwd(PyObject* const* a) {
     const at::Tensor &d = required(a[7], "dy"), &ids = required(a[2], "topk_idx");
     const int32_t R = dim(d, "dy", 3, 0), M = dim(d, "dy", 3, 1), H = dim(d, "dy", 3, 2);
     const int32_t T = dim(ids, "topk_idx", 2, 0), k = dim(ids, "topk_idx", 2, 1), E = integer(a[6], "num_experts");
-    void* const dout = address(a[0], "dout", at::kBFloat16, {T, H});
-    void* const y = a[8] != Py_None ? address(a[1], "y", at::kBFloat16, {R, M, H})
-                                    : address_or_null(a[1], "y", at::kBFloat16, {R, M, H});
-    auto* const idx = as<int64_t>(address(ids, "topk_idx", at::kLong, {T, k}));
-    auto* const w = as<float>(address_or_null(a[3], "topk_w", at::kFloat, {T, k}));
-    auto* const off = as<int32_t>(address(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
-    auto* const slot = as<int32_t>(address(a[5], "expert_slot", at::kInt, {T, k}));
-    void* const dy = address(d, "dy", at::kBFloat16, {R, M, H});
-    auto* const dw = as<float>(address_or_null(a[8], "dtopk_w", at::kFloat, {T, k}));
-    auto* const status = as<int32_t>(address_or_null(a[9], "status", at::kInt, {1}));
+    const void* const dout = reads(a[0], "dout", at::kBFloat16, {T, H});
+    const void* const y = a[8] != Py_None ? reads(a[1], "y", at::kBFloat16, {R, M, H})
+                                          : reads_or_null(a[1], "y", at::kBFloat16, {R, M, H});
+    auto* const idx = as<int64_t>(reads(ids, "topk_idx", at::kLong, {T, k}));
+    auto* const w = as<float>(reads_or_null(a[3], "topk_w", at::kFloat, {T, k}));
+    auto* const off = as<int32_t>(reads(a[4], "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
+    auto* const slot = as<int32_t>(reads(a[5], "expert_slot", at::kInt, {T, k}));
+    void* const dy = writes(d, "dy", at::kBFloat16, {R, M, H});
+    auto* const dw = as<float>(writes_or_null(a[8], "dtopk_w", at::kFloat, {T, k}));
+    auto* const status = as<int32_t>(writes_or_null(a[9], "status", at::kInt, {1}));
     void* const stream = stream_of(a[10]);
     return launched([&] {
         return g_ep.combine_permuted_bwd(dout, y, idx, w, off, slot, T, H, k, E, R, M, dy, dw, status, stream);

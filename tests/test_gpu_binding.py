@@ -57,3 +57,22 @@ def test_other_python_threads_run_during_a_call(tmp_path):
     for f, args in calls.items():
         f(**args)
     torch.cuda.synchronize()
+
+
+INPUTS = {"ep_rmsnorm": {"x", "residual", "weight"}, "ep_rmsnorm_bwd": {"dy", "z", "weight", "dz_in"},
+          "ep_dispatch_permuted_fp8": {"x_q", "x_scales", "topk_idx", "topk_w", "expert_offsets", "expert_slot"},
+          "ep_dispatch_permuted_fp8_ll": {"x_q", "x_scales", "topk_idx", "topk_w"},
+          "ep_dispatch_permuted_bwd": {"dperm_x", "dperm_w", "dx_in", "topk_idx", "expert_offsets", "expert_slot"},
+          "ep_combine_permuted_bwd": {"dout", "y", "topk_idx", "topk_w", "expert_offsets", "expert_slot"}}
+
+
+def test_inputs_that_are_lazy_clones_stay_so():
+    """A call only reads its inputs, so none of them gets memory of its own; outputs do."""
+    for f, args in arguments().items():
+        f(**args)
+        cloned = {n: torch._lazy_clone(v) if isinstance(v, torch.Tensor) else v for n, v in args.items()}
+        tensors = {n for n, v in cloned.items() if isinstance(v, torch.Tensor)}
+        assert all(torch._C._is_cow_tensor(cloned[n]) for n in tensors)
+        f(**cloned)
+        torch.cuda.synchronize()
+        assert {n for n in tensors if torch._C._is_cow_tensor(cloned[n])} == INPUTS[f.__name__]
