@@ -293,12 +293,12 @@ def combine_permuted(y: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[t
     return out
 
 
-def combine_permuted_bwd(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+def combine_permuted_bwd(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[torch.Tensor],
                          layout: ExpertLayout, status: Optional[torch.Tensor] = None, stream=None):
-    """Gradient of the weighted combine_permuted: (dy with zeros in rows that hold no entry, dtopk_w)."""
+    """Gradient of combine_permuted: (dy with zeros in rows that hold no entry, dtopk_w or None where unweighted)."""
     with _On(stream) as on:
         dy = on.made(torch.zeros_like(y))
-        dw = on.made(torch.empty_like(topk_w))
+        dw = on.made(torch.empty_like(topk_w)) if topk_w is not None else None
         L.ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, dy, dw,
                                   status, stream)
     return dy, dw
