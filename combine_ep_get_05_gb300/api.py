@@ -187,26 +187,30 @@ class Permuted:
 
 @dataclass
 class Normed:
-    residual: torch.Tensor                # x + residual (x itself where there is none)
+    residual: torch.Tensor                # x + residual (the one of them that there is, itself)
     y: Optional[torch.Tensor]             # bf16 [T][H]
     y_q: Optional[torch.Tensor]           # float8_e4m3fn [T][H]
     y_scales: Optional[torch.Tensor]      # fp32 [T][H/128]
 
 
-def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+def rmsnorm(x: Optional[torch.Tensor], weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
             bf16: bool = True, fp8: bool = False, stream=None) -> Normed:
-    """x + residual and its RMS norm, as bf16 rows, as E4M3 rows with 1x128 scales, or both."""
-    T, H = x.shape
-    dev = x.device
+    """x + residual (either may be None, not both) and its RMS norm, as bf16 rows, as E4M3 rows with 1x128
+    scales, or both."""
+    given = x if x is not None else residual
+    if given is None:
+        raise ValueError("x or residual is required")
+    T, H = given.shape
+    dev = given.device
     with _On(stream) as on:
         n = on.made(Normed(
-            residual=torch.empty_like(residual) if residual is not None else None,
+            residual=torch.empty_like(residual) if x is not None and residual is not None else None,
             y=torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
             y_q=torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev) if fp8 else None,
             y_scales=torch.empty((T, H // 128), dtype=torch.float32, device=dev) if fp8 else None))
         L.ep_rmsnorm(x, residual, weight, eps, n.residual, n.y, n.y_q, n.y_scales, stream)
     if n.residual is None:
-        n.residual = x
+        n.residual = given
     return n
 
 

@@ -41,3 +41,16 @@ def test_gradient_of_the_unweighted_return():
     weighted, dw = ep.combine_permuted_bwd(dout, y, idx, torch.ones((T, k), device="cuda"), lay)
     assert torch.equal(weighted, dy) and dw.shape == (T, k)
     assert torch.equal(ep.dispatch_permuted_bwd(dy, idx, lay)[0], ep.combine_permuted(dy, idx, None, lay))
+
+
+@pytest.mark.parametrize("carry", [torch.bfloat16, torch.float32])
+def test_norm_of_the_stream_alone(carry):
+    """A norm without an addition in front of it (a model's last one): the stream goes in as it is."""
+    stream, weight = rand((T, 1024), 55, carry), rand((1024,), 56)
+    n = ep.rmsnorm(None, weight, 1e-6, stream, fp8=True)
+    assert n.residual is stream
+    zero = ep.rmsnorm(torch.zeros((T, 1024), dtype=torch.bfloat16, device="cuda"), weight, 1e-6, stream, fp8=True)
+    assert torch.equal(n.y, zero.y) and torch.equal(n.y_scales, zero.y_scales)
+    assert torch.equal(n.y_q.view(torch.uint8), zero.y_q.view(torch.uint8))
+    with pytest.raises(ValueError, match="x or residual is required"):
+        ep.rmsnorm(None, weight, 1e-6)
