@@ -217,7 +217,8 @@ ep_status_t rmsnorm(PyObject* const* a) {
     const at::Tensor *x = tensor_of(a[0], "x"), *residual = tensor_of(a[1], "residual");
     if (x == nullptr && residual == nullptr) refuse("x or residual is required");
     const at::Tensor& in = x != nullptr ? *x : *residual;
-    const int32_t T = dim(in, x != nullptr ? "x" : "residual", 2, 0), H = dim(in, "x", 2, 1);
+    const char* const name = x != nullptr ? "x" : "residual";
+    const int32_t T = dim(in, name, 2, 0), H = dim(in, name, 2, 1);
     const at::Tensor* out = tensor_of(a[4], "residual_out");
     const at::ScalarType type = stream_type(residual != nullptr ? residual : out);
     if (out != nullptr && out->scalar_type() != type)
