@@ -93,3 +93,21 @@ def test_what_a_helper_returns_may_be_freed_by_the_callers_stream():
         torch.cuda.synchronize()
         assert torch.equal(copy, want)
         del again
+
+
+def test_a_stream_may_be_anything_with_a_handle():
+    """What the entry points ask of a stream, its cuda_stream, is enough for the helpers too."""
+    i = inputs()
+    want = everything(i, None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+
+    got = everything(i, Handle())
+    torch.cuda.synchronize()
+    assert not same(got, want)
+    external = everything(i, torch.cuda.ExternalStream(side.cuda_stream))
+    torch.cuda.synchronize()
+    assert not same(external, want)
