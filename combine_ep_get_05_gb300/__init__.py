@@ -22,24 +22,29 @@ combine, with R virtual EP ranks held as slabs of one GPU's HBM:
                      of the sort
   ep_rmsnorm / ep_rmsnorm_bwd  residual addition + RMS norm to bf16 and E4M3 rows, and its
                      gradient
+  ep_expert_gate_up / ep_expert_down  the experts' gated feed-forward block over the
+                     expert-major slabs, with a checkpoint in bf16 or 8 bits
+  ep_expert_down_bwd / ep_expert_gate_up_bwd / ep_expert_wgrad  its gradients
 
 The C ABI is include/ep.h (libep_gb300.so, built in-tree by build.py); the
 functions here with the same names are its ctypes binding, and api.py
 allocates buffers and chains the calls.
 """
 from ._lib import (  # noqa: F401
-    ABI_VERSION, DTYPE_BF16, DTYPE_E4M3, DTYPE_F32, EP_ERR_CUDA, EP_ERR_INVALID, EP_ERR_SCRATCH, EP_OK,
+    ABI_VERSION, ACT_GELU, ACT_SILU, DTYPE_BF16, DTYPE_E4M3, DTYPE_F32, EP_ERR_CUDA, EP_ERR_INVALID, EP_ERR_SCRATCH, EP_OK,
     LAYOUT_NOALLOC_SCRATCH_BYTES, EXPORTS, FLAG_BAD_EXPERT,
     FLAG_CAPACITY, FLAG_TIMEOUT, FLAG_WORKSPACE, NODES_DENSE, NODES_SPARSE, EpError, ep_combine, ep_dispatch,
     ep_dispatch_nodes, ep_get_layout, ep_get_layout_noalloc, ep_layout_workspace_size, ep_restripe_prob, lib,
     ep_combine_permuted, ep_dispatch_permuted, ep_expert_layout_workspace_size, ep_get_expert_layout,
     ep_permute_received, ep_combine_fp8, ep_combine_weights, ep_dispatch_permuted_ll, ep_combine_send,
     ep_combine_permuted_ll, ep_dispatch_permuted_fp8, ep_dispatch_permuted_fp8_ll, ep_dispatch_permuted_bwd,
-    ep_combine_permuted_bwd, ep_rmsnorm, ep_rmsnorm_bwd, ep_rmsnorm_bwd_workspace_size,
+    ep_combine_permuted_bwd, ep_rmsnorm, ep_rmsnorm_bwd, ep_rmsnorm_bwd_workspace_size, ep_expert_gate_up,
+    ep_expert_down, ep_expert_down_bwd, ep_expert_gate_up_bwd, ep_expert_wgrad,
 )
 from .api import (  # noqa: F401
-    Dispatched, ExpertLayout, Layout, Normed, Permuted, alloc_dispatch, alloc_layout, alloc_permuted, combine,
+    Dispatched, ExpertLayout, GateUp, Layout, Normed, Permuted, alloc_dispatch, alloc_layout, alloc_permuted, combine,
     combine_fp8, combine_permuted, combine_permuted_bwd, combine_weights, dispatch, dispatch_permuted,
-    dispatch_permuted_bwd, get_expert_layout, get_layout, read_flags, rmsnorm, rmsnorm_bwd,
+    dispatch_permuted_bwd, expert_down, expert_down_bwd, expert_gate_up, expert_gate_up_bwd, expert_wgrad,
+    get_expert_layout, get_layout, read_flags, rmsnorm, rmsnorm_bwd,
 )
 from .build import LIB_PATH, build as build_library  # noqa: F401

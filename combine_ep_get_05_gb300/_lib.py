@@ -34,6 +34,9 @@ DTYPE_BF16 = 0
 DTYPE_E4M3 = 1
 DTYPE_F32 = 2
 
+ACT_SILU = 0
+ACT_GELU = 1
+
 NODES_DENSE = 0
 NODES_SPARSE = 1
 
@@ -47,6 +50,7 @@ EXPORTS = (
     "ep_combine_permuted", "ep_dispatch_permuted_ll", "ep_combine_send", "ep_combine_permuted_ll",
     "ep_dispatch_permuted_fp8", "ep_dispatch_permuted_fp8_ll", "ep_dispatch_permuted_bwd", "ep_combine_permuted_bwd",
     "ep_rmsnorm", "ep_rmsnorm_bwd_workspace_size", "ep_rmsnorm_bwd",
+    "ep_expert_gate_up", "ep_expert_down", "ep_expert_down_bwd", "ep_expert_gate_up_bwd", "ep_expert_wgrad",
 )
 
 
@@ -109,6 +113,11 @@ def lib():
                     "ep_rmsnorm": (i32, [P, P, P, i32, i32, f32, i32, i32, P, P, P, P, P]),
                     "ep_rmsnorm_bwd_workspace_size": (sz, [i32, i32]),
                     "ep_rmsnorm_bwd": (i32, [P, P, P, P, i32, i32, f32, i32, i32, P, P, P, P, sz, P]),
+                    "ep_expert_gate_up": (i32, [P, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P]),
+                    "ep_expert_down": (i32, [P, P, P, i32, i32, i32, i32, i32, P, P, P]),
+                    "ep_expert_down_bwd": (i32, [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P]),
+                    "ep_expert_gate_up_bwd": (i32, [P, P, P, i32, i32, i32, i32, i32, P, P, P]),
+                    "ep_expert_wgrad": (i32, [P, P, P, i32, i32, i32, i32, i32, P, P, P]),
                 }
                 for name, (res, args) in sigs.items():
                     f = getattr(L, name)
@@ -455,7 +464,7 @@ def ep_combine_send(y_perm, recv_src_idx, recv_topk_idx, recv_topk_w, tokens_per
     _done("ep_combine_send", rc)
 
 
-# --------------------------------------------------------------------------- E4M3 rows, gradients, norm
+# --------------------------------------------------------------------------- E4M3 rows, gradients, norm, experts
 # Checks of arguments and calls in csrc/ep_binding.cpp: these are the calls whose GPU work is
 # shorter than their checks would be here. They refuse what _check refuses, in its words.
 
@@ -476,7 +485,8 @@ def _native():
                 loader.exec_module(module)
                 module.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
                     "ep_rmsnorm", "ep_rmsnorm_bwd", "ep_dispatch_permuted_fp8", "ep_dispatch_permuted_fp8_ll",
-                    "ep_dispatch_permuted_bwd", "ep_combine_permuted_bwd")})
+                    "ep_dispatch_permuted_bwd", "ep_combine_permuted_bwd", "ep_expert_gate_up", "ep_expert_down",
+                    "ep_expert_down_bwd", "ep_expert_gate_up_bwd", "ep_expert_wgrad")})
                 _binding = module
     return _binding
 
@@ -536,3 +546,43 @@ def ep_rmsnorm_bwd(dy, z, weight, dz_in, eps, dz, dx=None, dweight=None, workspa
     rc = (_binding or _native()).rmsnorm_bwd(dy, z, weight, dz_in, eps, dz, dx, dweight, workspace, stream)
     if rc != EP_OK:
         _done("ep_rmsnorm_bwd", rc)
+
+
+def ep_expert_gate_up(x, w_gate_up, expert_offsets, act, h, pre=None, pre_q=None, pre_scales=None, status=None,
+                      stream=None):
+    """h = act(x Wg^T) * (x Wu^T) for every expert's rows of the slabs x [R][max_rows][H], with w_gate_up [E][2F][H];
+    pre (bf16) or pre_q and pre_scales (E4M3, 1x128, bf16 scales) keep (x Wg^T | x Wu^T) for the gradient."""
+    rc = (_binding or _native()).expert_gate_up(x, w_gate_up, expert_offsets, act, h, pre, pre_q, pre_scales, status,
+                                                stream)
+    if rc != EP_OK:
+        _done("ep_expert_gate_up", rc)
+
+
+def ep_expert_down(h, w_down, expert_offsets, y, status=None, stream=None):
+    """y = h W^T for every expert's rows of the slabs h [R][max_rows][F], with w_down [E][H][F]."""
+    rc = (_binding or _native()).expert_down(h, w_down, expert_offsets, y, status, stream)
+    if rc != EP_OK:
+        _done("ep_expert_down", rc)
+
+
+def ep_expert_down_bwd(dy, w_down, pre, pre_q, pre_scales, expert_offsets, act, dpre, h=None, status=None, stream=None):
+    """Gradient of ep_expert_down's rows through the activation: dpre [R][max_rows][2F] from dy and the checkpoint
+    (pre, or pre_q and pre_scales), and h again for the gradient of w_down."""
+    rc = (_binding or _native()).expert_down_bwd(dy, w_down, pre, pre_q, pre_scales, expert_offsets, act, dpre, h,
+                                                 status, stream)
+    if rc != EP_OK:
+        _done("ep_expert_down_bwd", rc)
+
+
+def ep_expert_gate_up_bwd(dpre, w_gate_up, expert_offsets, dx, status=None, stream=None):
+    """Gradient of ep_expert_gate_up's rows: dx = dpre W for every expert's rows."""
+    rc = (_binding or _native()).expert_gate_up_bwd(dpre, w_gate_up, expert_offsets, dx, status, stream)
+    if rc != EP_OK:
+        _done("ep_expert_gate_up_bwd", rc)
+
+
+def ep_expert_wgrad(dout, rows, expert_offsets, dw, status=None, stream=None):
+    """Gradient of an expert's weights: dw[e] = dout_e^T rows_e, zeros for an expert without rows."""
+    rc = (_binding or _native()).expert_wgrad(dout, rows, expert_offsets, dw, status, stream)
+    if rc != EP_OK:
+        _done("ep_expert_wgrad", rc)

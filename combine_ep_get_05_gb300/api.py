@@ -306,3 +306,77 @@ def combine_permuted_bwd(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Te
         L.ep_combine_permuted_bwd(dout, y, topk_idx, topk_w, layout.offsets, layout.slot, layout.num_experts, dy, dw,
                                   status, stream)
     return dy, dw
+
+
+# --------------------------------------------------------------------------- the experts' feed-forward block
+
+@dataclass
+class GateUp:
+    h: torch.Tensor                       # bf16 [R][max_rows][F]
+    pre: Optional[torch.Tensor]           # bf16 [R][max_rows][2F] (save="bf16")
+    pre_q: Optional[torch.Tensor]         # float8_e4m3fn [R][max_rows][2F] (save="8bit")
+    pre_scales: Optional[torch.Tensor]    # bf16 [R][max_rows][2F/128] (save="8bit")
+
+
+def expert_gate_up(x: torch.Tensor, w_gate_up: torch.Tensor, layout: ExpertLayout, act: int = L.ACT_SILU,
+                   save: Optional[str] = None, status: Optional[torch.Tensor] = None, stream=None) -> GateUp:
+    """act(x Wg^T) * (x Wu^T) of every expert's rows; save="bf16" or "8bit" keeps what the gradient needs. Rows that
+    no expert owns are zeros in h; in the checkpoint they hold nothing of use."""
+    if save not in (None, "bf16", "8bit"):
+        raise ValueError(f'save must be None, "bf16" or "8bit", got {save!r}')
+    R, M, _ = x.shape
+    N, dev = w_gate_up.shape[1], x.device
+    with _On(stream) as on:
+        g = on.made(GateUp(
+            h=torch.zeros((R, M, N // 2), dtype=torch.bfloat16, device=dev),
+            pre=torch.empty((R, M, N), dtype=torch.bfloat16, device=dev) if save == "bf16" else None,
+            pre_q=torch.empty((R, M, N), dtype=torch.float8_e4m3fn, device=dev) if save == "8bit" else None,
+            pre_scales=torch.empty((R, M, N // 128), dtype=torch.bfloat16, device=dev) if save == "8bit" else None))
+        L.ep_expert_gate_up(x, w_gate_up, layout.offsets, act, g.h, g.pre, g.pre_q, g.pre_scales, status, stream)
+    return g
+
+
+def expert_down(h: torch.Tensor, w_down: torch.Tensor, layout: ExpertLayout, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """h W^T of every expert's rows; zeros in rows that no expert owns."""
+    with _On(stream) as on:
+        y = on.made(torch.zeros((*h.shape[:2], w_down.shape[1]), dtype=torch.bfloat16, device=h.device))
+        L.ep_expert_down(h, w_down, layout.offsets, y, status, stream)
+    return y
+
+
+def expert_down_bwd(dy: torch.Tensor, w_down: torch.Tensor, saved: GateUp, layout: ExpertLayout,
+                    act: int = L.ACT_SILU, status: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of expert_down through the activation, from the checkpoint that expert_gate_up kept: (dpre, h again),
+    zeros in rows that no expert owns."""
+    if saved.pre is None and saved.pre_q is None:
+        raise ValueError("expert_gate_up kept no checkpoint")
+    R, M, _ = dy.shape
+    F, dev = w_down.shape[2], dy.device
+    with _On(stream) as on:
+        dpre = on.made(torch.zeros((R, M, 2 * F), dtype=torch.bfloat16, device=dev))
+        h = on.made(torch.zeros((R, M, F), dtype=torch.bfloat16, device=dev))
+        eight = saved.pre is None
+        L.ep_expert_down_bwd(dy, w_down, saved.pre, saved.pre_q if eight else None, saved.pre_scales if eight else None,
+                             layout.offsets, act, dpre, h, status, stream)
+    return dpre, h
+
+
+def expert_gate_up_bwd(dpre: torch.Tensor, w_gate_up: torch.Tensor, layout: ExpertLayout,
+                       status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of expert_gate_up's rows; zeros in rows that no expert owns."""
+    with _On(stream) as on:
+        dx = on.made(torch.zeros((*dpre.shape[:2], w_gate_up.shape[2]), dtype=torch.bfloat16, device=dpre.device))
+        L.ep_expert_gate_up_bwd(dpre, w_gate_up, layout.offsets, dx, status, stream)
+    return dx
+
+
+def expert_wgrad(dout: torch.Tensor, rows: torch.Tensor, layout: ExpertLayout,
+                 status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the experts' weights, bf16 [E][width of dout][width of rows]: of w_gate_up from (dpre, x), of
+    w_down from (dy, h)."""
+    with _On(stream) as on:
+        dw = on.made(torch.empty((layout.num_experts, dout.shape[2], rows.shape[2]), dtype=torch.bfloat16,
+                                 device=dout.device))
+        L.ep_expert_wgrad(dout, rows, layout.offsets, dw, status, stream)
+    return dw

@@ -1,4 +1,4 @@
-// ep_binding.cpp -- Python binding of the norm, the E4M3 sort and the gradients
+// ep_binding.cpp -- Python binding of the norm, the E4M3 sort, the gradients and the experts' products
 // (module _ep_binding; combine_ep_get_05_gb300/_lib.py wraps it).
 //
 // These calls are a few microseconds of GPU work where a batch is small, and checking ten
@@ -172,11 +172,17 @@ struct {
     decltype(&ep_dispatch_permuted_fp8_ll) dispatch_permuted_fp8_ll;
     decltype(&ep_dispatch_permuted_bwd) dispatch_permuted_bwd;
     decltype(&ep_combine_permuted_bwd) combine_permuted_bwd;
+    decltype(&ep_expert_gate_up) expert_gate_up;
+    decltype(&ep_expert_down) expert_down;
+    decltype(&ep_expert_down_bwd) expert_down_bwd;
+    decltype(&ep_expert_gate_up_bwd) expert_gate_up_bwd;
+    decltype(&ep_expert_wgrad) expert_wgrad;
 } g_ep;
 
 template <typename F>
 void take(F*& to, PyObject* addresses, const char* name) {
     PyObject* v = PyDict_GetItemString(addresses, name);  // borrowed
+    if (v == nullptr && to != nullptr) return;  // stays as it was bound before
     if (v == nullptr) refuse("no address for %s", name);
     to = reinterpret_cast<F*>(PyLong_AsVoidPtr(v));
     if (to == nullptr) refuse("no address for %s", name);
@@ -189,6 +195,11 @@ ep_status_t bind(PyObject* const* a) {
     take(g_ep.dispatch_permuted_fp8_ll, a[0], "ep_dispatch_permuted_fp8_ll");
     take(g_ep.dispatch_permuted_bwd, a[0], "ep_dispatch_permuted_bwd");
     take(g_ep.combine_permuted_bwd, a[0], "ep_combine_permuted_bwd");
+    take(g_ep.expert_gate_up, a[0], "ep_expert_gate_up");
+    take(g_ep.expert_down, a[0], "ep_expert_down");
+    take(g_ep.expert_down_bwd, a[0], "ep_expert_down_bwd");
+    take(g_ep.expert_gate_up_bwd, a[0], "ep_expert_gate_up_bwd");
+    take(g_ep.expert_wgrad, a[0], "ep_expert_wgrad");
     return EP_OK;
 }
 
@@ -352,6 +363,121 @@ ep_status_t combine_permuted_bwd(PyObject* const* a) {
     });
 }
 
+// Rows of an expert-major slab and its experts' weights: the sizes that set a call's dimensions.
+struct Slab {
+    int32_t R, M, width;
+};
+Slab slab(const at::Tensor& t, const char* name) {
+    return {dim(t, name, 3, 0), dim(t, name, 3, 1), dim(t, name, 3, 2)};
+}
+struct Weights {
+    int32_t E, out, in;
+};
+Weights weights(const at::Tensor& t, const char* name) {
+    return {dim(t, name, 3, 0), dim(t, name, 3, 1), dim(t, name, 3, 2)};
+}
+// the up-projection's: an even number of rows, gate's and up's
+Weights gated_weights(const at::Tensor& t, const char* name) {
+    const Weights w = weights(t, name);
+    if (w.out % 2 != 0) refuse("%s must have an even number of rows an expert, got %d", name, w.out);
+    return w;
+}
+const int32_t* offsets_of(PyObject* o, int32_t E) {
+    return as<int32_t>(reads(o, "expert_offsets", at::kInt, {static_cast<int64_t>(E) + 1}));
+}
+int32_t* status_of(PyObject* o) { return as<int32_t>(writes_or_null(o, "status", at::kInt, {1})); }
+
+// x, w_gate_up, expert_offsets, act, h, pre, pre_q, pre_scales, status, stream
+ep_status_t expert_gate_up(PyObject* const* a) {
+    const at::Tensor &x = required(a[0], "x"), &w = required(a[1], "w_gate_up");
+    const Slab s = slab(x, "x");
+    const Weights d = gated_weights(w, "w_gate_up");
+    const int32_t H = s.width, F = d.out / 2, act = integer(a[3], "act");
+    const void* const px = reads(x, "x", at::kBFloat16, {s.R, s.M, H});
+    const void* const pw = reads(w, "w_gate_up", at::kBFloat16, {d.E, d.out, H});
+    const int32_t* const off = offsets_of(a[2], d.E);
+    void* const h = writes(a[4], "h", at::kBFloat16, {s.R, s.M, F});
+    void* const pre = writes_or_null(a[5], "pre", at::kBFloat16, {s.R, s.M, d.out});
+    uint8_t* q = nullptr;
+    if (a[6] != Py_None) q = as<uint8_t>(writes(a[6], "pre_q", code_type(a[6], "pre_q"), {s.R, s.M, d.out}));
+    void* const scales = q != nullptr ? writes(a[7], "pre_scales", at::kBFloat16, {s.R, s.M, d.out / 128})
+                                      : writes_or_null(a[7], "pre_scales", at::kBFloat16, {s.R, s.M, d.out / 128});
+    int32_t* const status = status_of(a[8]);
+    void* const stream = stream_of(a[9]);
+    return launched([&] {
+        return g_ep.expert_gate_up(px, pw, off, act, H, F, d.E, s.R, s.M, h, pre, q, scales, status, stream);
+    });
+}
+
+// h, w_down, expert_offsets, y, status, stream
+ep_status_t expert_down(PyObject* const* a) {
+    const at::Tensor &h = required(a[0], "h"), &w = required(a[1], "w_down");
+    const Slab s = slab(h, "h");
+    const Weights d = weights(w, "w_down");
+    const int32_t F = s.width, H = d.out;
+    const void* const ph = reads(h, "h", at::kBFloat16, {s.R, s.M, F});
+    const void* const pw = reads(w, "w_down", at::kBFloat16, {d.E, H, F});
+    const int32_t* const off = offsets_of(a[2], d.E);
+    void* const y = writes(a[3], "y", at::kBFloat16, {s.R, s.M, H});
+    int32_t* const status = status_of(a[4]);
+    void* const stream = stream_of(a[5]);
+    return launched([&] { return g_ep.expert_down(ph, pw, off, H, F, d.E, s.R, s.M, y, status, stream); });
+}
+
+// dy, w_down, pre, pre_q, pre_scales, expert_offsets, act, dpre, h, status, stream
+ep_status_t expert_down_bwd(PyObject* const* a) {
+    const at::Tensor &dy = required(a[0], "dy"), &w = required(a[1], "w_down");
+    const Slab s = slab(dy, "dy");
+    const Weights d = weights(w, "w_down");
+    const int32_t H = s.width, F = d.in, act = integer(a[6], "act");
+    const int64_t wide = 2 * static_cast<int64_t>(F);
+    const void* const pdy = reads(dy, "dy", at::kBFloat16, {s.R, s.M, H});
+    const void* const pw = reads(w, "w_down", at::kBFloat16, {d.E, H, F});
+    if ((a[2] == Py_None) == (a[3] == Py_None)) refuse("either pre or pre_q is required");
+    const void* const pre = reads_or_null(a[2], "pre", at::kBFloat16, {s.R, s.M, wide});
+    const uint8_t* q = nullptr;
+    if (a[3] != Py_None) q = as<uint8_t>(reads(a[3], "pre_q", code_type(a[3], "pre_q"), {s.R, s.M, wide}));
+    const void* const scales = q != nullptr ? reads(a[4], "pre_scales", at::kBFloat16, {s.R, s.M, wide / 128})
+                                            : reads_or_null(a[4], "pre_scales", at::kBFloat16, {s.R, s.M, wide / 128});
+    const int32_t* const off = offsets_of(a[5], d.E);
+    void* const dpre = writes(a[7], "dpre", at::kBFloat16, {s.R, s.M, wide});
+    void* const h = writes_or_null(a[8], "h", at::kBFloat16, {s.R, s.M, F});
+    int32_t* const status = status_of(a[9]);
+    void* const stream = stream_of(a[10]);
+    return launched([&] {
+        return g_ep.expert_down_bwd(pdy, pw, pre, q, scales, off, act, H, F, d.E, s.R, s.M, dpre, h, status, stream);
+    });
+}
+
+// dpre, w_gate_up, expert_offsets, dx, status, stream
+ep_status_t expert_gate_up_bwd(PyObject* const* a) {
+    const at::Tensor &dpre = required(a[0], "dpre"), &w = required(a[1], "w_gate_up");
+    const Slab s = slab(dpre, "dpre");
+    const Weights d = gated_weights(w, "w_gate_up");
+    const int32_t H = d.in, F = d.out / 2;
+    const void* const pd = reads(dpre, "dpre", at::kBFloat16, {s.R, s.M, d.out});
+    const void* const pw = reads(w, "w_gate_up", at::kBFloat16, {d.E, d.out, H});
+    const int32_t* const off = offsets_of(a[2], d.E);
+    void* const dx = writes(a[3], "dx", at::kBFloat16, {s.R, s.M, H});
+    int32_t* const status = status_of(a[4]);
+    void* const stream = stream_of(a[5]);
+    return launched([&] { return g_ep.expert_gate_up_bwd(pd, pw, off, H, F, d.E, s.R, s.M, dx, status, stream); });
+}
+
+// dout, in, expert_offsets, dw, status, stream
+ep_status_t expert_wgrad(PyObject* const* a) {
+    const at::Tensor &dout = required(a[0], "dout"), &in = required(a[1], "rows"), &dw = required(a[3], "dw");
+    const Slab s = slab(dout, "dout");
+    const int32_t E = dim(dw, "dw", 3, 0), I = s.width, J = slab(in, "rows").width;
+    const void* const pd = reads(dout, "dout", at::kBFloat16, {s.R, s.M, I});
+    const void* const pi = reads(in, "rows", at::kBFloat16, {s.R, s.M, J});
+    const int32_t* const off = offsets_of(a[2], E);
+    void* const pw = writes(dw, "dw", at::kBFloat16, {E, I, J});
+    int32_t* const status = status_of(a[4]);
+    void* const stream = stream_of(a[5]);
+    return launched([&] { return g_ep.expert_wgrad(pd, pi, off, I, J, E, s.R, s.M, pw, status, stream); });
+}
+
 // A call: the number of arguments, then the function; no C++ exception leaves it.
 template <ep_status_t (*kCall)(PyObject* const*), Py_ssize_t kArgs>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -384,6 +510,11 @@ PyMethodDef g_methods[] = {
     method<dispatch_permuted_fp8_ll, 15>("dispatch_permuted_fp8_ll"),
     method<dispatch_permuted_bwd, 11>("dispatch_permuted_bwd"),
     method<combine_permuted_bwd, 11>("combine_permuted_bwd"),
+    method<expert_gate_up, 10>("expert_gate_up"),
+    method<expert_down, 6>("expert_down"),
+    method<expert_down_bwd, 11>("expert_down_bwd"),
+    method<expert_gate_up_bwd, 6>("expert_gate_up_bwd"),
+    method<expert_wgrad, 6>("expert_wgrad"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,0 +1,59 @@
+// ep_expert.cuh -- what the experts' products share: an expert's rows, the gated activation
+// and its derivative, the 8-bit checkpoint's scale and codes. Internal header.
+#pragma once
+
+#include "ep_common.cuh"
+
+namespace ep {
+
+// The rows [first, first + count) of an expert in the slabs seen as one array of rows.
+struct ExpertRows {
+    long long first;
+    int count;
+    bool dropped;  // some lay past the slab's end
+};
+
+// Rows of expert e, whatever the offsets hold: never outside slab e / epr.
+__device__ __forceinline__ ExpertRows expert_rows(const int32_t* offsets, int e, int epr, int max_rows) {
+    const int r = e / epr;
+    const long long base = offsets[r * epr];
+    const long long a = offsets[e] - base, b = offsets[e + 1] - base;
+    const long long lo = a < 0 ? 0 : (a > max_rows ? max_rows : a);
+    const long long hi = b < lo ? lo : (b > max_rows ? max_rows : b);
+    return {static_cast<long long>(r) * max_rows + lo, static_cast<int>(hi - lo), b > max_rows && b > a};
+}
+
+// act(v) = v * s, s = sigmoid(p(v)); both activations are of this form, so that their
+// derivative is s + v * s * (1 - s) * p'(v). The exponential and the reciprocal are the fast
+// ones (a few 2^-22 relative): what comes out is rounded to bf16, 2^-9. exp overflows to
+// infinity where p < -88, whose reciprocal is 0: the right limit.
+struct Gate {
+    float s, slope;  // sigmoid(p(v)), p'(v)
+};
+
+__device__ __forceinline__ Gate gate_of(float v, int act) {
+    float p = v, slope = 1.0f;
+    if (act == EP_ACT_GELU) {
+        constexpr float kA = 1.5957691216057308f, kB = 0.044715f;  // 2 sqrt(2 / pi)
+        const float v2 = v * v;
+        p = kA * (v + kB * v * v2);
+        slope = kA * (1.0f + 3.0f * kB * v2);
+    }
+    return {__fdividef(1.0f, 1.0f + __expf(-p)), slope};
+}
+
+// bf16_rn(amax / 448), in fp32
+__device__ __forceinline__ float checkpoint_scale(float amax) {
+    return bf16_lo(pack_bf16x2_rn(__fdiv_rn(amax, 448.0f), 0.0f));
+}
+
+// What a block's values are multiplied by before they become codes; a scale below 2^-126 has
+// no finite reciprocal, and its values take the division (checkpoint_code).
+__device__ __forceinline__ float checkpoint_rcp(float scale) {
+    return scale == 0.0f ? 1.0f : scale < 0x1p-125f ? -1.0f : __frcp_rn(scale);
+}
+__device__ __forceinline__ float checkpoint_quotient(float c, float scale, float rcp) {
+    return rcp < 0.0f ? __fdiv_rn(c, scale) : c * rcp;
+}
+
+}  // namespace ep

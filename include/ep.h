@@ -71,6 +71,10 @@ typedef int32_t ep_node_mode_t;
 #define EP_NODES_DENSE 0  /* copy every chunk's whole token range to every node */
 #define EP_NODES_SPARSE 1 /* copy only the runs of consecutive tokens routed to the node */
 
+typedef int32_t ep_act_t; /* the gate's activation: act(v) = v * sigmoid(p(v)) */
+#define EP_ACT_SILU 0 /* p(v) = v */
+#define EP_ACT_GELU 1 /* GELU in its tanh form: p(v) = 2 sqrt(2/pi) (v + 0.044715 v^3) */
+
 /* ABI version of the loaded library (EP_ABI_VERSION at build time). */
 int32_t ep_abi_version(void);
 
@@ -542,6 +546,77 @@ ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, co
                            ep_dtype_t stream_dtype, ep_dtype_t weight_dtype, float eps, int32_t T,
                            int32_t H, void* dz, void* dx, float* dweight, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* The experts' feed-forward block                                           */
+/* ------------------------------------------------------------------------- */
+
+/* The products of the experts' gated feed-forward block, over the expert-major slabs that
+ * ep_dispatch_permuted fills and ep_combine_permuted reads, and their gradients. Common to all:
+ *   expert_offsets int32 [E+1] from the expert layout, read on the device: the rows of expert e
+ *     are the rows p0 <= p < p1 of rank r = e / (E/R), p0 = expert_offsets[e] -
+ *     expert_offsets[r*(E/R)], p1 = p0 + the expert's count. Rows past max_rows are dropped
+ *     with EP_FLAG_CAPACITY; a count below 0 is taken as 0. Rows of a slab that belong to no
+ *     expert are neither used nor written, whatever they hold.
+ *   w_gate_up bf16 [E][2F][H]: F gate rows, then F up rows; w_down bf16 [E][H][F]
+ *   1 <= R <= 256, E % R == 0, E <= 8192; H % 8 == 0, F % 8 == 0, both <= 65536;
+ *     max_rows >= 0, R * max_rows < 2^31. All arrays of one call are distinct ones.
+ *   Products of bf16 values are summed in fp32 by the tensor cores (whose additions
+ *   truncate: the sum of K products is good to about K * 2^-30 of its terms' size) in an order
+ *   that depends on the sizes only; what follows is fp32, and each output is rounded once.
+ *   Results are deterministic. EP_FLAG_TIMEOUT: a bounded wait gave up, and outputs are
+ *   incomplete. E = 1, R = 1 with offsets {0, T} is an ordinary dense layer. */
+
+/* ep_expert_gate_up -- for every row of every expert
+ *   gate[p][f] = sum over h of x[r][p][h] * w_gate_up[e][f][h]
+ *   up[p][f]   = sum over h of x[r][p][h] * w_gate_up[e][F + f][h]
+ *   h[r][p][f] = bf16_rn(act(gate) * up)
+ * and, for the gradient, a checkpoint of c = (gate | up), 2F channels a row, in one of two forms:
+ *   pre[r][p][j]        = bf16_rn(c[j])
+ *   pre_scales[r][p][b] = bf16_rn(max |c| over the 128 channels of block b / 448)
+ *   pre_q[r][p][j]      = e4m3(c[j] / pre_scales[r][p][b])   (rounded to nearest even, saturated)
+ * A block whose scale rounds to 0 has zero codes; a NaN becomes a NaN code and takes no part in
+ * the maximum; one with an infinity has scale infinity, zeros and NaN for the infinities.
+ *   x bf16 [R][max_rows][H]; h bf16 [R][max_rows][F]; pre bf16 [R][max_rows][2F] or NULL;
+ *   pre_q uint8 [R][max_rows][2F] and pre_scales bf16 [R][max_rows][2F/128]: both or neither,
+ *   F % 128 == 0 with them. Either checkpoint, both or none. One launch. */
+ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_t* expert_offsets, ep_act_t act,
+                              int32_t H, int32_t F, int32_t E, int32_t R, int32_t max_rows, void* h, void* pre,
+                              uint8_t* pre_q, void* pre_scales, int32_t* status, void* stream);
+
+/* ep_expert_down -- y[r][p][j] = bf16_rn(sum over f of h[r][p][f] * w_down[e][j][f]).
+ *   h bf16 [R][max_rows][F]; y bf16 [R][max_rows][H]. One launch. */
+ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* expert_offsets, int32_t H, int32_t F,
+                           int32_t E, int32_t R, int32_t max_rows, void* y, int32_t* status, void* stream);
+
+/* ep_expert_down_bwd -- gradient of ep_expert_down with respect to its rows, taken through the
+ * activation, from the checkpoint (gate | up) that ep_expert_gate_up kept (pre, or
+ * pre_q * pre_scales: one of the two forms):
+ *   dh[p][f]         = sum over j of dy[r][p][j] * w_down[e][j][f]
+ *   dpre[r][p][f]    = bf16_rn(dh * up * act'(gate))
+ *   dpre[r][p][F+f]  = bf16_rn(dh * act(gate))
+ *   h[r][p][f]       = bf16_rn(act(gate) * up)     (recomputed: the gradient of w_down reads it)
+ *   dy bf16 [R][max_rows][H]; dpre bf16 [R][max_rows][2F]; h bf16 [R][max_rows][F] or NULL;
+ *   the checkpoint as ep_expert_gate_up. One launch. */
+ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* pre, const uint8_t* pre_q,
+                               const void* pre_scales, const int32_t* expert_offsets, ep_act_t act, int32_t H,
+                               int32_t F, int32_t E, int32_t R, int32_t max_rows, void* dpre, void* h,
+                               int32_t* status, void* stream);
+
+/* ep_expert_gate_up_bwd -- gradient of the up-projection with respect to its rows:
+ *   dx[r][p][j] = bf16_rn(sum over c of dpre[r][p][c] * w_gate_up[e][c][j]), c over 2F channels
+ *   dpre bf16 [R][max_rows][2F]; dx bf16 [R][max_rows][H]. One launch. */
+ep_status_t ep_expert_gate_up_bwd(const void* dpre, const void* w_gate_up, const int32_t* expert_offsets, int32_t H,
+                                  int32_t F, int32_t E, int32_t R, int32_t max_rows, void* dx, int32_t* status,
+                                  void* stream);
+
+/* ep_expert_wgrad -- gradient of an expert's weights:
+ *   dw[e][i][j] = bf16_rn(sum over the expert's rows p of dout[r][p][i] * rows[r][p][j])
+ * dout = dpre, rows = x for w_gate_up (I = 2F, J = H); dout = dy, rows = h for w_down (I = H, J = F).
+ *   dout bf16 [R][max_rows][I]; rows bf16 [R][max_rows][J]; I % 8 == 0, J % 8 == 0, both <= 131072;
+ *   dw bf16 [E][I][J], all of it written: zeros for an expert without rows. One launch. */
+ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* expert_offsets, int32_t I, int32_t J,
+                            int32_t E, int32_t R, int32_t max_rows, void* dw, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }
