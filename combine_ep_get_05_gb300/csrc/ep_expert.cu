@@ -1,12 +1,15 @@
 // ep_expert.cu -- the experts' gated feed-forward block over the expert-major slabs: the
 // products of every expert's rows with its weights, and their gradients (include/ep.h).
 //
-// One kernel for all five: C[i][j] = sum over k of A[i][k] * B[j][k] in fp32, i a row of the
-// expert (of the weights, in their gradient), j an output channel, with the operator's
-// arithmetic on the finished sums. A CTA takes 128 channels of an expert and walks the
-// expert's rows 32 at a time: tiles of 16 k in shared memory, 16 sums a thread, a row's 128
-// channels in one warp.
+// One kernel for all five. The operand with the output's channels (the weights; in their own
+// gradient, the rows that were multiplied with them) lies along the tensor cores' 256 lanes
+// of a pair of CTAs, the expert's rows along the columns, of which a product takes any
+// multiple of 32: an expert with 140 rows costs 160 columns, not two tiles of 128 rows. Each
+// CTA of a persistent grid has a warp that copies tensor boxes into a ring of stages, one (of
+// the pair) that multiplies them into tensor memory, and eight that finish the sums of one
+// tile while the next is multiplied.
 #include "ep_expert.cuh"
+#include "ep_mma.cuh"
 
 namespace {
 
@@ -14,132 +17,577 @@ using namespace ep;
 
 enum Op { kGateUp, kDown, kDownBwd, kGateUpBwd, kWgrad };
 
-constexpr int kRows = 32, kCols = 128, kStep = 16, kThreads = 256;
+constexpr int kThreads = 384;        // 4 warps that feed and multiply, 8 that finish tiles
+constexpr int kProducer = 0, kMultiplier = 1, kTail = 2, kFinish = 4;  // first warp of each part
+constexpr int kHalfThreads = 128;    // 4 finishing warps: the 128 lanes of every other 32 columns
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kStageColumns = 256;  // of tensor memory: two tiles at a time
+constexpr int kMostStages = 8;
+constexpr size_t kSmemMost = 227 * 1024;
+
+template <int kOp>
+struct Traits {
+    static constexpr bool kGated = kOp == kGateUp;
+    static constexpr bool kAAcross = kOp == kDownBwd || kOp == kGateUpBwd || kOp == kWgrad;
+    static constexpr bool kBAcross = kOp == kWgrad;
+    static constexpr int kMostN = kGated ? 128 : 256;           // rows of an expert a tile
+    static constexpr uint32_t kABytes = (kGated ? 2 : 1) * 128 * kBlockK * 2;
+    static constexpr uint32_t kBBytes = kMostN / 2 * kBlockK * 2;
+    static constexpr uint32_t kStageBytes = kABytes + kBBytes;  // of one CTA
+};
 
 struct ExpertArgs {
-    const uint16_t* a;  // rows (the output's gradient, in kWgrad)
-    const uint16_t* b;  // weights (the rows, in kWgrad)
+    const int32_t* offsets;
+    int act;
+    int C;  // output channels, along the lanes (one half of them in kGateUp and kDownBwd)
+    int K;  // products of a sum (kWgrad: output rows, along the columns)
+    int E, R, max_rows;
+    int stages;
     const uint16_t* pre;
     const uint8_t* pre_q;
     const uint16_t* pre_scales;
-    const int32_t* offsets;
-    int act;
-    int N, K;  // output channels (one half of them in kGateUp and kDownBwd); products of a sum
-    int E, R, max_rows;
     uint16_t *out, *out_pre, *out_scales;
     uint8_t* out_q;
     int32_t* status;
 };
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p, size_t i) {
-    return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+// A tile: 256 channels (128 a CTA) of up to kMostN rows of an expert; in kWgrad, of up to
+// kMostN rows of its gradient.
+struct Tile {
+    int e;
+    long long row;  // first row of the slabs; kWgrad: the expert's
+    int rows;       // rows that are there (columns of the sums that are kept)
+    int n;          // columns that are multiplied: a multiple of 32
+    int channel;    // first of the pair's
+    int column;     // kWgrad: first row of dw[e]
+    int k;          // products of a sum
+};
+
+struct Shared {  // behind the stages
+    uint64_t full[kMostStages], ready[kMostStages], empty[kMostStages];
+    uint64_t sums_full[2], sums_empty[2], drain;
+    uint32_t tmem;
+    int stop;        // a wait gave up
+    int most_n;      // rows a tile, of this call
+    int scan[kThreads / 32];
+    float amax[2][2][4][64];  // [half][buffer][warp][gate and up of 32 columns]
+    int prefix[1];   // [E + 1] tiles of rows before each expert's (but kWgrad)
+};
+
+__device__ __forceinline__ int row_tiles(int count, int most_n, int* each) {
+    if (count == 0) return 0;
+    const int tiles = (count + most_n - 1) / most_n;
+    const int n = ((count + tiles - 1) / tiles + 31) / 32 * 32;  // even tiles, not full ones and a rest
+    *each = n;
+    return (count + n - 1) / n;
 }
-__device__ __forceinline__ uint16_t bf16_rn(float v) { return static_cast<uint16_t>(pack_bf16x2_rn(v, 0.0f)); }
 
 template <int kOp>
-__global__ void __launch_bounds__(kThreads) expert_kernel(ExpertArgs g) {
-    constexpr int kHalves = kOp == kGateUp ? 2 : 1;
-    __shared__ float s_a[kStep][kRows + 1];
-    __shared__ float s_b[kHalves][kStep][kCols + 1];
-    const int e = static_cast<int>(blockIdx.y);
-    const int col0 = static_cast<int>(blockIdx.x) * kCols;
-    const int tid = static_cast<int>(threadIdx.x), tx = tid % 32, ty = tid / 32;
-    const ExpertRows rows = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
-    if (rows.dropped && blockIdx.x == 0 && tid == 0) raise_flag(g.status, EP_FLAG_CAPACITY);
-    const int I = kOp == kWgrad ? g.K : rows.count;  // kWgrad: K is the number of its rows' channels
-    const int K = kOp == kWgrad ? rows.count : g.K;
-    const size_t N = static_cast<size_t>(g.N);
-    for (int row0 = 0; row0 < I; row0 += kRows) {
-        float c[kHalves][4][4] = {};
-        for (int k0 = 0; k0 < K; k0 += kStep) {
-            __syncthreads();
-            for (int n = tid; n < kRows * kStep; n += kThreads) {
-                const int i = n / kStep, k = n % kStep;
-                float v = 0.0f;
-                if (row0 + i < I && k0 + k < K) {
-                    if (kOp == kWgrad)
-                        v = bf16_at(g.a, static_cast<size_t>(rows.first + k0 + k) * I + row0 + i);
-                    else
-                        v = bf16_at(g.a, static_cast<size_t>(rows.first + row0 + i) * K + k0 + k);
-                }
-                s_a[k][i] = v;
-            }
-            for (int n = tid; n < kHalves * kCols * kStep; n += kThreads) {
-                const int half = n / (kCols * kStep), m = n % (kCols * kStep);
-                // consecutive threads along what is contiguous in memory
-                const bool k_major = kOp == kGateUp || kOp == kDown;
-                const int j = k_major ? m / kStep : m % kCols, k = k_major ? m % kStep : m / kCols;
-                float v = 0.0f;
-                if (col0 + j < g.N && k0 + k < K) {
-                    size_t at;
-                    if (kOp == kWgrad)
-                        at = static_cast<size_t>(rows.first + k0 + k) * N + col0 + j;
-                    else if (k_major)
-                        at = ((static_cast<size_t>(e) * kHalves + half) * N + col0 + j) * K + k0 + k;
-                    else
-                        at = (static_cast<size_t>(e) * K + k0 + k) * N + col0 + j;
-                    v = bf16_at(g.b, at);
-                }
-                s_b[half][k][j] = v;
-            }
-            __syncthreads();
-            for (int k = 0; k < kStep; ++k)
-                for (int half = 0; half < kHalves; ++half)
-                    for (int i = 0; i < 4; ++i)
-                        for (int j = 0; j < 4; ++j)
-                            c[half][i][j] = fmaf(s_a[k][ty * 4 + i], s_b[half][k][tx + 32 * j], c[half][i][j]);
+__device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared& s, long long t, Tile* tile) {
+    const int across = (g.C + 255) / 256;
+    if (kOp == kWgrad) {
+        const int down = (g.K + 255) / 256;
+        if (t >= static_cast<long long>(g.E) * across * down) return false;
+        const int e = static_cast<int>(t / (across * down)), l = static_cast<int>(t % (across * down));
+        const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        tile->e = e;
+        tile->row = r.first;
+        tile->k = r.count;
+        tile->channel = l % across * 256;
+        tile->column = l / across * 256;
+        tile->rows = g.K - tile->column < 256 ? g.K - tile->column : 256;
+        tile->n = (tile->rows + 31) / 32 * 32;
+        return true;
+    }
+    if (t >= static_cast<long long>(s.prefix[g.E]) * across) return false;
+    int lo = 0, hi = g.E;  // the last expert whose tiles begin at or before t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (static_cast<long long>(s.prefix[mid]) * across <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const ExpertRows r = expert_rows(g.offsets, lo, g.E / g.R, g.max_rows);
+    int each = 32;
+    const int tiles = row_tiles(r.count, s.most_n, &each);
+    // eight tiles of rows with all channels, then the next eight: the rows that are at work at a
+    // time, and the weights that they share, stay in L2
+    int l = static_cast<int>(t - static_cast<long long>(s.prefix[lo]) * across);
+    const int group = l / (8 * across);
+    l -= group * 8 * across;
+    const int width = tiles - group * 8 < 8 ? tiles - group * 8 : 8;
+    const int i = group * 8 + l % width;
+    tile->e = lo;
+    tile->row = r.first + static_cast<long long>(i) * each;
+    tile->rows = r.count - i * each < each ? r.count - i * each : each;
+    tile->n = (tile->rows + 31) / 32 * 32;
+    tile->channel = l / width * 256;
+    tile->column = 0;
+    tile->k = g.K;
+    return true;
+}
+
+// The number of tiles of rows before each expert's, by all threads. Rows a tile are halved while
+// the tiles would not fill the GPU.
+template <int kOp>
+__device__ void plan_tiles(const ExpertArgs& g, Shared& s) {
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    const int per = (g.E + kThreads - 1) / kThreads, first = tid * per;
+    const int last = first + per < g.E ? first + per : g.E;
+    const int across = (g.C + 255) / 256, pairs = static_cast<int>(gridDim.x / 2);
+    int each, before, sum, most_n = Traits<kOp>::kMostN;
+    for (;; most_n /= 2) {
+        sum = 0;
+        for (int e = first; e < last; ++e) {
+            const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+            if (r.dropped && blockIdx.x == 0 && most_n == Traits<kOp>::kMostN) raise_flag(g.status, EP_FLAG_CAPACITY);
+            sum += row_tiles(r.count, most_n, &each);
         }
-        for (int i = 0; i < 4; ++i) {
-            const int row = row0 + ty * 4 + i;
-            if (row >= I) break;  // the whole warp
-            const size_t at = kOp == kWgrad ? static_cast<size_t>(e) * I + row : static_cast<size_t>(rows.first + row);
-            float rcp[kHalves], scale[kHalves];
-            if (kOp == kGateUp && g.out_q != nullptr) {
-                for (int half = 0; half < kHalves; ++half) {
-                    float amax = 0.0f;
-                    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(c[half][i][j]));
-                    for (int d = 16; d > 0; d /= 2) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, d));
-                    scale[half] = checkpoint_scale(amax);
-                    rcp[half] = checkpoint_rcp(scale[half]);
-                    if (tx == 0)
-                        g.out_scales[(at * 2 * N + half * N + col0) / kCols] = bf16_rn(scale[half]);
+        before = sum;
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(kFullMask, before, d);
+            if (lane >= d) before += v;
+        }
+        __syncthreads();
+        if (lane == 31) s.scan[warp] = before;
+        __syncthreads();
+        int total = 0;
+        before -= sum;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s.scan[w];
+            total += s.scan[w];
+        }
+        if (most_n == 32 || static_cast<long long>(total) * across >= pairs) break;
+    }
+    for (int e = first; e < last; ++e) {
+        s.prefix[e] = before;
+        before += row_tiles(expert_rows(g.offsets, e, g.E / g.R, g.max_rows).count, most_n, &each);
+        if (e == g.E - 1) s.prefix[g.E] = before;
+    }
+    if (tid == 0) s.most_n = most_n;
+}
+
+// ---------------------------------------------------------------------------- finishing a tile
+
+// Two columns (rows of the output) at a time change places between neighbouring lanes (channels),
+// so that a lane moves two channels of one row: 4 bytes.
+__device__ __forceinline__ uint32_t lanes_to_row(float v0, float v1, bool odd) {
+    const uint32_t w = pack_bf16x2_rn(v0, v1), o = __shfl_xor_sync(kFullMask, w, 1);
+    return odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+}
+__device__ __forceinline__ void row_to_lanes(uint32_t w, bool odd, float& v0, float& v1) {
+    const uint32_t o = __shfl_xor_sync(kFullMask, w, 1);
+    v0 = odd ? bf16_hi(o) : bf16_lo(w);
+    v1 = odd ? bf16_hi(w) : bf16_lo(o);
+}
+// A 4 x 4 transpose of bytes among four neighbouring lanes: four codes of a lane's channel
+// become four channels' codes of one row, and back.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
+    const uint32_t a = __shfl_xor_sync(kFullMask, w, 1);
+    w = __byte_perm(w, a, lane & 1 ? 0x3715 : 0x6240);
+    const uint32_t b = __shfl_xor_sync(kFullMask, w, 2);
+    return __byte_perm(w, b, lane & 2 ? 0x3276 : 0x5410);
+}
+
+// v[j] of 32 rows from `to` on (this lane's channel, rows `stride` elements apart), as bf16
+__device__ __forceinline__ void store_rows(uint16_t* to, size_t stride, const float (&v)[32], int rows, bool there,
+                                           int lane) {
+    const bool odd = lane & 1;
+    to -= odd ? 1 : 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const uint32_t w = lanes_to_row(v[j], v[j + 1], odd);
+        const int row = j + (odd ? 1 : 0);
+        if (there && row < rows) *reinterpret_cast<uint32_t*>(to + row * stride) = w;
+    }
+}
+__device__ __forceinline__ void load_rows(float (&v)[32], const uint16_t* from, size_t stride, int rows, bool there,
+                                          int lane) {
+    const bool odd = lane & 1;
+    from -= odd ? 1 : 0;
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const int row = j + (odd ? 1 : 0);
+        w[j / 2] = there && row < rows ? __ldg(reinterpret_cast<const uint32_t*>(from + row * stride)) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) row_to_lanes(w[j / 2], odd, v[j], v[j + 1]);
+}
+
+// a checkpoint's codes times their scales; scales + row * scale_stride is the block's of a row
+__device__ __forceinline__ void load_codes(float (&v)[32], const uint8_t* from, size_t stride, const uint16_t* scales,
+                                           size_t scale_stride, int rows, bool there, int lane) {
+    from -= lane & 3;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const int row = j + (lane & 3);
+        w[j / 4] = there && row < rows ? __ldg(reinterpret_cast<const uint32_t*>(from + row * stride)) : 0;
+    }
+    const uint32_t mine = there && lane < rows ? static_cast<uint32_t>(__ldg(scales + lane * scale_stride)) << 16 : 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        float c[4];
+        e4m3x4_to_f32(transpose_bytes(w[j / 4], lane), c[0], c[1], c[2], c[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j + i] = c[i] * __uint_as_float(__shfl_sync(kFullMask, mine, j + i));
+    }
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) {  // 0 for NaN
+    return v == v ? __float_as_uint(v) & 0x7fffffffu : 0u;
+}
+
+// Scales and codes of 32 rows of one block of 128 channels; amax: lane j has row j's
+__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, uint16_t* scales, size_t scale_stride,
+                                            const float (&v)[32], float amax, int rows, bool there, bool writes_scale,
+                                            int lane) {
+    const float scale = checkpoint_scale(amax), rcp = checkpoint_rcp(scale);
+    if (writes_scale && there && lane < rows)
+        scales[lane * scale_stride] = static_cast<uint16_t>(__float_as_uint(scale) >> 16);
+    to -= lane & 3;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        float q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = checkpoint_quotient(v[j + i], __shfl_sync(kFullMask, scale, j + i),
+                                       __shfl_sync(kFullMask, rcp, j + i));
+        const uint32_t w = transpose_bytes(pack_e4m3x4_rn_sat(q[0], q[1], q[2], q[3]), lane);
+        const int row = j + (lane & 3);
+        if (there && row < rows) *reinterpret_cast<uint32_t*>(to + row * stride) = w;
+    }
+}
+
+// true in all 128 threads of a half of the finishing warps, or in none
+__device__ __forceinline__ bool half_agrees(bool ok, int half) {
+    int r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n"
+        " selp.s32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(static_cast<int>(ok)), "r"(1 + half)
+        : "memory");
+    return r != 0;
+}
+
+template <int kOp>
+__device__ __forceinline__ void finish_tile(const ExpertArgs& g, Shared& s, const Tile& t, uint32_t sums, int rank,
+                                            int warp, int lane) {
+    const int half = (warp - kFinish) / 4, quarter = warp % 4;
+    const int channel = t.channel + rank * 128 + quarter * 32 + lane;
+    const bool there = channel < g.C;
+    const size_t C = static_cast<size_t>(g.C);
+    sums += static_cast<uint32_t>(quarter * 32) << 16;
+    int buffer = 0;
+    for (int c0 = half * 32; c0 < t.n; c0 += 64) {
+        const int rows = t.rows - c0;  // of this chunk: 32 at most are looked at
+        float v[32];
+        if (t.k > 0) {
+            tmem_load32(v, sums + c0);
+            tmem_load_wait(v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        }
+        const size_t row = static_cast<size_t>(t.row) + c0;
+        if constexpr (kOp == kGateUp) {
+            float up[32];
+            tmem_load32(up, sums + 128 + c0);
+            tmem_load_wait(up);
+            if (g.out_pre != nullptr) {
+                store_rows(g.out_pre + row * 2 * C + channel, 2 * C, v, rows, there, lane);
+                store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, up, rows, there, lane);
+            }
+            if (g.out_q != nullptr) {
+                uint32_t gate_max = 0, up_max = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const uint32_t a = __reduce_max_sync(kFullMask, magnitude(v[j]));
+                    const uint32_t b = __reduce_max_sync(kFullMask, magnitude(up[j]));
+                    if (lane == j) gate_max = a, up_max = b;
+                }
+                float(&amax)[4][64] = s.amax[half][buffer];
+                amax[quarter][lane] = __uint_as_float(gate_max);
+                amax[quarter][32 + lane] = __uint_as_float(up_max);
+                asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+                float a = 0.0f, b = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    a = fmaxf(a, amax[w][lane]);
+                    b = fmaxf(b, amax[w][32 + lane]);
+                }
+                buffer ^= 1;
+                const size_t blocks = 2 * C / 128, block = row * blocks + (channel - lane) / 128;
+                store_codes(g.out_q + row * 2 * C + channel, 2 * C, g.out_scales + block, blocks, v, a, rows, there,
+                            quarter == 0, lane);
+                store_codes(g.out_q + row * 2 * C + C + channel, 2 * C, g.out_scales + block + C / 128, blocks, up, b,
+                            rows, there, quarter == 0, lane);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = v[j] * gate_of(v[j], g.act).s * up[j];
+            store_rows(g.out + row * C + channel, C, v, rows, there, lane);
+        } else if constexpr (kOp == kDownBwd) {
+            float gate[32], up[32];
+            if (g.pre != nullptr) {
+                load_rows(gate, g.pre + row * 2 * C + channel, 2 * C, rows, there, lane);
+                load_rows(up, g.pre + row * 2 * C + C + channel, 2 * C, rows, there, lane);
+            } else {
+                const size_t blocks = 2 * C / 128, block = row * blocks + channel / 128;
+                load_codes(gate, g.pre_q + row * 2 * C + channel, 2 * C, g.pre_scales + block, blocks, rows, there,
+                           lane);
+                load_codes(up, g.pre_q + row * 2 * C + C + channel, 2 * C, g.pre_scales + block + C / 128, blocks, rows,
+                           there, lane);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const Gate a = gate_of(gate[j], g.act);
+                const float act = gate[j] * a.s;
+                const float dgate = v[j] * up[j] * (a.s + act * (1.0f - a.s) * a.slope);
+                v[j] *= act;
+                up[j] *= act;  // h
+                gate[j] = dgate;
+            }
+            store_rows(g.out_pre + row * 2 * C + channel, 2 * C, gate, rows, there, lane);
+            store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, v, rows, there, lane);
+            if (g.out != nullptr) store_rows(g.out + row * C + channel, C, up, rows, there, lane);
+        } else if constexpr (kOp == kWgrad) {
+            const size_t at = static_cast<size_t>(t.e) * g.K + t.column + c0;
+            store_rows(g.out + at * C + channel, C, v, rows, there, lane);
+        } else {
+            store_rows(g.out + row * C + channel, C, v, rows, there, lane);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------- the kernel
+
+// `a`: the operand along the lanes, `b64` and `b16`: the one along the columns, in boxes of 64 rows
+// (or lines of k) and of 16.
+template <int kOp>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b64_map,
+                  const __grid_constant__ CUtensorMap b16_map, ExpertArgs g) {
+    using Tr = Traits<kOp>;
+    extern __shared__ __align__(1024) unsigned char s_stages[];
+    Shared& s = *reinterpret_cast<Shared*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    const int rank = static_cast<int>(cluster_rank());
+    const long long pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    if (tid == 0) {
+        for (int i = 0; i < g.stages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.ready[i], 2);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.sums_full[i], 1);
+            mbar_init(&s.sums_empty[i], 16);  // the finishing warps of both CTAs
+        }
+        mbar_init(&s.drain, 1);
+        mbar_init_fence();
+        s.stop = 0;
+        prefetch_tensor_map(a_map);
+        prefetch_tensor_map(b64_map);
+        prefetch_tensor_map(b16_map);
+    }
+    if (warp == kTail) tmem_alloc_pair(&s.tmem, kTmemColumns);
+    grid_dependency_wait();  // dependent launch: inputs are ready after this
+    if constexpr (kOp == kWgrad) {
+        if (blockIdx.x == 0)
+            for (int e = tid; e < g.E; e += kThreads)
+                if (expert_rows(g.offsets, e, g.E / g.R, g.max_rows).dropped) raise_flag(g.status, EP_FLAG_CAPACITY);
+    } else {
+        plan_tiles<kOp>(g, s);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+
+    if (warp == kProducer) {
+        if (lane == 0) {
+            int stage = 0, phase = 0;
+            long long issued = 0;
+            bool ok = true;
+            Tile t;
+            for (long long i = pair; ok && tile_at<kOp>(g, s, i, &t); i += pairs) {
+                const int half = t.n / 2, blocks = (t.k + kBlockK - 1) / kBlockK;
+                const int b_first = rank * half;
+                // bytes of this CTA's half of a stage: whole boxes, also where they hang over an end
+                const uint32_t b_bytes = kOp == kWgrad ? (half + 63) / 64 * kCrossBlock
+                                                       : static_cast<uint32_t>(half) * kBlockK * 2;
+                const uint32_t bytes = Tr::kABytes + b_bytes;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    ok = mbar_wait(&s.empty[stage], phase ^ 1, &s.stop);
+                    if (!ok) break;
+                    const uint32_t to = smem_addr(s_stages) + stage * Tr::kStageBytes;
+                    const uint32_t b_to = to + Tr::kABytes;
+                    const int k = kb * kBlockK, c = t.channel + rank * 128;
+                    uint32_t bar;
+                    if (kOp == kWgrad) {  // each CTA counts its own bytes: a tail is cleared there
+                        mbar_arrive_expect_tx(&s.full[stage], bytes);
+                        bar = smem_addr(&s.full[stage]);
+                    } else {  // CTA 0 counts both CTAs' bytes
+                        if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
+                        bar = peer_addr(&s.full[stage], 0);
+                    }
+                    if constexpr (kOp == kGateUp) {
+                        tma_load_pair_3d(to, a_map, k, c, 2 * t.e, bar);
+                        tma_load_pair_3d(to + 128 * kBlockK * 2, a_map, k, c, 2 * t.e + 1, bar);
+                    } else if constexpr (kOp == kDown) {
+                        tma_load_pair_3d(to, a_map, k, c, t.e, bar);
+                    } else {
+                        for (int i2 = 0; i2 < 2; ++i2) {
+                            if constexpr (kOp == kWgrad)
+                                tma_load_pair_2d(to + i2 * kCrossBlock, a_map, c + 64 * i2, static_cast<int>(t.row) + k,
+                                                 bar);
+                            else
+                                tma_load_pair_3d(to + i2 * kCrossBlock, a_map, c + 64 * i2, k, t.e, bar);
+                        }
+                    }
+                    if constexpr (kOp == kWgrad) {
+                        for (int j = 0; j * 64 < half; ++j)
+                            tma_load_pair_2d(b_to + j * kCrossBlock, b64_map, t.column + b_first + 64 * j,
+                                             static_cast<int>(t.row) + k, bar);
+                    } else {
+                        const int row = static_cast<int>(t.row) + b_first;
+                        int j = 0;
+                        for (; j + 64 <= half; j += 64)
+                            tma_load_pair_2d(b_to + j * kBlockK * 2, b64_map, k, row + j, bar);
+                        for (; j < half; j += 16) tma_load_pair_2d(b_to + j * kBlockK * 2, b16_map, k, row + j, bar);
+                    }
+                    ++issued;
+                    if (++stage == g.stages) stage = 0, phase ^= 1;
                 }
             }
-            for (int j = 0; j < 4; ++j) {
-                const int col = col0 + tx + 32 * j;
-                if (col >= g.N) continue;
-                const float v = c[0][i][j];
-                if (kOp == kGateUp) {
-                    const float up = c[kHalves - 1][i][j];
-                    g.out[at * N + col] = bf16_rn(v * gate_of(v, g.act).s * up);
-                    for (int half = 0; half < kHalves; ++half) {
-                        const size_t to = at * 2 * N + half * N + col;
-                        if (g.out_pre != nullptr) g.out_pre[to] = bf16_rn(c[half][i][j]);
-                        if (g.out_q != nullptr)
-                            g.out_q[to] = static_cast<uint8_t>(pack_e4m3x2_rn_sat(
-                                checkpoint_quotient(c[half][i][j], scale[half], rcp[half]), 0.0f));
+            if (!ok) s.stop = 1;
+            // The last stages are waited for: by their release, or where something gave up, by their
+            // bytes, so that no copy and no arrival is on its way when the CTA ends.
+            const int used = issued < g.stages ? static_cast<int>(issued) : g.stages;
+            for (int i = 0; i < used; ++i) {
+                if (stage == 0) phase ^= 1;
+                stage = stage == 0 ? g.stages - 1 : stage - 1;
+                if (ok && !mbar_wait(&s.empty[stage], phase, &s.stop)) ok = false;
+                if (!ok && (kOp == kWgrad || rank == 0)) mbar_wait(&s.full[stage], phase, nullptr);
+            }
+            if (!ok) {
+                s.stop = 1;
+                raise_flag(g.status, EP_FLAG_TIMEOUT);
+            }
+        }
+    } else if (warp == kMultiplier) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0, phase = 0;
+            uint32_t n_tile = 0;
+            bool ok = true;
+            Tile t;
+            for (long long i = pair; ok && tile_at<kOp>(g, s, i, &t); i += pairs) {
+                if (t.k == 0) continue;
+                const uint32_t at = n_tile % 2;
+                ok = mbar_wait(&s.sums_empty[at], (n_tile / 2 % 2) ^ 1, &s.stop);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t desc = product_desc(t.n, Tr::kAAcross, Tr::kBAcross);
+                const uint32_t sums = tmem + at * kStageColumns;
+                for (int k0 = 0; k0 < t.k; k0 += kBlockK) {
+                    ok = mbar_wait(kOp == kWgrad ? &s.ready[stage] : &s.full[stage], phase, &s.stop);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t from = smem_addr(s_stages) + stage * Tr::kStageBytes;
+                    uint64_t a = operand_desc(from, Tr::kAAcross);
+                    uint64_t up = operand_desc(from + 128 * kBlockK * 2, Tr::kAAcross);
+                    uint64_t b = operand_desc(from + Tr::kABytes, Tr::kBAcross);
+                    const int steps = t.k - k0 < kBlockK ? (t.k - k0 + 15) / 16 : kBlockK / 16;
+                    for (int j = 0; j < steps; ++j) {
+                        mma_pair(sums, a, b, desc, k0 + j > 0);
+                        if (Tr::kGated) mma_pair(sums + 128, up, b, desc, k0 + j > 0);
+                        a += Tr::kAAcross ? kStepAcross : kStepAlong;
+                        up += Tr::kAAcross ? kStepAcross : kStepAlong;
+                        b += Tr::kBAcross ? kStepAcross : kStepAlong;
                     }
-                } else if (kOp == kDownBwd) {
-                    float of[2];
-                    for (int half = 0; half < 2; ++half) {
-                        const size_t from = at * 2 * N + half * N + col;
-                        if (g.pre != nullptr)
-                            of[half] = bf16_at(g.pre, from);
-                        else
-                            of[half] = f16_to_f32(e4m3x2_to_f16x2(g.pre_q[from]) & 0xffffu) *
-                                       bf16_at(g.pre_scales, from / kCols);
-                    }
-                    const Gate s = gate_of(of[0], g.act);
-                    const float act = of[0] * s.s;
-                    g.out_pre[at * 2 * N + col] = bf16_rn(v * of[1] * (s.s + act * (1.0f - s.s) * s.slope));
-                    g.out_pre[at * 2 * N + N + col] = bf16_rn(v * act);
-                    if (g.out != nullptr) g.out[at * N + col] = bf16_rn(act * of[1]);
-                } else {
-                    g.out[at * N + col] = bf16_rn(v);
+                    mma_commit_pair(&s.empty[stage]);
+                    if (++stage == g.stages) stage = 0, phase ^= 1;
                 }
+                if (!ok) break;
+                mma_commit_pair(&s.sums_full[at]);
+                ++n_tile;
+            }
+            if (!ok) {  // the products that were begun still read shared memory
+                s.stop = 1;
+                mma_commit_pair(&s.drain);
+                mbar_wait(&s.drain, 0, nullptr);
+            }
+        }
+    } else if (warp == kTail) {
+        if constexpr (kOp == kWgrad) {
+            // k is an expert's rows: what lies behind the last of them in its last stage, other experts'
+            // rows or whatever a slab's end holds, is cleared before it is multiplied
+            int stage = 0, phase = 0;
+            bool ok = true;
+            Tile t;
+            for (long long i = pair; ok && tile_at<kOp>(g, s, i, &t); i += pairs) {
+                const int b_blocks = (t.n / 2 + 63) / 64;
+                for (int k0 = 0; k0 < t.k; k0 += kBlockK) {
+                    ok = mbar_wait(&s.full[stage], phase, &s.stop);
+                    if (!__all_sync(kFullMask, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const int left = t.k - k0;
+                    if (left < kBlockK && left % 16 != 0) {
+                        unsigned char* const at = s_stages + static_cast<size_t>(stage) * Tr::kStageBytes;
+                        const int lines = 16 - left % 16;  // up to the end of the last 16 k
+                        for (int n = lane; n < (2 + b_blocks) * lines * 8; n += 32) {
+                            const int block = n / (lines * 8), line = left + n / 8 % lines;
+                            *reinterpret_cast<uint4*>(at + block * kCrossBlock + line * 128 + n % 8 * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(peer_addr(&s.ready[stage], 0));
+                    if (++stage == g.stages) stage = 0, phase ^= 1;
+                }
+            }
+            if (!ok) s.stop = 1;
+        }
+    } else if (warp >= kFinish) {
+        const int half = (warp - kFinish) / 4;
+        uint32_t n_tile = 0;
+        Tile t;
+        for (long long i = pair; tile_at<kOp>(g, s, i, &t); i += pairs) {
+            const uint32_t at = n_tile % 2;
+            if (t.k > 0) {
+                const bool ok = mbar_wait(&s.sums_full[at], n_tile / 2 % 2, &s.stop);
+                if (!half_agrees(ok, half)) {
+                    s.stop = 1;
+                    break;
+                }
+                tc_fence_after();
+            }
+            finish_tile<kOp>(g, s, t, tmem + at * kStageColumns, rank, warp, lane);
+            if (t.k > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(peer_addr(&s.sums_empty[at], 0));
+                ++n_tile;
             }
         }
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA's shared or tensor memory is used by the other any more
+    if (warp == kTail) {
+        tc_fence_after();
+        tmem_free_pair(tmem, kTmemColumns);
+    }
+    cluster_sync();
 }
 
 bool valid(int E, int R, int max_rows) {
@@ -149,11 +597,39 @@ bool valid(int E, int R, int max_rows) {
 bool valid_width(int n, int most) { return n >= 8 && n <= most && n % 8 == 0; }
 constexpr int kMostWidth = 65536;
 
+ep_status_t zero_fill(void* p, size_t bytes, void* stream) {
+    const cudaError_t err = cudaMemsetAsync(p, 0, bytes, as_stream(stream));
+    return err == cudaSuccess ? EP_OK : cuda_fail(err);
+}
+
+// A map of bf16 `dims` (innermost first, dense), in boxes of 64 values by `lines`, swizzled for the
+// tensor cores.
+ep_status_t map_of(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t lines) {
+    const uint64_t dims[3] = {d0, d1, d2}, strides[2] = {d0 * 2, d0 * d1 * 2};
+    const uint32_t box[3] = {64, lines, 1};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d2 == 0 ? 2 : 3, base, dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <int kOp>
-ep_status_t launch(const ExpertArgs& g, void* stream) {
-    const dim3 grid((g.N + kCols - 1) / kCols, g.E);
-    expert_kernel<kOp><<<grid, kThreads, 0, as_stream(stream)>>>(g);
-    return check_launch();
+ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, const CUtensorMap& b16, void* stream) {
+    using Tr = Traits<kOp>;
+    static std::atomic<int> ready[kMaxDevices];
+    const size_t behind = sizeof(Shared) + (kOp == kWgrad ? 0 : sizeof(int) * static_cast<size_t>(g.E));
+    g.stages = static_cast<int>((kSmemMost - behind) / Tr::kStageBytes);
+    if (g.stages > kMostStages) g.stages = kMostStages;
+    const ep_status_t st = ensure_dynamic_smem(ready, expert_kernel<kOp>, static_cast<int>(kSmemMost));
+    if (st != EP_OK) return st;
+    const dim3 grid(static_cast<unsigned>(sm_count() / 2 * 2));
+    return launch_dependent(expert_kernel<kOp>, grid, dim3(kThreads), g.stages * Tr::kStageBytes + behind,
+                            as_stream(stream), a, b64, b16, g);
+}
+
+// Rows of the slabs as the operand along the columns: in boxes of 64 rows and of 16.
+ep_status_t row_maps(CUtensorMap* b64, CUtensorMap* b16, const void* rows, uint64_t width, const ExpertArgs& g) {
+    const uint64_t n = static_cast<uint64_t>(g.R) * g.max_rows;
+    const ep_status_t st = map_of(b64, rows, width, n, 0, 64);
+    return st != EP_OK ? st : map_of(b16, rows, width, n, 0, 16);
 }
 
 }  // namespace
@@ -172,11 +648,9 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
         !aligned16_or_null(pre) || !aligned16_or_null(pre_q) || !aligned16_or_null(pre_scales))
         return EP_ERR_INVALID;
     ExpertArgs g = {};
-    g.a = static_cast<const uint16_t*>(x);
-    g.b = static_cast<const uint16_t*>(w_gate_up);
     g.offsets = expert_offsets;
     g.act = act;
-    g.N = F;
+    g.C = F;
     g.K = H;
     g.E = E;
     g.R = R;
@@ -186,7 +660,10 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
     g.out_q = pre_q;
     g.out_scales = static_cast<uint16_t*>(pre_scales);
     g.status = status;
-    return launch<kGateUp>(g, stream);
+    CUtensorMap a, b64, b16;
+    ep_status_t st = map_of(&a, w_gate_up, H, F, 2ull * E, 128);
+    if (st == EP_OK) st = row_maps(&b64, &b16, x, H, g);
+    return st != EP_OK ? st : launch<kGateUp>(g, a, b64, b16, stream);
 }
 
 ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* expert_offsets, int32_t H, int32_t F,
@@ -196,17 +673,18 @@ ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* exp
     if (h == nullptr || w_down == nullptr || expert_offsets == nullptr || y == nullptr) return EP_ERR_INVALID;
     if (!aligned16(h) || !aligned16(w_down) || !aligned16(expert_offsets) || !aligned16(y)) return EP_ERR_INVALID;
     ExpertArgs g = {};
-    g.a = static_cast<const uint16_t*>(h);
-    g.b = static_cast<const uint16_t*>(w_down);
     g.offsets = expert_offsets;
-    g.N = H;
+    g.C = H;
     g.K = F;
     g.E = E;
     g.R = R;
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(y);
     g.status = status;
-    return launch<kDown>(g, stream);
+    CUtensorMap a, b64, b16;
+    ep_status_t st = map_of(&a, w_down, F, H, E, 128);
+    if (st == EP_OK) st = row_maps(&b64, &b16, h, F, g);
+    return st != EP_OK ? st : launch<kDown>(g, a, b64, b16, stream);
 }
 
 ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* pre, const uint8_t* pre_q,
@@ -223,14 +701,12 @@ ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* p
         !aligned16_or_null(pre) || !aligned16_or_null(pre_q) || !aligned16_or_null(pre_scales) || !aligned16_or_null(h))
         return EP_ERR_INVALID;
     ExpertArgs g = {};
-    g.a = static_cast<const uint16_t*>(dy);
-    g.b = static_cast<const uint16_t*>(w_down);
     g.pre = static_cast<const uint16_t*>(pre);
     g.pre_q = pre_q;
     g.pre_scales = static_cast<const uint16_t*>(pre_scales);
     g.offsets = expert_offsets;
     g.act = act;
-    g.N = F;
+    g.C = F;
     g.K = H;
     g.E = E;
     g.R = R;
@@ -238,7 +714,10 @@ ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* p
     g.out = static_cast<uint16_t*>(h);
     g.out_pre = static_cast<uint16_t*>(dpre);
     g.status = status;
-    return launch<kDownBwd>(g, stream);
+    CUtensorMap a, b64, b16;
+    ep_status_t st = map_of(&a, w_down, F, H, E, 64);
+    if (st == EP_OK) st = row_maps(&b64, &b16, dy, H, g);
+    return st != EP_OK ? st : launch<kDownBwd>(g, a, b64, b16, stream);
 }
 
 ep_status_t ep_expert_gate_up_bwd(const void* dpre, const void* w_gate_up, const int32_t* expert_offsets, int32_t H,
@@ -250,17 +729,18 @@ ep_status_t ep_expert_gate_up_bwd(const void* dpre, const void* w_gate_up, const
     if (!aligned16(dpre) || !aligned16(w_gate_up) || !aligned16(expert_offsets) || !aligned16(dx))
         return EP_ERR_INVALID;
     ExpertArgs g = {};
-    g.a = static_cast<const uint16_t*>(dpre);
-    g.b = static_cast<const uint16_t*>(w_gate_up);
     g.offsets = expert_offsets;
-    g.N = H;
+    g.C = H;
     g.K = 2 * F;
     g.E = E;
     g.R = R;
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(dx);
     g.status = status;
-    return launch<kGateUpBwd>(g, stream);
+    CUtensorMap a, b64, b16;
+    ep_status_t st = map_of(&a, w_gate_up, H, 2ull * F, E, 64);
+    if (st == EP_OK) st = row_maps(&b64, &b16, dpre, 2ull * F, g);
+    return st != EP_OK ? st : launch<kGateUpBwd>(g, a, b64, b16, stream);
 }
 
 ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* expert_offsets, int32_t I, int32_t J,
@@ -272,17 +752,20 @@ ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* e
     if (max_rows > 0 && (dout == nullptr || rows == nullptr || !aligned16(dout) || !aligned16(rows)))
         return EP_ERR_INVALID;
     ExpertArgs g = {};
-    g.a = static_cast<const uint16_t*>(dout);
-    g.b = static_cast<const uint16_t*>(rows);
     g.offsets = expert_offsets;
-    g.N = J;
+    g.C = J;
     g.K = I;
     g.E = E;
     g.R = R;
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(dw);
     g.status = status;
-    return launch<kWgrad>(g, stream);
+    if (max_rows == 0) return zero_fill(dw, static_cast<size_t>(E) * I * J * 2, stream);
+    const uint64_t n = static_cast<uint64_t>(R) * max_rows;
+    CUtensorMap a, b;
+    ep_status_t st = map_of(&a, rows, J, n, 0, 64);
+    if (st == EP_OK) st = map_of(&b, dout, I, n, 0, 64);
+    return st != EP_OK ? st : launch<kWgrad>(g, a, b, b, stream);
 }
 
 }  // extern "C"

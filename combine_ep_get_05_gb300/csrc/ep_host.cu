@@ -41,7 +41,8 @@ std::atomic<EncodeTiledFn> g_encode_tiled{nullptr};
 }  // namespace
 
 ep_status_t encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t elem_bytes, uint32_t rank,
-                              const void* base, const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+                              const void* base, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                              CUtensorMapSwizzle swizzle) {
     if (rank < 1 || rank > 5 || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) return EP_ERR_INVALID;
     if ((static_cast<uint64_t>(box[0]) * elem_bytes) % 16 != 0) return EP_ERR_INVALID;
     for (uint32_t i = 0; i < rank; ++i) {
@@ -67,7 +68,7 @@ ep_status_t encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, uint32
         if (i + 1 < rank) s[i] = strides[i];
     }
     const CUresult r = fn(map, type, rank, const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? EP_OK : cuda_fail(cudaErrorInvalidValue);
 }

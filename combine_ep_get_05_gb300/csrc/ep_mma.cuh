@@ -1,0 +1,146 @@
+// ep_mma.cuh -- tensor-core products of a pair of CTAs (tcgen05, cta_group::2): descriptors,
+// the instruction, tensor memory, and the barriers between the two CTAs. Internal header.
+//
+// A pair multiplies M = 256 rows of A (128 from each CTA's shared memory) with N columns of B
+// (N/2 from each), 16 k at a time, into tensor memory: CTA 0 holds rows 0 .. 127, CTA 1 rows
+// 128 .. 255, a row a lane, a column a 32-bit column. Operands lie in shared memory as 128-byte
+// swizzled tensor copies leave them, in one of two ways:
+//   along k:       rows of 64 k (128 bytes), 8 rows an atom of 1024 bytes
+//   across k:      blocks of 64 rows of the operand: 64 lines of one k each, 64 values a line
+#pragma once
+
+#include "ep_tma.cuh"
+
+namespace ep {
+
+constexpr int kBlockK = 64;                    // k of a stage: 128 bytes of bf16
+constexpr uint32_t kCrossBlock = 64 * 64 * 2;  // bytes of a block of 64 rows by 64 k, across k
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address, in the cluster's window, of `p`'s counterpart in CTA `rank`
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// one poll of a barrier's phase; the poll itself waits a little in hardware
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Waits until the phase is over; gives up after about 2 s, or once *stop is set, and returns false.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* stop) {
+    if (mbar_try(bar, parity)) return true;
+    const unsigned long long start = globaltimer_ns();
+    for (uint32_t i = 0; i < (1u << 26); ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if ((i & 63u) == 63u && ((stop != nullptr && *stop != 0) || globaltimer_ns() - start > 2000000000ull)) break;
+    }
+    return false;
+}
+
+// tensor loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)
+__device__ __forceinline__ void tma_load_pair_2d(uint32_t dst, const CUtensorMap& map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap_addr(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap& map, int x, int y, int z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap_addr(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// tensor memory: `columns` for the pair, the address into *at (shared); one warp of each CTA
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* at, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t at, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory operand descriptor: address and strides in units of 16 bytes, version 1, 128-byte
+// swizzle. Along k an atom of 8 rows follows another every 1024 bytes (and 16 k are 32 bytes
+// further); across k, 8 lines of k are 1024 bytes and a block of 64 rows kCrossBlock (and 16 k
+// are 16 lines, 2048 bytes, further).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool across) {
+    const uint64_t leading = across ? kCrossBlock >> 4 : 1;
+    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | leading << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+constexpr uint64_t kStepAlong = 32 >> 4, kStepAcross = 2048 >> 4;  // a descriptor's, per 16 k
+
+// Instruction descriptor: bf16 operands, fp32 sums, M = 256, N columns; bits 15 and 16: A, B across k.
+__device__ __forceinline__ uint32_t product_desc(int n, bool a_across, bool b_across) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (a_across ? 1u << 15 : 0u) | (b_across ? 1u << 16 : 0u) |
+           static_cast<uint32_t>(n >> 3) << 17 | (256u >> 4) << 24;
+}
+// D (+)= A B^T over 16 k; one thread of CTA 0, for the pair
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// arrives on the barrier, in both CTAs, when the thread's products so far are done
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// 32 columns of the warp's 32 lanes (lane quarter of the warp): v[j] = column j of this thread's lane
+__device__ __forceinline__ void tmem_load32(float (&v)[32], uint32_t at) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+// until the loads are done; the values are used only after it
+__device__ __forceinline__ void tmem_load_wait(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
+                   "+f"(v[31])
+                 :
+                 : "memory");
+}
+
+}  // namespace ep

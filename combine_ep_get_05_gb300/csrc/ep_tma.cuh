@@ -9,8 +9,8 @@
 // dimension's end read zeros, and a box store skips elements past the end. Rules the
 // host checks before encoding: the base address and every stride are multiples of 16
 // bytes, dimension 0 of a box spans a multiple of 16 bytes, every box dimension is at
-// most 256 elements; the device side only ever uses x = 0 (aligned) and non-negative
-// coordinates.
+// most 256 elements; the device side only ever uses aligned x (0, or multiples of 16 bytes) and
+// non-negative coordinates.
 #pragma once
 
 #include <cuda.h>
@@ -23,7 +23,8 @@ namespace ep {
 // elem_bytes, strides[i] = byte stride of dimension i + 1). Returns EP_OK, EP_ERR_INVALID
 // when the shape breaks a rule above, or EP_ERR_CUDA when the driver refuses it.
 ep_status_t encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t elem_bytes, uint32_t rank,
-                              const void* base, const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
+                              const void* base, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 // ---------------------------------------------------------------- device side
 
