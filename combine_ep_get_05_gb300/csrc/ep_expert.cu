@@ -18,11 +18,12 @@ using namespace ep;
 enum Op { kGateUp, kDown, kDownBwd, kGateUpBwd, kWgrad };
 
 constexpr int kThreads = 384;        // 4 warps that feed and multiply, 8 that finish tiles
-constexpr int kProducer = 0, kMultiplier = 1, kTail = 2, kFinish = 4;  // first warp of each part
-constexpr int kHalfThreads = 128;    // 4 finishing warps: the 128 lanes of every other 32 columns
+constexpr int kProducer = 0, kMultiplier = 1, kTail = 2, kScheduler = 3, kFinish = 4;  // first warp of each part
 constexpr uint32_t kTmemColumns = 512;
-constexpr uint32_t kStageColumns = 256;  // of tensor memory: two tiles at a time
+constexpr uint32_t kSlotColumns = 256;  // of tensor memory: two tiles at a time
 constexpr int kMostStages = 8;
+constexpr int kTiles = 4;  // that are planned ahead
+constexpr int kMostN = 256;  // rows of an expert a tile
 constexpr size_t kSmemMost = 227 * 1024;
 
 template <int kOp>
@@ -30,7 +31,6 @@ struct Traits {
     static constexpr bool kGated = kOp == kGateUp;
     static constexpr bool kAAcross = kOp == kDownBwd || kOp == kGateUpBwd || kOp == kWgrad;
     static constexpr bool kBAcross = kOp == kWgrad;
-    static constexpr int kMostN = kGated ? 128 : 256;           // rows of an expert a tile
     static constexpr uint32_t kABytes = (kGated ? 2 : 1) * 128 * kBlockK * 2;
     static constexpr uint32_t kBBytes = kMostN / 2 * kBlockK * 2;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes;  // of one CTA
@@ -54,8 +54,8 @@ struct ExpertArgs {
 // A tile: 256 channels (128 a CTA) of up to kMostN rows of an expert; in kWgrad, of up to
 // kMostN rows of its gradient.
 struct Tile {
-    int e;
     long long row;  // first row of the slabs; kWgrad: the expert's
+    int e;          // -1: there are no more tiles
     int rows;       // rows that are there (columns of the sums that are kept)
     int n;          // columns that are multiplied: a multiple of 32
     int channel;    // first of the pair's
@@ -64,14 +64,32 @@ struct Tile {
 };
 
 struct Shared {  // behind the stages
-    uint64_t full[kMostStages], ready[kMostStages], empty[kMostStages];
-    uint64_t sums_full[2], sums_empty[2], drain;
+    // a stage's bytes have come (CTA 0: both CTAs'), its products are done; a last stage of
+    // kWgrad: the CTA's own bytes have come, both CTAs have cleared its tail
+    uint64_t full[kMostStages], empty[kMostStages], part[kMostStages], ready[kMostStages];
+    uint64_t sums_full[2], sums_empty[2], tile_full[kTiles], tile_empty[kTiles], drain;
+    Tile tile[kTiles];
     uint32_t tmem;
-    int stop;        // a wait gave up
-    int most_n;      // rows a tile, of this call
-    int scan[kThreads / 32];
+    int stop;    // a wait gave up
+    int most_n;  // rows a tile, of this call
+    int scan[4][kThreads / 32];
     float amax[2][2][4][64];  // [half][buffer][warp][gate and up of 32 columns]
-    int prefix[1];   // [E + 1] tiles of rows before each expert's (but kWgrad)
+    int prefix[1];            // [E + 1] tiles of rows before each expert's (but kWgrad)
+};
+
+// The tiles of a role, in order. next() is false where there are no more, or a wait gave up (`ok`);
+// taken(), by one thread after all of the role's have read the tile, lets its place be used again.
+struct Tiles {
+    uint32_t at = kTiles - 1, phase = 1;
+    bool ok = true;
+    __device__ __forceinline__ bool next(Shared& s, Tile* t) {
+        if (++at == kTiles) at = 0, phase ^= 1;
+        ok = mbar_wait(&s.tile_full[at], phase, &s.stop);
+        if (!ok) return false;
+        *t = s.tile[at];
+        return t->e >= 0;
+    }
+    __device__ __forceinline__ void taken(Shared& s) { mbar_arrive(&s.tile_empty[at]); }
 };
 
 __device__ __forceinline__ int row_tiles(int count, int most_n, int* each) {
@@ -128,44 +146,49 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared& s, lo
     return true;
 }
 
-// The number of tiles of rows before each expert's, by all threads. Rows a tile are halved while
-// the tiles would not fill the GPU.
-template <int kOp>
+// The number of tiles of rows before each expert's, by all threads. A tile has 256 rows at
+// most, or 128, 64 or 32 where the tiles would not fill the GPU otherwise.
 __device__ void plan_tiles(const ExpertArgs& g, Shared& s) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     const int per = (g.E + kThreads - 1) / kThreads, first = tid * per;
     const int last = first + per < g.E ? first + per : g.E;
     const int across = (g.C + 255) / 256, pairs = static_cast<int>(gridDim.x / 2);
-    int each, before, sum, most_n = Traits<kOp>::kMostN;
-    for (;; most_n /= 2) {
-        sum = 0;
-        for (int e = first; e < last; ++e) {
-            const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
-            if (r.dropped && blockIdx.x == 0 && most_n == Traits<kOp>::kMostN) raise_flag(g.status, EP_FLAG_CAPACITY);
-            sum += row_tiles(r.count, most_n, &each);
-        }
-        before = sum;
-        for (int d = 1; d < 32; d *= 2) {
-            const int v = __shfl_up_sync(kFullMask, before, d);
-            if (lane >= d) before += v;
-        }
-        __syncthreads();
-        if (lane == 31) s.scan[warp] = before;
-        __syncthreads();
-        int total = 0;
-        before -= sum;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += s.scan[w];
-            total += s.scan[w];
-        }
-        if (most_n == 32 || static_cast<long long>(total) * across >= pairs) break;
+    int each, count = 0, sum[4] = {0, 0, 0, 0};
+    for (int e = first; e < last; ++e) {
+        const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        if (r.dropped && blockIdx.x == 0) raise_flag(g.status, EP_FLAG_CAPACITY);
+        count = r.count;
+        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(count, kMostN >> i, &each);
     }
+    for (int i = 0; i < 4; ++i) {
+        const int n = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(sum[i])));
+        if (lane == 0) s.scan[i][warp] = n;
+    }
+    __syncthreads();
+    int choice = 0, before = 0, mine = 0;
+    for (; choice < 4; ++choice) {
+        int total = 0;
+        before = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s.scan[choice][w];
+            total += s.scan[choice][w];
+        }
+        mine = choice == 0 ? sum[0] : choice == 1 ? sum[1] : choice == 2 ? sum[2] : sum[3];
+        if (choice == 3 || static_cast<long long>(total) * across >= pairs) break;
+    }
+    int upto = mine;
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(kFullMask, upto, d);
+        if (lane >= d) upto += v;
+    }
+    before += upto - mine;
     for (int e = first; e < last; ++e) {
         s.prefix[e] = before;
-        before += row_tiles(expert_rows(g.offsets, e, g.E / g.R, g.max_rows).count, most_n, &each);
+        if (per > 1) count = expert_rows(g.offsets, e, g.E / g.R, g.max_rows).count;
+        before += row_tiles(count, kMostN >> choice, &each);
         if (e == g.E - 1) s.prefix[g.E] = before;
     }
-    if (tid == 0) s.most_n = most_n;
+    if (tid == 0) s.most_n = kMostN >> choice;
 }
 
 // ---------------------------------------------------------------------------- finishing a tile
@@ -274,13 +297,14 @@ __device__ __forceinline__ bool half_agrees(bool ok, int half) {
 }
 
 template <int kOp>
-__device__ __forceinline__ void finish_tile(const ExpertArgs& g, Shared& s, const Tile& t, uint32_t sums, int rank,
-                                            int warp, int lane) {
+__device__ __forceinline__ void finish_tile(const ExpertArgs& g, Shared& s, const Tile& t, uint32_t sums, uint32_t ups,
+                                            int rank, int warp, int lane) {
     const int half = (warp - kFinish) / 4, quarter = warp % 4;
     const int channel = t.channel + rank * 128 + quarter * 32 + lane;
     const bool there = channel < g.C;
     const size_t C = static_cast<size_t>(g.C);
     sums += static_cast<uint32_t>(quarter * 32) << 16;
+    ups += static_cast<uint32_t>(quarter * 32) << 16;
     int buffer = 0;
     for (int c0 = half * 32; c0 < t.n; c0 += 64) {
         const int rows = t.rows - c0;  // of this chunk: 32 at most are looked at
@@ -295,7 +319,7 @@ __device__ __forceinline__ void finish_tile(const ExpertArgs& g, Shared& s, cons
         const size_t row = static_cast<size_t>(t.row) + c0;
         if constexpr (kOp == kGateUp) {
             float up[32];
-            tmem_load32(up, sums + 128 + c0);
+            tmem_load32(up, ups + c0);
             tmem_load_wait(up);
             if (g.out_pre != nullptr) {
                 store_rows(g.out_pre + row * 2 * C + channel, 2 * C, v, rows, there, lane);
@@ -364,6 +388,19 @@ __device__ __forceinline__ void finish_tile(const ExpertArgs& g, Shared& s, cons
 
 // ---------------------------------------------------------------------------- the kernel
 
+// whether the last k of a stage do not fill their 16 (kWgrad, where k are rows)
+__device__ __forceinline__ bool has_tail(int left) { return left < kBlockK && left % 16 != 0; }
+
+// Tensor memory of a tile: one of two slots, gate and up side by side; a gated tile of more than
+// 128 rows takes both.
+template <int kOp>
+__device__ __forceinline__ uint32_t slots_of(const Tile& t) {
+    return Traits<kOp>::kGated && t.n > static_cast<int>(kSlotColumns / 2) ? 2 : 1;
+}
+__device__ __forceinline__ uint32_t up_sums(uint32_t tmem, uint32_t first, uint32_t slots) {
+    return slots == 2 ? tmem + (first + 1) % 2 * kSlotColumns : tmem + first % 2 * kSlotColumns + kSlotColumns / 2;
+}
+
 // `a`: the operand along the lanes, `b64` and `b16`: the one along the columns, in boxes of 64 rows
 // (or lines of k) and of 16.
 template <int kOp>
@@ -380,12 +417,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < g.stages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.ready[i], 2);
             mbar_init(&s.empty[i], 1);
+            mbar_init(&s.part[i], 1);
+            mbar_init(&s.ready[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.sums_full[i], 1);
             mbar_init(&s.sums_empty[i], 16);  // the finishing warps of both CTAs
+        }
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(&s.tile_full[i], 1);
+            mbar_init(&s.tile_empty[i], 9 + (rank == 0 ? 1 : 0) + (kOp == kWgrad ? 1 : 0));
         }
         mbar_init(&s.drain, 1);
         mbar_init_fence();
@@ -401,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int e = tid; e < g.E; e += kThreads)
                 if (expert_rows(g.offsets, e, g.E / g.R, g.max_rows).dropped) raise_flag(g.status, EP_FLAG_CAPACITY);
     } else {
-        plan_tiles<kOp>(g, s);
+        plan_tiles(g, s);
     }
     tc_fence_before();
     __syncthreads();
@@ -409,32 +451,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
 
-    if (warp == kProducer) {
+    Tile t;
+    Tiles tiles;
+    if (warp == kScheduler) {
         if (lane == 0) {
-            int stage = 0, phase = 0;
+            uint32_t at = 0, phase = 0;
+            for (long long i = pair;; i += pairs) {
+                const bool more = tile_at<kOp>(g, s, i, &t);
+                if (!more) t.e = -1;
+                if (!mbar_wait(&s.tile_empty[at], phase ^ 1, &s.stop)) {
+                    s.stop = 1;
+                    break;
+                }
+                s.tile[at] = t;
+                mbar_arrive(&s.tile_full[at]);
+                if (++at == kTiles) at = 0, phase ^= 1;
+                if (!more) break;
+            }
+        }
+    } else if (warp == kProducer) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
             long long issued = 0;
             bool ok = true;
-            Tile t;
-            for (long long i = pair; ok && tile_at<kOp>(g, s, i, &t); i += pairs) {
-                const int half = t.n / 2, blocks = (t.k + kBlockK - 1) / kBlockK;
+            while (ok && tiles.next(s, &t)) {
+                tiles.taken(s);
+                const int half = t.n / 2;
                 const int b_first = rank * half;
                 // bytes of this CTA's half of a stage: whole boxes, also where they hang over an end
                 const uint32_t b_bytes = kOp == kWgrad ? (half + 63) / 64 * kCrossBlock
                                                        : static_cast<uint32_t>(half) * kBlockK * 2;
                 const uint32_t bytes = Tr::kABytes + b_bytes;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    ok = mbar_wait(&s.empty[stage], phase ^ 1, &s.stop);
+                for (int k = 0; k < t.k; k += kBlockK) {
+                    ok = mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop);
                     if (!ok) break;
+                    empty ^= 1u << stage;
                     const uint32_t to = smem_addr(s_stages) + stage * Tr::kStageBytes;
                     const uint32_t b_to = to + Tr::kABytes;
-                    const int k = kb * kBlockK, c = t.channel + rank * 128;
+                    const int c = t.channel + rank * 128;
                     uint32_t bar;
-                    if (kOp == kWgrad) {  // each CTA counts its own bytes: a tail is cleared there
-                        mbar_arrive_expect_tx(&s.full[stage], bytes);
-                        bar = smem_addr(&s.full[stage]);
+                    if (kOp == kWgrad && has_tail(t.k - k)) {  // each CTA counts its own bytes: it clears them
+                        mbar_arrive_expect_tx(&s.part[stage], bytes);
+                        bar = smem_addr(&s.part[stage]);
+                        part ^= 1u << stage;
+                        last_part |= 1u << stage;
                     } else {  // CTA 0 counts both CTAs' bytes
                         if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
                         bar = peer_addr(&s.full[stage], 0);
+                        full ^= 1u << stage;
+                        last_part &= ~(1u << stage);
                     }
                     if constexpr (kOp == kGateUp) {
                         tma_load_pair_3d(to, a_map, k, c, 2 * t.e, bar);
@@ -442,12 +508,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else if constexpr (kOp == kDown) {
                         tma_load_pair_3d(to, a_map, k, c, t.e, bar);
                     } else {
-                        for (int i2 = 0; i2 < 2; ++i2) {
+                        for (int j = 0; j < 2; ++j) {
                             if constexpr (kOp == kWgrad)
-                                tma_load_pair_2d(to + i2 * kCrossBlock, a_map, c + 64 * i2, static_cast<int>(t.row) + k,
+                                tma_load_pair_2d(to + j * kCrossBlock, a_map, c + 64 * j, static_cast<int>(t.row) + k,
                                                  bar);
                             else
-                                tma_load_pair_3d(to + i2 * kCrossBlock, a_map, c + 64 * i2, k, t.e, bar);
+                                tma_load_pair_3d(to + j * kCrossBlock, a_map, c + 64 * j, k, t.e, bar);
                         }
                     }
                     if constexpr (kOp == kWgrad) {
@@ -462,18 +528,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (; j < half; j += 16) tma_load_pair_2d(b_to + j * kBlockK * 2, b16_map, k, row + j, bar);
                     }
                     ++issued;
-                    if (++stage == g.stages) stage = 0, phase ^= 1;
+                    if (++stage == g.stages) stage = 0;
                 }
             }
+            ok = ok && tiles.ok;
             if (!ok) s.stop = 1;
-            // The last stages are waited for: by their release, or where something gave up, by their
-            // bytes, so that no copy and no arrival is on its way when the CTA ends.
+            // The last use of every stage is waited for: by its release, or where something gave up, by
+            // its bytes, so that no copy and no arrival is on its way when the CTA ends.
             const int used = issued < g.stages ? static_cast<int>(issued) : g.stages;
             for (int i = 0; i < used; ++i) {
-                if (stage == 0) phase ^= 1;
                 stage = stage == 0 ? g.stages - 1 : stage - 1;
-                if (ok && !mbar_wait(&s.empty[stage], phase, &s.stop)) ok = false;
-                if (!ok && (kOp == kWgrad || rank == 0)) mbar_wait(&s.full[stage], phase, nullptr);
+                if (ok && !mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop)) ok = false;
+                if (ok) continue;
+                if (last_part >> stage & 1)
+                    mbar_wait(&s.part[stage], (part >> stage & 1) ^ 1, nullptr);
+                else if (rank == 0)
+                    mbar_wait(&s.full[stage], (full >> stage & 1) ^ 1, nullptr);
             }
             if (!ok) {
                 s.stop = 1;
@@ -482,42 +552,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMultiplier) {
         if (lane == 0 && rank == 0) {
-            int stage = 0, phase = 0;
-            uint32_t n_tile = 0;
+            int stage = 0;
+            uint32_t full = 0, ready = 0, slot = 0;
             bool ok = true;
-            Tile t;
-            for (long long i = pair; ok && tile_at<kOp>(g, s, i, &t); i += pairs) {
+            while (ok && tiles.next(s, &t)) {
+                tiles.taken(s);
                 if (t.k == 0) continue;
-                const uint32_t at = n_tile % 2;
-                ok = mbar_wait(&s.sums_empty[at], (n_tile / 2 % 2) ^ 1, &s.stop);
+                const uint32_t first = slot, slots = slots_of<kOp>(t);
+                for (uint32_t i = 0; ok && i < slots; ++i)
+                    ok = mbar_wait<true>(&s.sums_empty[(slot + i) % 2], ((slot + i) / 2 % 2) ^ 1, &s.stop);
                 if (!ok) break;
+                slot += slots;
                 tc_fence_after();
                 const uint32_t desc = product_desc(t.n, Tr::kAAcross, Tr::kBAcross);
-                const uint32_t sums = tmem + at * kStageColumns;
-                for (int k0 = 0; k0 < t.k; k0 += kBlockK) {
-                    ok = mbar_wait(kOp == kWgrad ? &s.ready[stage] : &s.full[stage], phase, &s.stop);
+                const uint32_t sums = tmem + first % 2 * kSlotColumns, ups = up_sums(tmem, first, slots);
+                for (int k = 0; k < t.k; k += kBlockK) {
+                    if (kOp == kWgrad && has_tail(t.k - k)) {
+                        ok = mbar_wait<true>(&s.ready[stage], ready >> stage & 1, &s.stop);
+                        ready ^= 1u << stage;
+                    } else {
+                        ok = mbar_wait(&s.full[stage], full >> stage & 1, &s.stop);
+                        full ^= 1u << stage;
+                    }
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t from = smem_addr(s_stages) + stage * Tr::kStageBytes;
                     uint64_t a = operand_desc(from, Tr::kAAcross);
                     uint64_t up = operand_desc(from + 128 * kBlockK * 2, Tr::kAAcross);
                     uint64_t b = operand_desc(from + Tr::kABytes, Tr::kBAcross);
-                    const int steps = t.k - k0 < kBlockK ? (t.k - k0 + 15) / 16 : kBlockK / 16;
+                    const int steps = t.k - k < kBlockK ? (t.k - k + 15) / 16 : kBlockK / 16;
                     for (int j = 0; j < steps; ++j) {
-                        mma_pair(sums, a, b, desc, k0 + j > 0);
-                        if (Tr::kGated) mma_pair(sums + 128, up, b, desc, k0 + j > 0);
+                        mma_pair(sums, a, b, desc, k + j > 0);
+                        if (Tr::kGated) mma_pair(ups, up, b, desc, k + j > 0);
                         a += Tr::kAAcross ? kStepAcross : kStepAlong;
                         up += Tr::kAAcross ? kStepAcross : kStepAlong;
                         b += Tr::kBAcross ? kStepAcross : kStepAlong;
                     }
                     mma_commit_pair(&s.empty[stage]);
-                    if (++stage == g.stages) stage = 0, phase ^= 1;
+                    if (++stage == g.stages) stage = 0;
                 }
                 if (!ok) break;
-                mma_commit_pair(&s.sums_full[at]);
-                ++n_tile;
+                for (uint32_t i = 0; i < slots; ++i) mma_commit_pair(&s.sums_full[(first + i) % 2]);
             }
-            if (!ok) {  // the products that were begun still read shared memory
+            if (!ok || !tiles.ok) {  // the products that were begun still read shared memory
                 s.stop = 1;
                 mma_commit_pair(&s.drain);
                 mbar_wait(&s.drain, 0, nullptr);
@@ -525,57 +602,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kTail) {
         if constexpr (kOp == kWgrad) {
-            // k is an expert's rows: what lies behind the last of them in its last stage, other experts'
+            // k is an expert's rows: what lies behind the last of them in their last 16, other experts'
             // rows or whatever a slab's end holds, is cleared before it is multiplied
-            int stage = 0, phase = 0;
+            uint32_t blocks = 0, part = 0;
             bool ok = true;
-            Tile t;
-            for (long long i = pair; ok && tile_at<kOp>(g, s, i, &t); i += pairs) {
-                const int b_blocks = (t.n / 2 + 63) / 64;
-                for (int k0 = 0; k0 < t.k; k0 += kBlockK) {
-                    ok = mbar_wait(&s.full[stage], phase, &s.stop);
-                    if (!__all_sync(kFullMask, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    const int left = t.k - k0;
-                    if (left < kBlockK && left % 16 != 0) {
-                        unsigned char* const at = s_stages + static_cast<size_t>(stage) * Tr::kStageBytes;
-                        const int lines = 16 - left % 16;  // up to the end of the last 16 k
-                        for (int n = lane; n < (2 + b_blocks) * lines * 8; n += 32) {
-                            const int block = n / (lines * 8), line = left + n / 8 % lines;
-                            *reinterpret_cast<uint4*>(at + block * kCrossBlock + line * 128 + n % 8 * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(peer_addr(&s.ready[stage], 0));
-                    if (++stage == g.stages) stage = 0, phase ^= 1;
+            while (ok && tiles.next(s, &t)) {
+                __syncwarp();
+                if (lane == 0) tiles.taken(s);
+                blocks += static_cast<uint32_t>((t.k + kBlockK - 1) / kBlockK);
+                const int left = t.k % kBlockK;
+                if (!has_tail(left)) continue;
+                const uint32_t stage = (blocks - 1) % static_cast<uint32_t>(g.stages);
+                ok = __all_sync(kFullMask, mbar_wait(&s.part[stage], part >> stage & 1, &s.stop));
+                if (!ok) break;
+                part ^= 1u << stage;
+                unsigned char* const at = s_stages + static_cast<size_t>(stage) * Tr::kStageBytes;
+                const int lines = 16 - left % 16, b_blocks = (t.n / 2 + 63) / 64;
+                for (int n = lane; n < (2 + b_blocks) * lines * 8; n += 32) {
+                    const int block = n / (lines * 8), line = left + n / 8 % lines;
+                    *reinterpret_cast<uint4*>(at + block * kCrossBlock + line * 128 + n % 8 * 16) =
+                        make_uint4(0, 0, 0, 0);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(peer_addr(&s.ready[stage], 0));
             }
-            if (!ok) s.stop = 1;
+            if (!ok || !tiles.ok) s.stop = 1;
         }
-    } else if (warp >= kFinish) {
+    } else {
         const int half = (warp - kFinish) / 4;
-        uint32_t n_tile = 0;
-        Tile t;
-        for (long long i = pair; tile_at<kOp>(g, s, i, &t); i += pairs) {
-            const uint32_t at = n_tile % 2;
+        uint32_t slot = 0;
+        while (true) {
+            const bool more = tiles.next(s, &t);
+            if (!half_agrees(tiles.ok, half)) {
+                s.stop = 1;
+                break;
+            }
+            if (!more) break;
+            if (lane == 0) tiles.taken(s);
+            const uint32_t first = slot, slots = slots_of<kOp>(t);
             if (t.k > 0) {
-                const bool ok = mbar_wait(&s.sums_full[at], n_tile / 2 % 2, &s.stop);
+                bool ok = true;
+                for (uint32_t i = 0; ok && i < slots; ++i)
+                    ok = mbar_wait(&s.sums_full[(slot + i) % 2], (slot + i) / 2 % 2, &s.stop);
                 if (!half_agrees(ok, half)) {
                     s.stop = 1;
                     break;
                 }
+                slot += slots;
                 tc_fence_after();
             }
-            finish_tile<kOp>(g, s, t, tmem + at * kStageColumns, rank, warp, lane);
+            finish_tile<kOp>(g, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots), rank, warp, lane);
             if (t.k > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(peer_addr(&s.sums_empty[at], 0));
-                ++n_tile;
+                if (lane == 0)
+                    for (uint32_t i = 0; i < slots; ++i)
+                        mbar_arrive_cluster(peer_addr(&s.sums_empty[(first + i) % 2], 0));
             }
         }
     }

@@ -34,23 +34,36 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// one poll of a barrier's phase; the poll itself waits a little in hardware
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// One poll of a barrier's phase; the poll itself waits a little in hardware. kCluster: the other
+// CTA's threads arrive there too.
+template <bool kCluster>
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+    if (kCluster)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
     return done != 0;
 }
 // Waits until the phase is over; gives up after about 2 s, or once *stop is set, and returns false.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* stop) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<kCluster>(bar, parity)) return true;
     const unsigned long long start = globaltimer_ns();
     for (uint32_t i = 0; i < (1u << 26); ++i) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<kCluster>(bar, parity)) return true;
         if ((i & 63u) == 63u && ((stop != nullptr && *stop != 0) || globaltimer_ns() - start > 2000000000ull)) break;
     }
     return false;
