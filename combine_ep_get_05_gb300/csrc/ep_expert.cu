@@ -23,7 +23,7 @@ constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSlotColumns = 256;  // of tensor memory: two tiles at a time
 constexpr int kMostStages = 8;
 constexpr int kTiles = 4;  // that are planned ahead
-constexpr int kMostN = 256;  // rows of an expert a tile
+constexpr int kMostNLog = 8, kMostN = 1 << kMostNLog;  // rows of an expert a tile
 constexpr size_t kSmemMost = 227 * 1024;
 
 template <int kOp>
@@ -71,7 +71,7 @@ struct Shared {  // behind the stages
     Tile tile[kTiles];
     uint32_t tmem;
     int stop;    // a wait gave up
-    int most_n;  // rows a tile, of this call
+    int choice;  // kMostN >> choice rows a tile, of this call
     int scan[4][kThreads / 32];
     float amax[2][2][4][64];  // [half][buffer][warp][gate and up of 32 columns]
     int prefix[1];            // [E + 1] tiles of rows before each expert's (but kWgrad)
@@ -92,55 +92,55 @@ struct Tiles {
     __device__ __forceinline__ void taken(Shared& s) { mbar_arrive(&s.tile_empty[at]); }
 };
 
-__device__ __forceinline__ int row_tiles(int count, int most_n, int* each) {
-    if (count == 0) return 0;
-    const int tiles = (count + most_n - 1) / most_n;
-    const int n = ((count + tiles - 1) / tiles + 31) / 32 * 32;  // even tiles, not full ones and a rest
-    *each = n;
-    return (count + n - 1) / n;
+// Tiles of an expert's rows, of most_n = kMostN >> choice rows at most, and rows of each: even
+// tiles, not full ones and a rest. (With tiles - 1 of them not all rows are reached: the rows of
+// each are at most most_n, and (tiles - 1) * most_n < count.)
+__device__ __forceinline__ int row_tiles(int count, int choice) {
+    return static_cast<int>((static_cast<uint32_t>(count) + (kMostN >> choice) - 1) >> (kMostNLog - choice));
 }
+__device__ __forceinline__ int rows_each(int count, int tiles) { return ((count + tiles - 1) / tiles + 31) & ~31; }
 
 template <int kOp>
-__device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared& s, long long t, Tile* tile) {
-    const int across = (g.C + 255) / 256;
+__device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared& s, uint32_t t, Tile* tile) {
+    const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
     if (kOp == kWgrad) {
-        const int down = (g.K + 255) / 256;
-        if (t >= static_cast<long long>(g.E) * across * down) return false;
-        const int e = static_cast<int>(t / (across * down)), l = static_cast<int>(t % (across * down));
+        const uint32_t down = (static_cast<uint32_t>(g.K) + 255) / 256;
+        if (t >= static_cast<uint32_t>(g.E) * across * down) return false;
+        const int e = static_cast<int>(t / (across * down));
+        const uint32_t l = t - e * (across * down);
         const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
         tile->e = e;
         tile->row = r.first;
         tile->k = r.count;
-        tile->channel = l % across * 256;
-        tile->column = l / across * 256;
+        tile->channel = static_cast<int>(l % across * 256);
+        tile->column = static_cast<int>(l / across * 256);
         tile->rows = g.K - tile->column < 256 ? g.K - tile->column : 256;
         tile->n = (tile->rows + 31) / 32 * 32;
         return true;
     }
-    if (t >= static_cast<long long>(s.prefix[g.E]) * across) return false;
+    if (t >= static_cast<uint32_t>(s.prefix[g.E]) * across) return false;
     int lo = 0, hi = g.E;  // the last expert whose tiles begin at or before t
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (static_cast<long long>(s.prefix[mid]) * across <= t)
+        if (static_cast<uint32_t>(s.prefix[mid]) * across <= t)
             lo = mid;
         else
             hi = mid;
     }
     const ExpertRows r = expert_rows(g.offsets, lo, g.E / g.R, g.max_rows);
-    int each = 32;
-    const int tiles = row_tiles(r.count, s.most_n, &each);
+    const int tiles = row_tiles(r.count, s.choice), each = rows_each(r.count, tiles);
     // eight tiles of rows with all channels, then the next eight: the rows that are at work at a
     // time, and the weights that they share, stay in L2
-    int l = static_cast<int>(t - static_cast<long long>(s.prefix[lo]) * across);
-    const int group = l / (8 * across);
+    uint32_t l = t - s.prefix[lo] * across;
+    const uint32_t group = l / (8 * across);
     l -= group * 8 * across;
-    const int width = tiles - group * 8 < 8 ? tiles - group * 8 : 8;
-    const int i = group * 8 + l % width;
+    const uint32_t left = tiles - group * 8, width = left < 8 ? left : 8;
+    const int i = static_cast<int>(group * 8 + l % width);
     tile->e = lo;
     tile->row = r.first + static_cast<long long>(i) * each;
     tile->rows = r.count - i * each < each ? r.count - i * each : each;
     tile->n = (tile->rows + 31) / 32 * 32;
-    tile->channel = l / width * 256;
+    tile->channel = static_cast<int>(l / width * 256);
     tile->column = 0;
     tile->k = g.K;
     return true;
@@ -153,12 +153,12 @@ __device__ void plan_tiles(const ExpertArgs& g, Shared& s) {
     const int per = (g.E + kThreads - 1) / kThreads, first = tid * per;
     const int last = first + per < g.E ? first + per : g.E;
     const int across = (g.C + 255) / 256, pairs = static_cast<int>(gridDim.x / 2);
-    int each, count = 0, sum[4] = {0, 0, 0, 0};
+    int count = 0, sum[4] = {0, 0, 0, 0};
     for (int e = first; e < last; ++e) {
         const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
         if (r.dropped && blockIdx.x == 0) raise_flag(g.status, EP_FLAG_CAPACITY);
         count = r.count;
-        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(count, kMostN >> i, &each);
+        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(count, i);
     }
     for (int i = 0; i < 4; ++i) {
         const int n = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(sum[i])));
@@ -185,10 +185,10 @@ __device__ void plan_tiles(const ExpertArgs& g, Shared& s) {
     for (int e = first; e < last; ++e) {
         s.prefix[e] = before;
         if (per > 1) count = expert_rows(g.offsets, e, g.E / g.R, g.max_rows).count;
-        before += row_tiles(count, kMostN >> choice, &each);
+        before += row_tiles(count, choice);
         if (e == g.E - 1) s.prefix[g.E] = before;
     }
-    if (tid == 0) s.most_n = kMostN >> choice;
+    if (tid == 0) s.choice = choice;
 }
 
 // ---------------------------------------------------------------------------- finishing a tile
@@ -412,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Shared& s = *reinterpret_cast<Shared*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     const int rank = static_cast<int>(cluster_rank());
-    const long long pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
     if (tid == 0) {
         for (int i = 0; i < g.stages; ++i) {
@@ -456,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kScheduler) {
         if (lane == 0) {
             uint32_t at = 0, phase = 0;
-            for (long long i = pair;; i += pairs) {
+            for (uint32_t i = pair;; i += pairs) {
                 const bool more = tile_at<kOp>(g, s, i, &t);
                 if (!more) t.e = -1;
                 if (!mbar_wait(&s.tile_empty[at], phase ^ 1, &s.stop)) {
@@ -470,133 +470,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kProducer) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
-            long long issued = 0;
-            bool ok = true;
-            while (ok && tiles.next(s, &t)) {
-                tiles.taken(s);
-                const int half = t.n / 2;
-                const int b_first = rank * half;
-                // bytes of this CTA's half of a stage: whole boxes, also where they hang over an end
-                const uint32_t b_bytes = kOp == kWgrad ? (half + 63) / 64 * kCrossBlock
-                                                       : static_cast<uint32_t>(half) * kBlockK * 2;
-                const uint32_t bytes = Tr::kABytes + b_bytes;
-                for (int k = 0; k < t.k; k += kBlockK) {
-                    ok = mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop);
-                    if (!ok) break;
-                    empty ^= 1u << stage;
-                    const uint32_t to = smem_addr(s_stages) + stage * Tr::kStageBytes;
-                    const uint32_t b_to = to + Tr::kABytes;
-                    const int c = t.channel + rank * 128;
-                    uint32_t bar;
-                    if (kOp == kWgrad && has_tail(t.k - k)) {  // each CTA counts its own bytes: it clears them
+        // the whole warp keeps the books, so that they stay uniform; one lane issues
+        const bool leader = elected();
+        int stage = 0;
+        uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
+        uint32_t issued = 0;
+        bool ok = true;
+        while (ok && tiles.next(s, &t)) {
+            __syncwarp();
+            if (leader) tiles.taken(s);
+            const int half = t.n / 2;
+            const int b_first = rank * half;
+            // bytes of this CTA's half of a stage: whole boxes, also where they hang over an end
+            const uint32_t b_bytes = kOp == kWgrad ? (half + 63) / 64 * kCrossBlock
+                                                   : static_cast<uint32_t>(half) * kBlockK * 2;
+            const uint32_t bytes = Tr::kABytes + b_bytes;
+            const int c = t.channel + rank * 128, row = static_cast<int>(t.row) + (kOp == kWgrad ? 0 : b_first);
+            for (int k = 0; k < t.k; k += kBlockK) {
+                ok = __all_sync(kFullMask, mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop));
+                if (!ok) break;
+                empty ^= 1u << stage;
+                const uint32_t to = smem_addr(s_stages) + stage * Tr::kStageBytes;
+                const uint32_t b_to = to + Tr::kABytes;
+                const bool tail = kOp == kWgrad && has_tail(t.k - k);
+                // a tail's bytes each CTA counts itself, since it clears them; others CTA 0 counts for both
+                const uint32_t bar = tail ? smem_addr(&s.part[stage]) : peer_addr(&s.full[stage], 0);
+                if (leader) {
+                    if (tail)
                         mbar_arrive_expect_tx(&s.part[stage], bytes);
-                        bar = smem_addr(&s.part[stage]);
-                        part ^= 1u << stage;
-                        last_part |= 1u << stage;
-                    } else {  // CTA 0 counts both CTAs' bytes
-                        if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
-                        bar = peer_addr(&s.full[stage], 0);
-                        full ^= 1u << stage;
-                        last_part &= ~(1u << stage);
-                    }
+                    else if (rank == 0)
+                        mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
                     if constexpr (kOp == kGateUp) {
                         tma_load_pair_3d(to, a_map, k, c, 2 * t.e, bar);
                         tma_load_pair_3d(to + 128 * kBlockK * 2, a_map, k, c, 2 * t.e + 1, bar);
                     } else if constexpr (kOp == kDown) {
                         tma_load_pair_3d(to, a_map, k, c, t.e, bar);
+                    } else if constexpr (kOp == kWgrad) {
+                        tma_load_pair_2d(to, a_map, c, row + k, bar);
+                        tma_load_pair_2d(to + kCrossBlock, a_map, c + 64, row + k, bar);
                     } else {
-                        for (int j = 0; j < 2; ++j) {
-                            if constexpr (kOp == kWgrad)
-                                tma_load_pair_2d(to + j * kCrossBlock, a_map, c + 64 * j, static_cast<int>(t.row) + k,
-                                                 bar);
-                            else
-                                tma_load_pair_3d(to + j * kCrossBlock, a_map, c + 64 * j, k, t.e, bar);
-                        }
+                        tma_load_pair_3d(to, a_map, c, k, t.e, bar);
+                        tma_load_pair_3d(to + kCrossBlock, a_map, c + 64, k, t.e, bar);
                     }
                     if constexpr (kOp == kWgrad) {
-                        for (int j = 0; j * 64 < half; ++j)
-                            tma_load_pair_2d(b_to + j * kCrossBlock, b64_map, t.column + b_first + 64 * j,
-                                             static_cast<int>(t.row) + k, bar);
+                        tma_load_pair_2d(b_to, b64_map, t.column + b_first, row + k, bar);
+                        if (half > 64)
+                            tma_load_pair_2d(b_to + kCrossBlock, b64_map, t.column + b_first + 64, row + k, bar);
                     } else {
-                        const int row = static_cast<int>(t.row) + b_first;
                         int j = 0;
                         for (; j + 64 <= half; j += 64)
                             tma_load_pair_2d(b_to + j * kBlockK * 2, b64_map, k, row + j, bar);
                         for (; j < half; j += 16) tma_load_pair_2d(b_to + j * kBlockK * 2, b16_map, k, row + j, bar);
                     }
-                    ++issued;
-                    if (++stage == g.stages) stage = 0;
                 }
-            }
-            ok = ok && tiles.ok;
-            if (!ok) s.stop = 1;
-            // The last use of every stage is waited for: by its release, or where something gave up, by
-            // its bytes, so that no copy and no arrival is on its way when the CTA ends.
-            const int used = issued < g.stages ? static_cast<int>(issued) : g.stages;
-            for (int i = 0; i < used; ++i) {
-                stage = stage == 0 ? g.stages - 1 : stage - 1;
-                if (ok && !mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop)) ok = false;
-                if (ok) continue;
-                if (last_part >> stage & 1)
-                    mbar_wait(&s.part[stage], (part >> stage & 1) ^ 1, nullptr);
-                else if (rank == 0)
-                    mbar_wait(&s.full[stage], (full >> stage & 1) ^ 1, nullptr);
-            }
-            if (!ok) {
-                s.stop = 1;
-                raise_flag(g.status, EP_FLAG_TIMEOUT);
+                if (tail) {
+                    part ^= 1u << stage;
+                    last_part |= 1u << stage;
+                } else {
+                    full ^= 1u << stage;
+                    last_part &= ~(1u << stage);
+                }
+                ++issued;
+                if (++stage == g.stages) stage = 0;
             }
         }
+        ok = ok && tiles.ok;
+        if (!ok) s.stop = 1;
+        // The last use of every stage is waited for: by its release, or where something gave up, by
+        // its bytes, so that no copy and no arrival is on its way when the CTA ends.
+        const int used = issued < static_cast<uint32_t>(g.stages) ? static_cast<int>(issued) : g.stages;
+        for (int i = 0; i < used; ++i) {
+            stage = stage == 0 ? g.stages - 1 : stage - 1;
+            if (ok && !mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop)) ok = false;
+            if (ok) continue;
+            if (last_part >> stage & 1)
+                mbar_wait(&s.part[stage], (part >> stage & 1) ^ 1, nullptr);
+            else if (rank == 0)
+                mbar_wait(&s.full[stage], (full >> stage & 1) ^ 1, nullptr);
+        }
+        if (!ok) {
+            s.stop = 1;
+            raise_flag(g.status, EP_FLAG_TIMEOUT);
+        }
     } else if (warp == kMultiplier) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool leader = elected();
             int stage = 0;
             uint32_t full = 0, ready = 0, slot = 0;
             bool ok = true;
+            constexpr uint64_t kAStep = Tr::kAAcross ? kStepAcross : kStepAlong;
+            constexpr uint64_t kBStep = Tr::kBAcross ? kStepAcross : kStepAlong;
             while (ok && tiles.next(s, &t)) {
-                tiles.taken(s);
+                __syncwarp();
+                if (leader) tiles.taken(s);
                 if (t.k == 0) continue;
                 const uint32_t first = slot, slots = slots_of<kOp>(t);
                 for (uint32_t i = 0; ok && i < slots; ++i)
-                    ok = mbar_wait<true>(&s.sums_empty[(slot + i) % 2], ((slot + i) / 2 % 2) ^ 1, &s.stop);
+                    ok = __all_sync(kFullMask, mbar_wait<true>(&s.sums_empty[(slot + i) % 2],
+                                                               ((slot + i) / 2 % 2) ^ 1, &s.stop));
                 if (!ok) break;
                 slot += slots;
                 tc_fence_after();
                 const uint32_t desc = product_desc(t.n, Tr::kAAcross, Tr::kBAcross);
                 const uint32_t sums = tmem + first % 2 * kSlotColumns, ups = up_sums(tmem, first, slots);
                 for (int k = 0; k < t.k; k += kBlockK) {
-                    if (kOp == kWgrad && has_tail(t.k - k)) {
+                    const bool tail = kOp == kWgrad && has_tail(t.k - k);
+                    if (tail) {
                         ok = mbar_wait<true>(&s.ready[stage], ready >> stage & 1, &s.stop);
                         ready ^= 1u << stage;
                     } else {
                         ok = mbar_wait(&s.full[stage], full >> stage & 1, &s.stop);
                         full ^= 1u << stage;
                     }
+                    ok = __all_sync(kFullMask, ok);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t from = smem_addr(s_stages) + stage * Tr::kStageBytes;
-                    uint64_t a = operand_desc(from, Tr::kAAcross);
-                    uint64_t up = operand_desc(from + 128 * kBlockK * 2, Tr::kAAcross);
-                    uint64_t b = operand_desc(from + Tr::kABytes, Tr::kBAcross);
-                    const int steps = t.k - k < kBlockK ? (t.k - k + 15) / 16 : kBlockK / 16;
-                    for (int j = 0; j < steps; ++j) {
-                        mma_pair(sums, a, b, desc, k + j > 0);
-                        if (Tr::kGated) mma_pair(ups, up, b, desc, k + j > 0);
-                        a += Tr::kAAcross ? kStepAcross : kStepAlong;
-                        up += Tr::kAAcross ? kStepAcross : kStepAlong;
-                        b += Tr::kBAcross ? kStepAcross : kStepAlong;
+                    const uint64_t a = operand_desc(from, Tr::kAAcross);
+                    const uint64_t up = operand_desc(from + 128 * kBlockK * 2, Tr::kAAcross);
+                    const uint64_t b = operand_desc(from + Tr::kABytes, Tr::kBAcross);
+                    const int left = t.k - k;
+                    if (leader) {
+#pragma unroll
+                        for (int j = 0; j < kBlockK / 16; ++j) {
+                            if (j * 16 >= left) break;
+                            mma_pair(sums, a + j * kAStep, b + j * kBStep, desc, j > 0 || k > 0);
+                            if (Tr::kGated) mma_pair(ups, up + j * kAStep, b + j * kBStep, desc, j > 0 || k > 0);
+                        }
+                        mma_commit_pair(&s.empty[stage]);
                     }
-                    mma_commit_pair(&s.empty[stage]);
                     if (++stage == g.stages) stage = 0;
                 }
                 if (!ok) break;
-                for (uint32_t i = 0; i < slots; ++i) mma_commit_pair(&s.sums_full[(first + i) % 2]);
+                if (leader)
+                    for (uint32_t i = 0; i < slots; ++i) mma_commit_pair(&s.sums_full[(first + i) % 2]);
             }
             if (!ok || !tiles.ok) {  // the products that were begun still read shared memory
                 s.stop = 1;
-                mma_commit_pair(&s.drain);
+                if (leader) mma_commit_pair(&s.drain);
                 mbar_wait(&s.drain, 0, nullptr);
             }
         }

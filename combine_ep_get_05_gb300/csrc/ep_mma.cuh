@@ -21,6 +21,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// one lane of the (converged) warp, the same one every time
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -60,11 +66,16 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
 // Waits until the phase is over; gives up after about 2 s, or once *stop is set, and returns false.
 template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* stop) {
-    if (mbar_try<kCluster>(bar, parity)) return true;
-    const unsigned long long start = globaltimer_ns();
+    unsigned long long start = 0;
     for (uint32_t i = 0; i < (1u << 26); ++i) {
         if (mbar_try<kCluster>(bar, parity)) return true;
-        if ((i & 63u) == 63u && ((stop != nullptr && *stop != 0) || globaltimer_ns() - start > 2000000000ull)) break;
+        if ((i & 63u) != 63u) continue;
+        if (stop != nullptr && *stop != 0) break;
+        const unsigned long long now = globaltimer_ns();
+        if (start == 0)
+            start = now;
+        else if (now - start > 2000000000ull)
+            break;
     }
     return false;
 }
