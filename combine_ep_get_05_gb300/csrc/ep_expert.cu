@@ -74,6 +74,7 @@ struct Shared {  // behind the stages
     int choice;  // kMostN >> choice rows a tile, of this call
     int scan[4][kThreads / 32];
     float amax[2][2][4][64];  // [half][buffer][warp][gate and up of 32 columns]
+    alignas(16) unsigned char patch[8][kPatchBytes];  // of the finishing warps
     int prefix[1];            // [E + 1] tiles of rows before each expert's (but kWgrad)
 };
 
@@ -193,94 +194,165 @@ __device__ void plan_tiles(const ExpertArgs& g, Shared& s) {
 
 // ---------------------------------------------------------------------------- finishing a tile
 
-// Two columns (rows of the output) at a time change places between neighbouring lanes (channels),
-// so that a lane moves two channels of one row: 4 bytes.
-__device__ __forceinline__ uint32_t lanes_to_row(float v0, float v1, bool odd) {
-    const uint32_t w = pack_bf16x2_rn(v0, v1), o = __shfl_xor_sync(kFullMask, w, 1);
-    return odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
-}
-__device__ __forceinline__ void row_to_lanes(uint32_t w, bool odd, float& v0, float& v1) {
-    const uint32_t o = __shfl_xor_sync(kFullMask, w, 1);
-    v0 = odd ? bf16_hi(o) : bf16_lo(w);
-    v1 = odd ? bf16_hi(w) : bf16_lo(o);
-}
-// A 4 x 4 transpose of bytes among four neighbouring lanes: four codes of a lane's channel
-// become four channels' codes of one row, and back.
-__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
-    const uint32_t a = __shfl_xor_sync(kFullMask, w, 1);
-    w = __byte_perm(w, a, lane & 1 ? 0x3715 : 0x6240);
-    const uint32_t b = __shfl_xor_sync(kFullMask, w, 2);
-    return __byte_perm(w, b, lane & 2 ? 0x3276 : 0x5410);
-}
+// 32 rows of 32 channels, of which `rows` and, 8 at a time, `channels` are there: 16-byte vectors of
+// bf16, 8-byte ones of codes, four neighbouring lanes a row.
+struct Window {
+    int rows, channels;
+    __device__ __forceinline__ bool has(int q, int lane) const {
+        return 8 * q + lane / 4 < rows && lane % 4 * 8 < channels;
+    }
+};
 
-// v[j] of 32 rows from `to` on (this lane's channel, rows `stride` elements apart), as bf16
-__device__ __forceinline__ void store_rows(uint16_t* to, size_t stride, const float (&v)[32], int rows, bool there,
-                                           int lane) {
-    const bool odd = lane & 1;
-    to -= odd ? 1 : 0;
+__device__ __forceinline__ void store_rows(uint16_t* to, size_t stride, const uint32_t (&w)[16], const Window& win,
+                                           uint32_t patch, int lane) {
+    __syncwarp();  // what was in the patch has been read
+    patch_put(patch, w, lane);
+    __syncwarp();
+    to += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-        const uint32_t w = lanes_to_row(v[j], v[j + 1], odd);
-        const int row = j + (odd ? 1 : 0);
-        if (there && row < rows) *reinterpret_cast<uint32_t*>(to + row * stride) = w;
+    for (int q = 0; q < 4; ++q) {
+        const uint4 v = ld_shared_v4(row_place(patch, q, lane));
+        if (win.has(q, lane)) st_v4(to + 8 * q * stride, v);
     }
 }
-__device__ __forceinline__ void load_rows(float (&v)[32], const uint16_t* from, size_t stride, int rows, bool there,
+__device__ __forceinline__ void load_rows(uint4 (&v)[4], const uint16_t* from, size_t stride, const Window& win,
                                           int lane) {
-    const bool odd = lane & 1;
-    from -= odd ? 1 : 0;
+    from += lane / 4 * stride + lane % 4 * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        v[q] = win.has(q, lane) ? ld_stream_v4(from + 8 * q * stride) : make_uint4(0, 0, 0, 0);
+}
+// rows into fragments
+__device__ __forceinline__ void spread(uint32_t (&w)[16], const uint4 (&v)[4], uint32_t patch, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) st_shared_v4(row_place(patch, q, lane), v[q]);
+    __syncwarp();
+    patch_get(w, patch, lane);
+}
+__device__ __forceinline__ void pack(uint32_t (&w)[16], const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            w[4 * q + b] = pack_bf16x2_rn(v[i], v[i + 1]);
+        }
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t codes_of_f16x2(uint32_t two) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(two));
+    return r;
+}
+
+// Codes of 32 rows of one block of 128 channels, of which the warp has 32; rcp: lane j has row j's.
+// The quotients go through the patch as fp16, whose 11 bits leave the rounding to 4 as it is but
+// beside a midpoint of codes (by 2^-12 of the value).
+__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const float (&v)[32], float rcp,
+                                            const Window& win, uint32_t patch, int lane) {
     uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-        const int row = j + (odd ? 1 : 0);
-        w[j / 2] = there && row < rows ? __ldg(reinterpret_cast<const uint32_t*>(from + row * stride)) : 0;
+    for (int q = 0; q < 4; ++q) {
+        const float r0 = __shfl_sync(kFullMask, rcp, 8 * q + lane % 4 * 2);
+        const float r1 = __shfl_sync(kFullMask, rcp, 8 * q + lane % 4 * 2 + 1);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            w[4 * q + b] = pack_f16x2_rn(v[i] * r0, v[i + 1] * r1);
+        }
     }
+    __syncwarp();
+    patch_put(patch, w, lane);
+    __syncwarp();
+    to += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) row_to_lanes(w[j / 2], odd, v[j], v[j + 1]);
-}
-
-// a checkpoint's codes times their scales; scales + row * scale_stride is the block's of a row
-__device__ __forceinline__ void load_codes(float (&v)[32], const uint8_t* from, size_t stride, const uint16_t* scales,
-                                           size_t scale_stride, int rows, bool there, int lane) {
-    from -= lane & 3;
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const int row = j + (lane & 3);
-        w[j / 4] = there && row < rows ? __ldg(reinterpret_cast<const uint32_t*>(from + row * stride)) : 0;
-    }
-    const uint32_t mine = there && lane < rows ? static_cast<uint32_t>(__ldg(scales + lane * scale_stride)) << 16 : 0;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        float c[4];
-        e4m3x4_to_f32(transpose_bytes(w[j / 4], lane), c[0], c[1], c[2], c[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j + i] = c[i] * __uint_as_float(__shfl_sync(kFullMask, mine, j + i));
+    for (int q = 0; q < 4; ++q) {
+        const uint4 f = ld_shared_v4(row_place(patch, q, lane));
+        const uint32_t a = codes_of_f16x2(f.x) | codes_of_f16x2(f.y) << 16;
+        const uint32_t b = codes_of_f16x2(f.z) | codes_of_f16x2(f.w) << 16;
+        if (win.has(q, lane)) st_v2(to + 8 * q * stride, a, b);
     }
 }
-
-__device__ __forceinline__ uint32_t magnitude(float v) {  // 0 for NaN
-    return v == v ? __float_as_uint(v) & 0x7fffffffu : 0u;
+__device__ __forceinline__ void load_codes(uint4 (&v)[4], const uint8_t* from, size_t stride, const Window& win,
+                                           int lane) {
+    from += lane / 4 * stride + lane % 4 * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint2 c = win.has(q, lane) ? __ldg(reinterpret_cast<const uint2*>(from + 8 * q * stride))
+                                         : make_uint2(0, 0);
+        v[q].x = c.x;
+        v[q].y = c.y;
+    }
+}
+// codes into fragments of fp16 (every code is one), times their scales; scale: lane j has row j's
+__device__ __forceinline__ void spread_codes(float (&v)[32], const uint4 (&c)[4], float scale, uint32_t patch,
+                                             int lane) {
+    uint4 f[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        f[q] = make_uint4(e4m3x2_to_f16x2(c[q].x), e4m3x2_to_f16x2(c[q].x >> 16), e4m3x2_to_f16x2(c[q].y),
+                          e4m3x2_to_f16x2(c[q].y >> 16));
+    uint32_t w[16];
+    spread(w, f, patch, lane);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float s0 = __shfl_sync(kFullMask, scale, 8 * q + lane % 4 * 2);
+        const float s1 = __shfl_sync(kFullMask, scale, 8 * q + lane % 4 * 2 + 1);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            v[i] = f16_to_f32(w[4 * q + b] & 0xffffu) * s0;
+            v[i + 1] = f16_to_f32(w[4 * q + b] >> 16) * s1;
+        }
+    }
+}
+__device__ __forceinline__ void unpack(float (&v)[32], const uint32_t (&w)[16]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            v[i] = bf16_lo(w[4 * q + b]);
+            v[i + 1] = bf16_hi(w[4 * q + b]);
+        }
 }
 
-// Scales and codes of 32 rows of one block of 128 channels; amax: lane j has row j's
-__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, uint16_t* scales, size_t scale_stride,
-                                            const float (&v)[32], float amax, int rows, bool there, bool writes_scale,
-                                            int lane) {
-    const float scale = checkpoint_scale(amax), rcp = checkpoint_rcp(scale);
-    if (writes_scale && there && lane < rows)
-        scales[lane * scale_stride] = static_cast<uint16_t>(__float_as_uint(scale) >> 16);
-    to -= lane & 3;
+// max |v| of every column over the warp's lanes, NaN apart, into to[column]
+__device__ __forceinline__ void column_max(float* to, const float (&v)[32], int lane) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        float q[4];
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q[i] = checkpoint_quotient(v[j + i], __shfl_sync(kFullMask, scale, j + i),
-                                       __shfl_sync(kFullMask, rcp, j + i));
-        const uint32_t w = transpose_bytes(pack_e4m3x4_rn_sat(q[0], q[1], q[2], q[3]), lane);
-        const int row = j + (lane & 3);
-        if (there && row < rows) *reinterpret_cast<uint32_t*>(to + row * stride) = w;
+        for (int i = 0; i < 2; ++i) {
+            float m = fmaxf(fmaxf(fabsf(v[4 * q + i]), fabsf(v[4 * q + 2 + i])),
+                            fmaxf(fabsf(v[16 + 4 * q + i]), fabsf(v[16 + 4 * q + 2 + i])));
+            m = m == m ? m : 0.0f;  // all of them NaN
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
+            if (lane < 4) to[8 * q + 2 * lane + i] = m;
+        }
+}
+
+template <bool kGelu>
+__device__ __forceinline__ void activate(float (&v)[32], const float (&up)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = v[j] * gate_of<kGelu>(v[j]).s * up[j];
+}
+// dh in v, gate and up -> dup in v, dgate in gate, h in up
+template <bool kGelu>
+__device__ __forceinline__ void activate_bwd(float (&v)[32], float (&gate)[32], float (&up)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const Gate a = gate_of<kGelu>(gate[j]);
+        const float act = gate[j] * a.s;
+        gate[j] = v[j] * up[j] * (a.s + act * (1.0f - a.s) * a.slope);
+        v[j] *= act;
+        up[j] *= act;
     }
 }
 
@@ -296,94 +368,124 @@ __device__ __forceinline__ bool half_agrees(bool ok, int half) {
     return r != 0;
 }
 
-template <int kOp>
-__device__ __forceinline__ void finish_tile(const ExpertArgs& g, Shared& s, const Tile& t, uint32_t sums, uint32_t ups,
-                                            int rank, int warp, int lane) {
+// What the gradient reads of 32 rows of the checkpoint, on its way.
+struct Kept {
+    uint4 gate[4], up[4];        // bf16, or codes in x and y,
+    float gate_scale, up_scale;  // and lane j's row's scales
+};
+__device__ __forceinline__ void load_kept(Kept& kept, const ExpertArgs& g, size_t row, int channel, const Window& win,
+                                          int lane) {
+    const size_t C = static_cast<size_t>(g.C), at = row * 2 * C + channel;
+    if (g.pre != nullptr) {
+        load_rows(kept.gate, g.pre + at, 2 * C, win, lane);
+        load_rows(kept.up, g.pre + at + C, 2 * C, win, lane);
+    } else {
+        load_codes(kept.gate, g.pre_q + at, 2 * C, win, lane);
+        load_codes(kept.up, g.pre_q + at + C, 2 * C, win, lane);
+        const bool there = lane < win.rows && win.channels > 0;
+        const uint16_t* scales = g.pre_scales + (row + lane) * (2 * C / 128) + channel / 128;
+        kept.gate_scale = there ? __uint_as_float(static_cast<uint32_t>(__ldg(scales)) << 16) : 0.0f;
+        kept.up_scale = there ? __uint_as_float(static_cast<uint32_t>(__ldg(scales + C / 128)) << 16) : 0.0f;
+    }
+}
+
+// One warp's part of a tile: 32 channels, every other 32 columns. `ready`, called before the sums
+// are read, waits for them; false: give up.
+template <int kOp, typename Ready>
+__device__ __forceinline__ bool finish_tile(const ExpertArgs& g, Shared& s, const Tile& t, uint32_t sums, uint32_t ups,
+                                            int rank, int warp, int lane, Ready ready) {
     const int half = (warp - kFinish) / 4, quarter = warp % 4;
-    const int channel = t.channel + rank * 128 + quarter * 32 + lane;
-    const bool there = channel < g.C;
+    const int channel = t.channel + rank * 128 + quarter * 32;  // the warp's first
     const size_t C = static_cast<size_t>(g.C);
+    const uint32_t patch = smem_addr(s.patch[warp - kFinish]);
     sums += static_cast<uint32_t>(quarter * 32) << 16;
     ups += static_cast<uint32_t>(quarter * 32) << 16;
+    Kept kept;
+    if constexpr (kOp == kDownBwd)  // on its way while the sums are made
+        load_kept(kept, g, static_cast<size_t>(t.row) + half * 32, channel, {t.rows - half * 32, g.C - channel}, lane);
+    if (!ready()) return false;
     int buffer = 0;
     for (int c0 = half * 32; c0 < t.n; c0 += 64) {
-        const int rows = t.rows - c0;  // of this chunk: 32 at most are looked at
+        const Window win = {t.rows - c0, g.C - channel};
+        const size_t row = static_cast<size_t>(t.row) + c0;
+        uint32_t w[16];
         float v[32];
         if (t.k > 0) {
-            tmem_load32(v, sums + c0);
+            tmem_load(v, sums + c0);
             tmem_load_wait(v);
         } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.0f;
         }
-        const size_t row = static_cast<size_t>(t.row) + c0;
         if constexpr (kOp == kGateUp) {
             float up[32];
-            tmem_load32(up, ups + c0);
+            tmem_load(up, ups + c0);
             tmem_load_wait(up);
             if (g.out_pre != nullptr) {
-                store_rows(g.out_pre + row * 2 * C + channel, 2 * C, v, rows, there, lane);
-                store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, up, rows, there, lane);
+                pack(w, v);
+                store_rows(g.out_pre + row * 2 * C + channel, 2 * C, w, win, patch, lane);
+                pack(w, up);
+                store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, w, win, patch, lane);
             }
             if (g.out_q != nullptr) {
-                uint32_t gate_max = 0, up_max = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t a = __reduce_max_sync(kFullMask, magnitude(v[j]));
-                    const uint32_t b = __reduce_max_sync(kFullMask, magnitude(up[j]));
-                    if (lane == j) gate_max = a, up_max = b;
-                }
                 float(&amax)[4][64] = s.amax[half][buffer];
-                amax[quarter][lane] = __uint_as_float(gate_max);
-                amax[quarter][32 + lane] = __uint_as_float(up_max);
+                buffer ^= 1;
+                column_max(amax[quarter], v, lane);
+                column_max(amax[quarter] + 32, up, lane);
                 asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
                 float a = 0.0f, b = 0.0f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    a = fmaxf(a, amax[w][lane]);
-                    b = fmaxf(b, amax[w][32 + lane]);
+                for (int i = 0; i < 4; ++i) {
+                    a = fmaxf(a, amax[i][lane]);
+                    b = fmaxf(b, amax[i][32 + lane]);
                 }
-                buffer ^= 1;
-                const size_t blocks = 2 * C / 128, block = row * blocks + (channel - lane) / 128;
-                store_codes(g.out_q + row * 2 * C + channel, 2 * C, g.out_scales + block, blocks, v, a, rows, there,
-                            quarter == 0, lane);
-                store_codes(g.out_q + row * 2 * C + C + channel, 2 * C, g.out_scales + block + C / 128, blocks, up, b,
-                            rows, there, quarter == 0, lane);
+                a = checkpoint_scale(a);
+                b = checkpoint_scale(b);
+                if (quarter == 0 && lane < win.rows && win.channels > 0) {
+                    uint16_t* const scales = g.out_scales + (row + lane) * (2 * C / 128) + channel / 128;
+                    scales[0] = static_cast<uint16_t>(__float_as_uint(a) >> 16);
+                    scales[C / 128] = static_cast<uint16_t>(__float_as_uint(b) >> 16);
+                }
+                store_codes(g.out_q + row * 2 * C + channel, 2 * C, v, checkpoint_rcp(a), win, patch, lane);
+                store_codes(g.out_q + row * 2 * C + C + channel, 2 * C, up, checkpoint_rcp(b), win, patch, lane);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = v[j] * gate_of(v[j], g.act).s * up[j];
-            store_rows(g.out + row * C + channel, C, v, rows, there, lane);
+            if (g.act == EP_ACT_GELU)
+                activate<true>(v, up);
+            else
+                activate<false>(v, up);
+            pack(w, v);
+            store_rows(g.out + row * C + channel, C, w, win, patch, lane);
         } else if constexpr (kOp == kDownBwd) {
             float gate[32], up[32];
             if (g.pre != nullptr) {
-                load_rows(gate, g.pre + row * 2 * C + channel, 2 * C, rows, there, lane);
-                load_rows(up, g.pre + row * 2 * C + C + channel, 2 * C, rows, there, lane);
+                spread(w, kept.gate, patch, lane);
+                unpack(gate, w);
+                spread(w, kept.up, patch, lane);
+                unpack(up, w);
             } else {
-                const size_t blocks = 2 * C / 128, block = row * blocks + channel / 128;
-                load_codes(gate, g.pre_q + row * 2 * C + channel, 2 * C, g.pre_scales + block, blocks, rows, there,
-                           lane);
-                load_codes(up, g.pre_q + row * 2 * C + C + channel, 2 * C, g.pre_scales + block + C / 128, blocks, rows,
-                           there, lane);
+                spread_codes(gate, kept.gate, kept.gate_scale, patch, lane);
+                spread_codes(up, kept.up, kept.up_scale, patch, lane);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const Gate a = gate_of(gate[j], g.act);
-                const float act = gate[j] * a.s;
-                const float dgate = v[j] * up[j] * (a.s + act * (1.0f - a.s) * a.slope);
-                v[j] *= act;
-                up[j] *= act;  // h
-                gate[j] = dgate;
+            if (g.act == EP_ACT_GELU)
+                activate_bwd<true>(v, gate, up);
+            else
+                activate_bwd<false>(v, gate, up);
+            pack(w, gate);
+            store_rows(g.out_pre + row * 2 * C + channel, 2 * C, w, win, patch, lane);
+            if (c0 + 64 < t.n) load_kept(kept, g, row + 64, channel, {t.rows - c0 - 64, g.C - channel}, lane);
+            pack(w, v);
+            store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, w, win, patch, lane);
+            if (g.out != nullptr) {
+                pack(w, up);
+                store_rows(g.out + row * C + channel, C, w, win, patch, lane);
             }
-            store_rows(g.out_pre + row * 2 * C + channel, 2 * C, gate, rows, there, lane);
-            store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, v, rows, there, lane);
-            if (g.out != nullptr) store_rows(g.out + row * C + channel, C, up, rows, there, lane);
-        } else if constexpr (kOp == kWgrad) {
-            const size_t at = static_cast<size_t>(t.e) * g.K + t.column + c0;
-            store_rows(g.out + at * C + channel, C, v, rows, there, lane);
         } else {
-            store_rows(g.out + row * C + channel, C, v, rows, there, lane);
+            pack(w, v);
+            const size_t at = kOp == kWgrad ? static_cast<size_t>(t.e) * g.K + t.column + c0 : row;
+            store_rows(g.out + at * C + channel, C, w, win, patch, lane);
         }
     }
+    return true;
 }
 
 // ---------------------------------------------------------------------------- the kernel
@@ -652,24 +754,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!more) break;
             if (lane == 0) tiles.taken(s);
             const uint32_t first = slot, slots = slots_of<kOp>(t);
-            if (t.k > 0) {
+            const auto ready = [&] {
+                if (t.k == 0) return true;
                 bool ok = true;
                 for (uint32_t i = 0; ok && i < slots; ++i)
-                    ok = mbar_wait(&s.sums_full[(slot + i) % 2], (slot + i) / 2 % 2, &s.stop);
-                if (!half_agrees(ok, half)) {
-                    s.stop = 1;
-                    break;
-                }
-                slot += slots;
+                    ok = mbar_wait(&s.sums_full[(first + i) % 2], (first + i) / 2 % 2, &s.stop);
+                ok = half_agrees(ok, half);
                 tc_fence_after();
+                return ok;
+            };
+            if (!finish_tile<kOp>(g, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots), rank, warp,
+                                  lane, ready)) {
+                s.stop = 1;
+                break;
             }
-            finish_tile<kOp>(g, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots), rank, warp, lane);
             if (t.k > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     for (uint32_t i = 0; i < slots; ++i)
                         mbar_arrive_cluster(peer_addr(&s.sums_empty[(first + i) % 2], 0));
+                slot += slots;
             }
         }
     }

@@ -31,9 +31,10 @@ struct Gate {
     float s, slope;  // sigmoid(p(v)), p'(v)
 };
 
-__device__ __forceinline__ Gate gate_of(float v, int act) {
+template <bool kGelu>
+__device__ __forceinline__ Gate gate_of(float v) {
     float p = v, slope = 1.0f;
-    if (act == EP_ACT_GELU) {
+    if (kGelu) {
         constexpr float kA = 1.5957691216057308f, kB = 0.044715f;  // 2 sqrt(2 / pi)
         const float v2 = v * v;
         p = kA * (v + kB * v * v2);
@@ -42,18 +43,12 @@ __device__ __forceinline__ Gate gate_of(float v, int act) {
     return {__fdividef(1.0f, 1.0f + __expf(-p)), slope};
 }
 
-// bf16_rn(amax / 448), in fp32
+// bf16_rn(amax / 448), 0 below 2^-100 (so that its reciprocal is finite)
 __device__ __forceinline__ float checkpoint_scale(float amax) {
-    return bf16_lo(pack_bf16x2_rn(__fdiv_rn(amax, 448.0f), 0.0f));
+    const float scale = bf16_lo(pack_bf16x2_rn(__fdiv_rn(amax, 448.0f), 0.0f));
+    return scale < 0x1p-100f ? 0.0f : scale;
 }
-
-// What a block's values are multiplied by before they become codes; a scale below 2^-126 has
-// no finite reciprocal, and its values take the division (checkpoint_code).
-__device__ __forceinline__ float checkpoint_rcp(float scale) {
-    return scale == 0.0f ? 1.0f : scale < 0x1p-125f ? -1.0f : __frcp_rn(scale);
-}
-__device__ __forceinline__ float checkpoint_quotient(float c, float scale, float rcp) {
-    return rcp < 0.0f ? __fdiv_rn(c, scale) : c * rcp;
-}
+// what a block's values are multiplied by before they become codes
+__device__ __forceinline__ float checkpoint_rcp(float scale) { return scale == 0.0f ? 0.0f : __frcp_rn(scale); }
 
 }  // namespace ep

@@ -142,28 +142,78 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
         : "memory");
 }
 
-// 32 columns of the warp's 32 lanes (lane quarter of the warp): v[j] = column j of this thread's lane
-__device__ __forceinline__ void tmem_load32(float (&v)[32], uint32_t at) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+// ---------------------------------------------------------------------------- 32 x 32 sums a warp
+// A warp's 32 lanes of tensor memory by 32 columns, as the fragments of 8 x 8 matrices that
+// stmatrix and ldmatrix move: v[16 h + 4 q + i] is lane 16 h + 8 (i / 2) + t / 4, column
+// 8 q + 2 (t % 4) + i % 2, for thread t of the warp.
+
+__device__ __forceinline__ void tmem_load_half(float* v, uint32_t at) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(at));
+}
+__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at) {
+    tmem_load_half(v, at);
+    tmem_load_half(v + 16, at + (16u << 16));
 }
 // until the loads are done; the values are used only after it
 __device__ __forceinline__ void tmem_load_wait(float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
-                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
-                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
-                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
-                   "+f"(v[31])
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                   "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+                   "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+                   "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
                  :
+                 : "memory");
+}
+
+// Between fragments and rows: a warp's patch of shared memory, 32 rows (columns of the sums) of
+// 32 channels (lanes) of 16 bits, 64 bytes each. A row's four 16-byte vectors change places with
+// the row, so that both the eight rows of a matrix and two whole rows fall on all banks.
+constexpr uint32_t kPatchBytes = 32 * 64;
+
+__device__ __forceinline__ uint32_t patch_vector(uint32_t patch, int row, int vector) {
+    return patch + row * 64 + ((vector ^ (row / 2 % 4)) * 16);
+}
+// a thread's vector of 8 rows from 8 q on: as the matrices take them, and row by row (row t / 4,
+// vector t % 4: neighbours in memory)
+__device__ __forceinline__ uint32_t matrix_place(uint32_t patch, int q, int lane) {
+    return patch_vector(patch, lane % 8, lane / 8) + q * 512;
+}
+__device__ __forceinline__ uint32_t row_place(uint32_t patch, int q, int lane) {
+    return patch_vector(patch, lane / 4, lane % 4) + q * 512;
+}
+// w[4 q + b]: two columns (8 q + 2 (t % 4) and the next) of lane 8 b + t / 4
+__device__ __forceinline__ void patch_put(uint32_t patch, const uint32_t (&w)[16], int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         matrix_place(patch, q, lane)),
+                     "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                     : "memory");
+}
+__device__ __forceinline__ void patch_get(uint32_t (&w)[16], uint32_t patch, int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * q]), "=r"(w[4 * q + 1]), "=r"(w[4 * q + 2]), "=r"(w[4 * q + 3])
+                     : "r"(matrix_place(patch, q, lane))
+                     : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
 
