@@ -74,7 +74,7 @@ struct Shared {  // behind the stages
     int choice;  // kMostN >> choice rows a tile, of this call
     int scan[4][kThreads / 32];
     float amax[2][2][4][64];  // [half][buffer][warp][gate and up of 32 columns]
-    alignas(16) unsigned char patch[8][kPatchBytes];  // of the finishing warps
+    alignas(512) unsigned char patch[8][kPatchBytes];  // of the finishing warps
     int prefix[1];            // [E + 1] tiles of rows before each expert's (but kWgrad)
 };
 
@@ -389,11 +389,27 @@ __device__ __forceinline__ void load_kept(Kept& kept, const ExpertArgs& g, size_
     }
 }
 
+// A patch as one tensor copy (its places are those of the 64-byte swizzle): rows and channels past
+// the map's ends are left out. Plain 16-byte stores of the same patch, eight rows an instruction,
+// held the gradient of weights with few rows an expert (16384 tokens' 128 uneven experts) at 2.56 ms.
+__device__ __forceinline__ void store_patch(const CUtensorMap& map, int x, int y, int z, const uint32_t (&w)[16],
+                                            unsigned char* patch, bool there, int lane) {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+    patch_put(smem_addr(patch), w, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && there) {
+        tma_store_3d(map, x, y, z, patch);
+        bulk_commit();
+    }
+}
+
 // One warp's part of a tile: 32 channels, every other 32 columns. `ready`, called before the sums
 // are read, waits for them; false: give up.
 template <int kOp, typename Ready>
-__device__ __forceinline__ bool finish_tile(const ExpertArgs& g, Shared& s, const Tile& t, uint32_t sums, uint32_t ups,
-                                            int rank, int warp, int lane, Ready ready) {
+__device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorMap& out_map, Shared& s, const Tile& t,
+                                            uint32_t sums, uint32_t ups, int rank, int warp, int lane, Ready ready) {
     const int half = (warp - kFinish) / 4, quarter = warp % 4;
     const int channel = t.channel + rank * 128 + quarter * 32;  // the warp's first
     const size_t C = static_cast<size_t>(g.C);
@@ -479,10 +495,13 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, Shared& s, cons
                 pack(w, up);
                 store_rows(g.out + row * C + channel, C, w, win, patch, lane);
             }
+        } else if constexpr (kOp == kWgrad) {
+            pack(w, v);
+            store_patch(out_map, channel, t.column + c0, t.e, w, s.patch[warp - kFinish],
+                        win.rows > 0 && win.channels > 0, lane);
         } else {
             pack(w, v);
-            const size_t at = kOp == kWgrad ? static_cast<size_t>(t.e) * g.K + t.column + c0 : row;
-            store_rows(g.out + at * C + channel, C, w, win, patch, lane);
+            store_rows(g.out + row * C + channel, C, w, win, patch, lane);
         }
     }
     return true;
@@ -504,7 +523,7 @@ __device__ __forceinline__ uint32_t up_sums(uint32_t tmem, uint32_t first, uint3
 }
 
 // `a`: the operand along the lanes, `b64` and `b16`: the one along the columns, in boxes of 64 rows
-// (or lines of k) and of 16.
+// (or lines of k) and of 16; in kWgrad, `b16` is the output, in boxes of a warp's patch.
 template <int kOp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b64_map,
@@ -763,8 +782,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            if (!finish_tile<kOp>(g, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots), rank, warp,
-                                  lane, ready)) {
+            if (!finish_tile<kOp>(g, b16_map, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots),
+                                  rank, warp, lane, ready)) {
                 s.stop = 1;
                 break;
             }
@@ -773,10 +792,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     for (uint32_t i = 0; i < slots; ++i)
-                        mbar_arrive_cluster(peer_addr(&s.sums_empty[(first + i) % 2], 0));
+                        mbar_arrive_cluster_relaxed(peer_addr(&s.sums_empty[(first + i) % 2], 0));
                 slot += slots;
             }
         }
+        if (kOp == kWgrad && lane == 0) bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
@@ -802,12 +822,13 @@ ep_status_t zero_fill(void* p, size_t bytes, void* stream) {
 }
 
 // A map of bf16 `dims` (innermost first, dense), in boxes of 64 values by `lines`, swizzled for the
-// tensor cores.
-ep_status_t map_of(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t lines) {
+// tensor cores (or of 32, as patches are).
+ep_status_t map_of(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t lines,
+                   uint32_t values = 64) {
     const uint64_t dims[3] = {d0, d1, d2}, strides[2] = {d0 * 2, d0 * d1 * 2};
-    const uint32_t box[3] = {64, lines, 1};
+    const uint32_t box[3] = {values, lines, 1};
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d2 == 0 ? 2 : 3, base, dims, strides, box,
-                             CU_TENSOR_MAP_SWIZZLE_128B);
+                             values == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 template <int kOp>
@@ -961,10 +982,11 @@ ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* e
     g.status = status;
     if (max_rows == 0) return zero_fill(dw, static_cast<size_t>(E) * I * J * 2, stream);
     const uint64_t n = static_cast<uint64_t>(R) * max_rows;
-    CUtensorMap a, b;
+    CUtensorMap a, b, out;
     ep_status_t st = map_of(&a, rows, J, n, 0, 64);
     if (st == EP_OK) st = map_of(&b, dout, I, n, 0, 64);
-    return st != EP_OK ? st : launch<kWgrad>(g, a, b, b, stream);
+    if (st == EP_OK) st = map_of(&out, dw, J, I, E, 32, 32);
+    return st != EP_OK ? st : launch<kWgrad>(g, a, b, out, stream);
 }
 
 }  // extern "C"
