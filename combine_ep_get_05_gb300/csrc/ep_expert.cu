@@ -389,20 +389,28 @@ __device__ __forceinline__ void load_kept(Kept& kept, const ExpertArgs& g, size_
     }
 }
 
-// A patch as one tensor copy (its places are those of the 64-byte swizzle): rows and channels past
-// the map's ends are left out. Plain 16-byte stores of the same patch, eight rows an instruction,
-// held the gradient of weights with few rows an expert (16384 tokens' 128 uneven experts) at 2.56 ms.
+// A patch as two tensor copies of 16 rows (its places are those of the 64-byte swizzle), each
+// filled while the other is read: rows and channels past the map's ends are left out. Plain
+// 16-byte stores of the same patch, eight rows an instruction, kept a tile's sums some 1500 cycles
+// longer.
 __device__ __forceinline__ void store_patch(const CUtensorMap& map, int x, int y, int z, const uint32_t (&w)[16],
-                                            unsigned char* patch, bool there, int lane) {
-    if (lane == 0) bulk_wait_read_all();
+                                            unsigned char* patch, const Window& win, int lane) {
+    const auto send = [&](int from) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && win.rows > from && win.channels > 0) {
+            tma_store_3d(map, x, y + from, z, patch + from * 64);
+            bulk_commit();
+        }
+    };
+    if (lane == 0) bulk_wait_read<1>();
     __syncwarp();
-    patch_put(smem_addr(patch), w, lane);
-    fence_proxy_async_smem();
+    patch_put<0, 2>(smem_addr(patch), w, lane);
+    send(0);
+    if (lane == 0) bulk_wait_read<1>();
     __syncwarp();
-    if (lane == 0 && there) {
-        tma_store_3d(map, x, y, z, patch);
-        bulk_commit();
-    }
+    patch_put<2, 4>(smem_addr(patch), w, lane);
+    send(16);
 }
 
 // One warp's part of a tile: 32 channels, every other 32 columns. `ready`, called before the sums
@@ -435,8 +443,13 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
         }
         if constexpr (kOp == kGateUp) {
             float up[32];
-            tmem_load(up, ups + c0);
-            tmem_load_wait(up);
+            if (t.k > 0) {
+                tmem_load(up, ups + c0);
+                tmem_load_wait(up);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) up[j] = 0.0f;
+            }
             if (g.out_pre != nullptr) {
                 pack(w, v);
                 store_rows(g.out_pre + row * 2 * C + channel, 2 * C, w, win, patch, lane);
@@ -488,17 +501,16 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
                 activate_bwd<false>(v, gate, up);
             pack(w, gate);
             store_rows(g.out_pre + row * 2 * C + channel, 2 * C, w, win, patch, lane);
-            if (c0 + 64 < t.n) load_kept(kept, g, row + 64, channel, {t.rows - c0 - 64, g.C - channel}, lane);
             pack(w, v);
             store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, w, win, patch, lane);
             if (g.out != nullptr) {
                 pack(w, up);
                 store_rows(g.out + row * C + channel, C, w, win, patch, lane);
             }
+            if (c0 + 64 < t.n) load_kept(kept, g, row + 64, channel, {t.rows - c0 - 64, g.C - channel}, lane);
         } else if constexpr (kOp == kWgrad) {
             pack(w, v);
-            store_patch(out_map, channel, t.column + c0, t.e, w, s.patch[warp - kFinish],
-                        win.rows > 0 && win.channels > 0, lane);
+            store_patch(out_map, channel, t.column + c0, t.e, w, s.patch[warp - kFinish], win, lane);
         } else {
             pack(w, v);
             store_rows(g.out + row * C + channel, C, w, win, patch, lane);
@@ -553,11 +565,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(&s.drain, 1);
         mbar_init_fence();
         s.stop = 0;
+    }
+    if (warp == kTail) tmem_alloc_pair(&s.tmem, kTmemColumns);
+    if (tid == kFinish * 32) {
         prefetch_tensor_map(a_map);
         prefetch_tensor_map(b64_map);
         prefetch_tensor_map(b16_map);
     }
-    if (warp == kTail) tmem_alloc_pair(&s.tmem, kTmemColumns);
+    __syncwarp();
+    cluster_arrive();  // the other CTA waits for these barriers while the tiles are planned
     grid_dependency_wait();  // dependent launch: inputs are ready after this
     if constexpr (kOp == kWgrad) {
         if (blockIdx.x == 0)
@@ -568,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
 
@@ -764,6 +780,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         const int half = (warp - kFinish) / 4;
         uint32_t slot = 0;
+        // A pass without rows while the first sums are made: it brings the code in, which takes
+        // longer than a small tile itself (16 experts of 1024 x 512, 127 tokens: 2 us of 13).
+        t = {0, 0, 0, 64, 0, 0, 0};
+        finish_tile<kOp>(g, b16_map, s, t, tmem, tmem, rank, warp, lane, [] { return true; });
         while (true) {
             const bool more = tiles.next(s, &t);
             if (!half_agrees(tiles.ok, half)) {
@@ -800,13 +820,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // neither CTA's shared or tensor memory is used by the other any more
+    cluster_sync_relaxed();  // neither CTA's shared or tensor memory is used by the other any more
     if (warp == kTail) {
         tc_fence_after();
         tmem_free_pair(tmem, kTmemColumns);
     }
-    cluster_sync();
 }
 
 bool valid(int E, int R, int max_rows) {
@@ -985,7 +1003,7 @@ ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* e
     CUtensorMap a, b, out;
     ep_status_t st = map_of(&a, rows, J, n, 0, 64);
     if (st == EP_OK) st = map_of(&b, dout, I, n, 0, 64);
-    if (st == EP_OK) st = map_of(&out, dw, J, I, E, 32, 32);
+    if (st == EP_OK) st = map_of(&out, dw, J, I, E, 16, 32);
     return st != EP_OK ? st : launch<kWgrad>(g, a, b, out, stream);
 }
 

@@ -27,8 +27,12 @@ __device__ __forceinline__ bool elected() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// the cluster's barrier in two parts: what the threads wrote before arriving is seen after waiting
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the same without order for memory accesses (a release waits until all stores have reached L2)
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // the address, in the cluster's window, of `p`'s counterpart in CTA `rank`
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -192,10 +196,11 @@ __device__ __forceinline__ uint32_t matrix_place(uint32_t patch, int q, int lane
 __device__ __forceinline__ uint32_t row_place(uint32_t patch, int q, int lane) {
     return patch_vector(patch, lane / 4, lane % 4) + q * 512;
 }
-// w[4 q + b]: two columns (8 q + 2 (t % 4) and the next) of lane 8 b + t / 4
+// w[4 q + b]: two columns (8 q + 2 (t % 4) and the next) of lane 8 b + t / 4; from row 8 kFrom to 8 kTo
+template <int kFrom = 0, int kTo = 4>
 __device__ __forceinline__ void patch_put(uint32_t patch, const uint32_t (&w)[16], int lane) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = kFrom; q < kTo; ++q)
         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                          matrix_place(patch, q, lane)),
                      "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
