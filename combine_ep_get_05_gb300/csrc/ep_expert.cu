@@ -17,8 +17,10 @@ using namespace ep;
 
 enum Op { kGateUp, kDown, kDownBwd, kGateUpBwd, kWgrad };
 
-constexpr int kThreads = 384;        // 4 warps that feed and multiply, 8 that finish tiles
-constexpr int kProducer = 0, kMultiplier = 1, kTail = 2, kScheduler = 3, kFinish = 4;  // first warp of each part
+// Warps: two that copy the operands in, one that multiplies, one that clears tails, one that plans
+// tiles, and four groups of four (32 lanes of the sums each) that finish them.
+constexpr int kProducer = 0, kMultiplier = 1, kTail = 2, kScheduler = 3, kFinish = 4, kGroups = 4;
+constexpr int kFinishWarps = 4 * kGroups, kLastFinish = kFinish + kFinishWarps - 1;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSlotColumns = 256;  // of tensor memory: two tiles at a time
 constexpr int kMostStages = 8;
@@ -34,6 +36,11 @@ struct Traits {
     static constexpr uint32_t kABytes = (kGated ? 2 : 1) * 128 * kBlockK * 2;
     static constexpr uint32_t kBBytes = kMostN / 2 * kBlockK * 2;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes;  // of one CTA
+    static constexpr int kPatches = kOp == kWgrad ? 2 : 1;      // a finishing warp (kWgrad: four of a pair)
+    // the second warp that copies in: the tails' place where there are none (20 warps leave 96
+    // registers a thread, 21 no more than 80)
+    static constexpr int kColumnProducer = kOp == kWgrad ? kLastFinish + 1 : kTail;
+    static constexpr int kThreads = 32 * (kOp == kWgrad ? kLastFinish + 2 : kLastFinish + 1);
 };
 
 struct ExpertArgs {
@@ -63,7 +70,7 @@ struct Tile {
     int k;          // products of a sum
 };
 
-struct Shared {  // behind the stages
+struct Planned {
     // a stage's bytes have come (CTA 0: both CTAs'), its products are done; a last stage of
     // kWgrad: the CTA's own bytes have come, both CTAs have cleared its tail
     uint64_t full[kMostStages], empty[kMostStages], part[kMostStages], ready[kMostStages];
@@ -72,10 +79,14 @@ struct Shared {  // behind the stages
     uint32_t tmem;
     int stop;    // a wait gave up
     int choice;  // kMostN >> choice rows a tile, of this call
-    int scan[4][kThreads / 32];
-    float amax[2][2][4][64];  // [half][buffer][warp][gate and up of 32 columns]
-    alignas(512) unsigned char patch[8][kPatchBytes];  // of the finishing warps
-    int prefix[1];            // [E + 1] tiles of rows before each expert's (but kWgrad)
+    int scan[4][32];  // of the plan: a warp's tiles, for each choice
+};
+
+template <int kOp>
+struct Shared : Planned {  // behind the stages
+    alignas(1024) unsigned char patch[kFinishWarps * Traits<kOp>::kPatches][kPatchBytes];
+    float amax[kOp == kGateUp ? kGroups * 2 * 4 : 1][2 * kChunk];  // [group, buffer, warp][gate and up]
+    int prefix[1];  // [E + 1] tiles of rows before each expert's (but kWgrad)
 };
 
 // The tiles of a role, in order. next() is false where there are no more, or a wait gave up (`ok`);
@@ -83,14 +94,14 @@ struct Shared {  // behind the stages
 struct Tiles {
     uint32_t at = kTiles - 1, phase = 1;
     bool ok = true;
-    __device__ __forceinline__ bool next(Shared& s, Tile* t) {
+    __device__ __forceinline__ bool next(Planned& s, Tile* t) {
         if (++at == kTiles) at = 0, phase ^= 1;
         ok = mbar_wait(&s.tile_full[at], phase, &s.stop);
         if (!ok) return false;
         *t = s.tile[at];
         return t->e >= 0;
     }
-    __device__ __forceinline__ void taken(Shared& s) { mbar_arrive(&s.tile_empty[at]); }
+    __device__ __forceinline__ void taken(Planned& s) { mbar_arrive(&s.tile_empty[at]); }
 };
 
 // Tiles of an expert's rows, of most_n = kMostN >> choice rows at most, and rows of each: even
@@ -101,8 +112,28 @@ __device__ __forceinline__ int row_tiles(int count, int choice) {
 }
 __device__ __forceinline__ int rows_each(int count, int tiles) { return ((count + tiles - 1) / tiles + 31) & ~31; }
 
+// Tile l of an expert that has r.count rows. Eight tiles of rows with all channels, then the next
+// eight: the rows that are at work at a time, and the weights that they share, stay in L2.
+__device__ __forceinline__ void tile_of(const ExpertArgs& g, int choice, int e, const ExpertRows& r, uint32_t l,
+                                        Tile* tile) {
+    const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
+    const int tiles = row_tiles(r.count, choice), each = rows_each(r.count, tiles);
+    const uint32_t group = l / (8 * across);
+    l -= group * 8 * across;
+    const uint32_t left = tiles - group * 8, width = left < 8 ? left : 8;
+    const int i = static_cast<int>(group * 8 + l % width);
+    tile->e = e;
+    tile->row = r.first + static_cast<long long>(i) * each;
+    tile->rows = r.count - i * each < each ? r.count - i * each : each;
+    tile->n = (tile->rows + 31) / 32 * 32;
+    tile->channel = static_cast<int>(l / width * 256);
+    tile->column = 0;
+    tile->k = g.K;
+}
+
+// Tile t of the call; false where there are not so many.
 template <int kOp>
-__device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared& s, uint32_t t, Tile* tile) {
+__device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared<kOp>& s, uint32_t t, Tile* tile) {
     const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
     if (kOp == kWgrad) {
         const uint32_t down = (static_cast<uint32_t>(g.K) + 255) / 256;
@@ -128,73 +159,75 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared& s, ui
         else
             hi = mid;
     }
-    const ExpertRows r = expert_rows(g.offsets, lo, g.E / g.R, g.max_rows);
-    const int tiles = row_tiles(r.count, s.choice), each = rows_each(r.count, tiles);
-    // eight tiles of rows with all channels, then the next eight: the rows that are at work at a
-    // time, and the weights that they share, stay in L2
-    uint32_t l = t - s.prefix[lo] * across;
-    const uint32_t group = l / (8 * across);
-    l -= group * 8 * across;
-    const uint32_t left = tiles - group * 8, width = left < 8 ? left : 8;
-    const int i = static_cast<int>(group * 8 + l % width);
-    tile->e = lo;
-    tile->row = r.first + static_cast<long long>(i) * each;
-    tile->rows = r.count - i * each < each ? r.count - i * each : each;
-    tile->n = (tile->rows + 31) / 32 * 32;
-    tile->channel = static_cast<int>(l / width * 256);
-    tile->column = 0;
-    tile->k = g.K;
+    tile_of(g, s.choice, lo, expert_rows(g.offsets, lo, g.E / g.R, g.max_rows), t - s.prefix[lo] * across, tile);
     return true;
 }
 
-// The number of tiles of rows before each expert's, by all threads. A tile has 256 rows at
-// most, or 128, 64 or 32 where the tiles would not fill the GPU otherwise.
-__device__ void plan_tiles(const ExpertArgs& g, Shared& s) {
+// The number of tiles of rows before each expert's, by all threads, and the pair's first tile, by
+// the thread that meets it. A tile has 256 rows at most, or 128, 64 or 32 where the tiles would not
+// fill the GPU otherwise.
+template <int kOp>
+__device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, uint32_t pair, uint32_t pairs) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    constexpr int kThreads = Traits<kOp>::kThreads;
     const int per = (g.E + kThreads - 1) / kThreads, first = tid * per;
     const int last = first + per < g.E ? first + per : g.E;
-    const int across = (g.C + 255) / 256, pairs = static_cast<int>(gridDim.x / 2);
-    int count = 0, sum[4] = {0, 0, 0, 0};
+    const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
+    ExpertRows r = {0, 0, false};
+    int sum[4] = {0, 0, 0, 0};
     for (int e = first; e < last; ++e) {
-        const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
         if (r.dropped && blockIdx.x == 0) raise_flag(g.status, EP_FLAG_CAPACITY);
-        count = r.count;
-        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(count, i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(r.count, i);
     }
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(sum[i])));
         if (lane == 0) s.scan[i][warp] = n;
     }
     __syncthreads();
-    int choice = 0, before = 0, mine = 0;
-    for (; choice < 4; ++choice) {
-        int total = 0;
-        before = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += s.scan[choice][w];
-            total += s.scan[choice][w];
-        }
-        mine = choice == 0 ? sum[0] : choice == 1 ? sum[1] : choice == 2 ? sum[2] : sum[3];
-        if (choice == 3 || static_cast<long long>(total) * across >= pairs) break;
+    // lane w of every warp has warp w's sum of the choice
+    static_assert(kThreads <= 32 * 32);
+    int choice = 0, mine = sum[0], others = 0;
+    uint32_t total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        others = lane < kThreads / 32 ? s.scan[i][lane] : 0;
+        total = __reduce_add_sync(kFullMask, static_cast<unsigned>(others));
+        choice = i;
+        mine = sum[i];
+        if (total * across >= pairs) break;
     }
+    int before = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(lane < warp ? others : 0)));
     int upto = mine;
+#pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int v = __shfl_up_sync(kFullMask, upto, d);
         if (lane >= d) upto += v;
     }
     before += upto - mine;
     for (int e = first; e < last; ++e) {
+        if (per > 1) r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        const uint32_t begin = static_cast<uint32_t>(before) * across;
         s.prefix[e] = before;
-        if (per > 1) count = expert_rows(g.offsets, e, g.E / g.R, g.max_rows).count;
-        before += row_tiles(count, choice);
+        before += row_tiles(r.count, choice);
+        if (begin <= pair && pair < before * across) {
+            Tile t;
+            tile_of(g, choice, e, r, pair - begin, &t);
+            s.tile[0] = t;
+        }
         if (e == g.E - 1) s.prefix[g.E] = before;
     }
-    if (tid == 0) s.choice = choice;
+    if (tid == 0) {
+        s.choice = choice;
+        if (pair >= total * across) s.tile[0].e = -1;
+    }
 }
 
 // ---------------------------------------------------------------------------- finishing a tile
 
-// 32 rows of 32 channels, of which `rows` and, 8 at a time, `channels` are there: 16-byte vectors of
+// 16 rows of 32 channels, of which `rows` and, 8 at a time, `channels` are there: 16-byte vectors of
 // bf16, 8-byte ones of codes, four neighbouring lanes a row.
 struct Window {
     int rows, channels;
@@ -203,39 +236,39 @@ struct Window {
     }
 };
 
-__device__ __forceinline__ void store_rows(uint16_t* to, size_t stride, const uint32_t (&w)[16], const Window& win,
+__device__ __forceinline__ void store_rows(uint16_t* to, size_t stride, const uint32_t (&w)[8], const Window& win,
                                            uint32_t patch, int lane) {
     __syncwarp();  // what was in the patch has been read
     patch_put(patch, w, lane);
     __syncwarp();
     to += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         const uint4 v = ld_shared_v4(row_place(patch, q, lane));
         if (win.has(q, lane)) st_v4(to + 8 * q * stride, v);
     }
 }
-__device__ __forceinline__ void load_rows(uint4 (&v)[4], const uint16_t* from, size_t stride, const Window& win,
+__device__ __forceinline__ void load_rows(uint4 (&v)[2], const uint16_t* from, size_t stride, const Window& win,
                                           int lane) {
     from += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
         v[q] = win.has(q, lane) ? ld_stream_v4(from + 8 * q * stride) : make_uint4(0, 0, 0, 0);
 }
 // rows into fragments
-__device__ __forceinline__ void spread(uint32_t (&w)[16], const uint4 (&v)[4], uint32_t patch, int lane) {
+__device__ __forceinline__ void spread(uint32_t (&w)[8], const uint4 (&v)[2], uint32_t patch, int lane) {
     __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) st_shared_v4(row_place(patch, q, lane), v[q]);
+    for (int q = 0; q < 2; ++q) st_shared_v4(row_place(patch, q, lane), v[q]);
     __syncwarp();
     patch_get(w, patch, lane);
 }
-__device__ __forceinline__ void pack(uint32_t (&w)[16], const float (&v)[32]) {
+__device__ __forceinline__ void pack(uint32_t (&w)[8], const float (&v)[16]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            const int i = fragment(q, b);
             w[4 * q + b] = pack_bf16x2_rn(v[i], v[i + 1]);
         }
 }
@@ -251,19 +284,19 @@ __device__ __forceinline__ uint32_t codes_of_f16x2(uint32_t two) {
     return r;
 }
 
-// Codes of 32 rows of one block of 128 channels, of which the warp has 32; rcp: lane j has row j's.
+// Codes of 16 rows of one block of 128 channels, of which the warp has 32; rcp: lane j has row j's.
 // The quotients go through the patch as fp16, whose 11 bits leave the rounding to 4 as it is but
 // beside a midpoint of codes (by 2^-12 of the value).
-__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const float (&v)[32], float rcp,
+__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const float (&v)[16], float rcp,
                                             const Window& win, uint32_t patch, int lane) {
-    uint32_t w[16];
+    uint32_t w[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         const float r0 = __shfl_sync(kFullMask, rcp, 8 * q + lane % 4 * 2);
         const float r1 = __shfl_sync(kFullMask, rcp, 8 * q + lane % 4 * 2 + 1);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            const int i = fragment(q, b);
             w[4 * q + b] = pack_f16x2_rn(v[i] * r0, v[i + 1] * r1);
         }
     }
@@ -272,18 +305,18 @@ __device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const fl
     __syncwarp();
     to += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         const uint4 f = ld_shared_v4(row_place(patch, q, lane));
         const uint32_t a = codes_of_f16x2(f.x) | codes_of_f16x2(f.y) << 16;
         const uint32_t b = codes_of_f16x2(f.z) | codes_of_f16x2(f.w) << 16;
         if (win.has(q, lane)) st_v2(to + 8 * q * stride, a, b);
     }
 }
-__device__ __forceinline__ void load_codes(uint4 (&v)[4], const uint8_t* from, size_t stride, const Window& win,
+__device__ __forceinline__ void load_codes(uint4 (&v)[2], const uint8_t* from, size_t stride, const Window& win,
                                            int lane) {
     from += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         const uint2 c = win.has(q, lane) ? __ldg(reinterpret_cast<const uint2*>(from + 8 * q * stride))
                                          : make_uint2(0, 0);
         v[q].x = c.x;
@@ -291,46 +324,46 @@ __device__ __forceinline__ void load_codes(uint4 (&v)[4], const uint8_t* from, s
     }
 }
 // codes into fragments of fp16 (every code is one), times their scales; scale: lane j has row j's
-__device__ __forceinline__ void spread_codes(float (&v)[32], const uint4 (&c)[4], float scale, uint32_t patch,
+__device__ __forceinline__ void spread_codes(float (&v)[16], const uint4 (&c)[2], float scale, uint32_t patch,
                                              int lane) {
-    uint4 f[4];
+    uint4 f[2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
         f[q] = make_uint4(e4m3x2_to_f16x2(c[q].x), e4m3x2_to_f16x2(c[q].x >> 16), e4m3x2_to_f16x2(c[q].y),
                           e4m3x2_to_f16x2(c[q].y >> 16));
-    uint32_t w[16];
+    uint32_t w[8];
     spread(w, f, patch, lane);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         const float s0 = __shfl_sync(kFullMask, scale, 8 * q + lane % 4 * 2);
         const float s1 = __shfl_sync(kFullMask, scale, 8 * q + lane % 4 * 2 + 1);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            const int i = fragment(q, b);
             v[i] = f16_to_f32(w[4 * q + b] & 0xffffu) * s0;
             v[i + 1] = f16_to_f32(w[4 * q + b] >> 16) * s1;
         }
     }
 }
-__device__ __forceinline__ void unpack(float (&v)[32], const uint32_t (&w)[16]) {
+__device__ __forceinline__ void unpack(float (&v)[16], const uint32_t (&w)[8]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int i = 16 * (b / 2) + 4 * q + 2 * (b % 2);
+            const int i = fragment(q, b);
             v[i] = bf16_lo(w[4 * q + b]);
             v[i + 1] = bf16_hi(w[4 * q + b]);
         }
 }
 
 // max |v| of every column over the warp's lanes, NaN apart, into to[column]
-__device__ __forceinline__ void column_max(float* to, const float (&v)[32], int lane) {
+__device__ __forceinline__ void column_max(float* to, const float (&v)[16], int lane) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float m = fmaxf(fmaxf(fabsf(v[4 * q + i]), fabsf(v[4 * q + 2 + i])),
-                            fmaxf(fabsf(v[16 + 4 * q + i]), fabsf(v[16 + 4 * q + 2 + i])));
+                            fmaxf(fabsf(v[8 + 4 * q + i]), fabsf(v[8 + 4 * q + 2 + i])));
             m = m == m ? m : 0.0f;  // all of them NaN
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
@@ -339,38 +372,49 @@ __device__ __forceinline__ void column_max(float* to, const float (&v)[32], int 
 }
 
 template <bool kGelu>
-__device__ __forceinline__ void activate(float (&v)[32], const float (&up)[32]) {
+__device__ __forceinline__ void activate(float (&v)[16], const float (&up)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = v[j] * gate_of<kGelu>(v[j]).s * up[j];
+    for (int j = 0; j < 16; ++j) v[j] = v[j] * gate_of<kGelu>(v[j]).s * up[j];
 }
-// dh in v, gate and up -> dup in v, dgate in gate, h in up
+// dh, gate and up into dgate, dup and h, packed
 template <bool kGelu>
-__device__ __forceinline__ void activate_bwd(float (&v)[32], float (&gate)[32], float (&up)[32]) {
+__device__ __forceinline__ void activate_bwd(uint32_t (&dgate)[8], uint32_t (&dup)[8], uint32_t (&h)[8],
+                                             const float (&dh)[16], const float (&gate)[16], const float (&up)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const Gate a = gate_of<kGelu>(gate[j]);
-        const float act = gate[j] * a.s;
-        gate[j] = v[j] * up[j] * (a.s + act * (1.0f - a.s) * a.slope);
-        v[j] *= act;
-        up[j] *= act;
-    }
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float dg[2], du[2], hh[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = fragment(q, b) + j;
+                const Gate a = gate_of<kGelu>(gate[i]);
+                const float act = gate[i] * a.s;
+                dg[j] = dh[i] * up[i] * (a.s + act * (1.0f - a.s) * a.slope);
+                du[j] = dh[i] * act;
+                hh[j] = act * up[i];
+            }
+            dgate[4 * q + b] = pack_bf16x2_rn(dg[0], dg[1]);
+            dup[4 * q + b] = pack_bf16x2_rn(du[0], du[1]);
+            h[4 * q + b] = pack_bf16x2_rn(hh[0], hh[1]);
+        }
 }
 
-// true in all 128 threads of a half of the finishing warps, or in none
-__device__ __forceinline__ bool half_agrees(bool ok, int half) {
+// true in all 128 threads of a group of finishing warps, or in none
+__device__ __forceinline__ bool group_agrees(bool ok, int group) {
     int r;
     asm volatile(
         "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n"
         " selp.s32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"(static_cast<int>(ok)), "r"(1 + half)
+        : "r"(static_cast<int>(ok)), "r"(1 + group)
         : "memory");
     return r != 0;
 }
 
-// What the gradient reads of 32 rows of the checkpoint, on its way.
+// What the gradient reads of 16 rows of the checkpoint, on its way.
 struct Kept {
-    uint4 gate[4], up[4];        // bf16, or codes in x and y,
+    uint4 gate[2], up[2];        // bf16, or codes in x and y,
     float gate_scale, up_scale;  // and lane j's row's scales
 };
 __device__ __forceinline__ void load_kept(Kept& kept, const ExpertArgs& g, size_t row, int channel, const Window& win,
@@ -382,43 +426,43 @@ __device__ __forceinline__ void load_kept(Kept& kept, const ExpertArgs& g, size_
     } else {
         load_codes(kept.gate, g.pre_q + at, 2 * C, win, lane);
         load_codes(kept.up, g.pre_q + at + C, 2 * C, win, lane);
-        const bool there = lane < win.rows && win.channels > 0;
+        const bool there = lane < kChunk && lane < win.rows && win.channels > 0;
         const uint16_t* scales = g.pre_scales + (row + lane) * (2 * C / 128) + channel / 128;
         kept.gate_scale = there ? __uint_as_float(static_cast<uint32_t>(__ldg(scales)) << 16) : 0.0f;
         kept.up_scale = there ? __uint_as_float(static_cast<uint32_t>(__ldg(scales + C / 128)) << 16) : 0.0f;
     }
 }
 
-// A patch as two tensor copies of 16 rows (its places are those of the 64-byte swizzle), each
-// filled while the other is read: rows and channels past the map's ends are left out. Plain
-// 16-byte stores of the same patch, eight rows an instruction, kept a tile's sums some 1500 cycles
-// longer.
-__device__ __forceinline__ void store_patch(const CUtensorMap& map, int x, int y, int z, const uint32_t (&w)[16],
-                                            unsigned char* patch, const Window& win, int lane) {
-    const auto send = [&](int from) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && win.rows > from && win.channels > 0) {
-            tma_store_3d(map, x, y + from, z, patch + from * 64);
-            bulk_commit();
-        }
-    };
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    patch_put<0, 2>(smem_addr(patch), w, lane);
-    send(0);
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    patch_put<2, 4>(smem_addr(patch), w, lane);
-    send(16);
+// all 64 threads of two neighbouring finishing warps
+__device__ __forceinline__ void pair_sync(int warp) {
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + kGroups + (warp - kFinish) / 2) : "memory");
+}
+// 16 rows of two warps' 64 channels as one tensor copy, from one of two patches that are filled in
+// turn: rows and channels past the map's ends are left out. The copies' rows cost alike whatever
+// their length (a tile's sums of 64-byte rows, a patch a warp, took twice as long), and plain
+// 16-byte stores longer still.
+__device__ __forceinline__ void store_patch(const CUtensorMap& map, int x, int y, int z, const uint32_t (&w)[8],
+                                            unsigned char* patch, const Window& win, int warp, int lane) {
+    const int side = warp % 2;
+    const bool sends = side == 0 && lane == 0;
+    if (sends) bulk_wait_read<1>();
+    pair_sync(warp);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) matrices_put(wide_matrix_place(smem_addr(patch), q, side, lane), w, q);
+    fence_proxy_async_smem();
+    pair_sync(warp);
+    if (sends && win.rows > 0 && win.channels > 0) {
+        tma_store_3d(map, x, y, z, patch);
+        bulk_commit();
+    }
 }
 
-// One warp's part of a tile: 32 channels, every other 32 columns. `ready`, called before the sums
+// One warp's part of a tile: 32 channels, every fourth 16 columns. `ready`, called before the sums
 // are read, waits for them; false: give up.
 template <int kOp, typename Ready>
-__device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorMap& out_map, Shared& s, const Tile& t,
+__device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorMap& out_map, Shared<kOp>& s, const Tile& t,
                                             uint32_t sums, uint32_t ups, int rank, int warp, int lane, Ready ready) {
-    const int half = (warp - kFinish) / 4, quarter = warp % 4;
+    const int group = (warp - kFinish) / 4, quarter = warp % 4;
     const int channel = t.channel + rank * 128 + quarter * 32;  // the warp's first
     const size_t C = static_cast<size_t>(g.C);
     const uint32_t patch = smem_addr(s.patch[warp - kFinish]);
@@ -426,29 +470,29 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
     ups += static_cast<uint32_t>(quarter * 32) << 16;
     Kept kept;
     if constexpr (kOp == kDownBwd)  // on its way while the sums are made
-        load_kept(kept, g, static_cast<size_t>(t.row) + half * 32, channel, {t.rows - half * 32, g.C - channel}, lane);
+        load_kept(kept, g, static_cast<size_t>(t.row) + group * kChunk, channel, {t.rows - group * kChunk, g.C - channel}, lane);
     if (!ready()) return false;
     int buffer = 0;
-    for (int c0 = half * 32; c0 < t.n; c0 += 64) {
+    for (int c0 = group * kChunk; c0 < t.n; c0 += kGroups * kChunk) {
         const Window win = {t.rows - c0, g.C - channel};
         const size_t row = static_cast<size_t>(t.row) + c0;
-        uint32_t w[16];
-        float v[32];
+        uint32_t w[8];
+        float v[16];
         if (t.k > 0) {
             tmem_load(v, sums + c0);
             tmem_load_wait(v);
         } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
         }
         if constexpr (kOp == kGateUp) {
-            float up[32];
+            float up[16];
             if (t.k > 0) {
                 tmem_load(up, ups + c0);
                 tmem_load_wait(up);
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) up[j] = 0.0f;
+                for (int j = 0; j < 16; ++j) up[j] = 0.0f;
             }
             if (g.out_pre != nullptr) {
                 pack(w, v);
@@ -457,20 +501,20 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
                 store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, w, win, patch, lane);
             }
             if (g.out_q != nullptr) {
-                float(&amax)[4][64] = s.amax[half][buffer];
+                float(*const amax)[2 * kChunk] = &s.amax[(group * 2 + buffer) * 4];
                 buffer ^= 1;
                 column_max(amax[quarter], v, lane);
-                column_max(amax[quarter] + 32, up, lane);
-                asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+                column_max(amax[quarter] + kChunk, up, lane);
+                asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
                 float a = 0.0f, b = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    a = fmaxf(a, amax[i][lane]);
-                    b = fmaxf(b, amax[i][32 + lane]);
+                    a = fmaxf(a, amax[i][lane % kChunk]);
+                    b = fmaxf(b, amax[i][kChunk + lane % kChunk]);
                 }
                 a = checkpoint_scale(a);
                 b = checkpoint_scale(b);
-                if (quarter == 0 && lane < win.rows && win.channels > 0) {
+                if (quarter == 0 && lane < kChunk && lane < win.rows && win.channels > 0) {
                     uint16_t* const scales = g.out_scales + (row + lane) * (2 * C / 128) + channel / 128;
                     scales[0] = static_cast<uint16_t>(__float_as_uint(a) >> 16);
                     scales[C / 128] = static_cast<uint16_t>(__float_as_uint(b) >> 16);
@@ -485,7 +529,7 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
             pack(w, v);
             store_rows(g.out + row * C + channel, C, w, win, patch, lane);
         } else if constexpr (kOp == kDownBwd) {
-            float gate[32], up[32];
+            float gate[16], up[16];
             if (g.pre != nullptr) {
                 spread(w, kept.gate, patch, lane);
                 unpack(gate, w);
@@ -495,22 +539,21 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
                 spread_codes(gate, kept.gate, kept.gate_scale, patch, lane);
                 spread_codes(up, kept.up, kept.up_scale, patch, lane);
             }
+            uint32_t dup[8], h[8];
             if (g.act == EP_ACT_GELU)
-                activate_bwd<true>(v, gate, up);
+                activate_bwd<true>(w, dup, h, v, gate, up);
             else
-                activate_bwd<false>(v, gate, up);
-            pack(w, gate);
-            store_rows(g.out_pre + row * 2 * C + channel, 2 * C, w, win, patch, lane);
-            pack(w, v);
-            store_rows(g.out_pre + row * 2 * C + C + channel, 2 * C, w, win, patch, lane);
-            if (g.out != nullptr) {
-                pack(w, up);
-                store_rows(g.out + row * C + channel, C, w, win, patch, lane);
-            }
-            if (c0 + 64 < t.n) load_kept(kept, g, row + 64, channel, {t.rows - c0 - 64, g.C - channel}, lane);
+                activate_bwd<false>(w, dup, h, v, gate, up);
+            uint16_t* const dpre = g.out_pre + row * 2 * C + channel;
+            store_rows(dpre, 2 * C, w, win, patch, lane);
+            store_rows(dpre + C, 2 * C, dup, win, patch, lane);
+            if (g.out != nullptr) store_rows(g.out + row * C + channel, C, h, win, patch, lane);
+            if (c0 + kGroups * kChunk < t.n) load_kept(kept, g, row + kGroups * kChunk, channel, {t.rows - c0 - kGroups * kChunk, g.C - channel}, lane);
         } else if constexpr (kOp == kWgrad) {
             pack(w, v);
-            store_patch(out_map, channel, t.column + c0, t.e, w, s.patch[warp - kFinish], win, lane);
+            store_patch(out_map, channel, t.column + c0, t.e, w,
+                        s.patch[(warp - kFinish) / 2 * 4 + buffer * 2], win, warp, lane);
+            buffer ^= 1;
         } else {
             pack(w, v);
             store_rows(g.out + row * C + channel, C, w, win, patch, lane);
@@ -534,21 +577,30 @@ __device__ __forceinline__ uint32_t up_sums(uint32_t tmem, uint32_t first, uint3
     return slots == 2 ? tmem + (first + 1) % 2 * kSlotColumns : tmem + first % 2 * kSlotColumns + kSlotColumns / 2;
 }
 
+// bytes of a CTA's part of the operand along the lanes that lie before the last channel
+template <int kOp>
+__device__ __forceinline__ uint32_t a_bytes(int channels) {
+    if (!Traits<kOp>::kAAcross) return channels > 0 ? Traits<kOp>::kABytes : 0;
+    return channels > 64 ? 2 * kCrossBlock : channels > 0 ? kCrossBlock : 0;
+}
+
 // `a`: the operand along the lanes, `b64` and `b16`: the one along the columns, in boxes of 64 rows
 // (or lines of k) and of 16; in kWgrad, `b16` is the output, in boxes of a warp's patch.
 template <int kOp>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b64_map,
                   const __grid_constant__ CUtensorMap b16_map, ExpertArgs g) {
     using Tr = Traits<kOp>;
     extern __shared__ __align__(1024) unsigned char s_stages[];
-    Shared& s = *reinterpret_cast<Shared*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
+    Shared<kOp>& s = *reinterpret_cast<Shared<kOp>*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     const int rank = static_cast<int>(cluster_rank());
     const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
-    if (tid == 0) {
-        for (int i = 0; i < g.stages; ++i) {
+    // by warps that have few experts to plan, while the others ask for theirs
+    allow_dependents();  // every CTA of the grid is resident: the next kernel takes no place from it
+    if (tid == (kLastFinish - 1) * 32) {
+        for (int i = 0; i < kMostStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
             mbar_init(&s.part[i], 1);
@@ -556,18 +608,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.sums_full[i], 1);
-            mbar_init(&s.sums_empty[i], 16);  // the finishing warps of both CTAs
+            mbar_init(&s.sums_empty[i], 2 * kFinishWarps);  // of both CTAs
         }
         for (int i = 0; i < kTiles; ++i) {
             mbar_init(&s.tile_full[i], 1);
-            mbar_init(&s.tile_empty[i], 9 + (rank == 0 ? 1 : 0) + (kOp == kWgrad ? 1 : 0));
+            // both producers, the finishing warps; the multiplier in CTA 0; the tail's warp
+            mbar_init(&s.tile_empty[i], 2 + kFinishWarps + (rank == 0 ? 1 : 0) + (kOp == kWgrad ? 1 : 0));
         }
         mbar_init(&s.drain, 1);
         mbar_init_fence();
         s.stop = 0;
     }
-    if (warp == kTail) tmem_alloc_pair(&s.tmem, kTmemColumns);
-    if (tid == kFinish * 32) {
+    if (warp == kLastFinish) tmem_alloc_pair(&s.tmem, kTmemColumns);
+    if (tid == (kLastFinish - 2) * 32) {
         prefetch_tensor_map(a_map);
         prefetch_tensor_map(b64_map);
         prefetch_tensor_map(b16_map);
@@ -576,12 +629,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_arrive();  // the other CTA waits for these barriers while the tiles are planned
     grid_dependency_wait();  // dependent launch: inputs are ready after this
     if constexpr (kOp == kWgrad) {
+        if (tid == 0) {
+            Tile first;
+            if (!tile_at<kOp>(g, s, pair, &first)) first.e = -1;
+            s.tile[0] = first;
+        }
         if (blockIdx.x == 0)
-            for (int e = tid; e < g.E; e += kThreads)
+            for (int e = tid; e < g.E; e += Tr::kThreads)
                 if (expert_rows(g.offsets, e, g.E / g.R, g.max_rows).dropped) raise_flag(g.status, EP_FLAG_CAPACITY);
     } else {
-        plan_tiles(g, s);
+        plan_tiles<kOp>(g, s, pair, pairs);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_wait();
@@ -592,9 +651,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Tiles tiles;
     if (warp == kScheduler) {
         if (lane == 0) {
-            uint32_t at = 0, phase = 0;
-            for (uint32_t i = pair;; i += pairs) {
-                const bool more = tile_at<kOp>(g, s, i, &t);
+            bool more = s.tile[0].e >= 0;  // the first tile is there
+            mbar_arrive(&s.tile_full[0]);
+            uint32_t at = 1, phase = 0;
+            for (uint32_t i = pair + pairs; more; i += pairs) {
+                more = tile_at<kOp>(g, s, i, &t);
                 if (!more) t.e = -1;
                 if (!mbar_wait(&s.tile_empty[at], phase ^ 1, &s.stop)) {
                     s.stop = 1;
@@ -603,12 +664,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 s.tile[at] = t;
                 mbar_arrive(&s.tile_full[at]);
                 if (++at == kTiles) at = 0, phase ^= 1;
-                if (!more) break;
             }
         }
-    } else if (warp == kProducer) {
-        // the whole warp keeps the books, so that they stay uniform; one lane issues
-        const bool leader = elected();
+    } else if (warp == kProducer || warp == Tr::kColumnProducer) {
+        // One warp copies the operand along the lanes (and counts the bytes of both), the other the one
+        // along the columns: a stage's copies take one thread longer to issue than to multiply. The whole
+        // warp keeps the books, so that they stay uniform; one lane issues.
+        const bool leader = elected(), lanes = warp == kProducer;
         int stage = 0;
         uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
         uint32_t issued = 0;
@@ -618,11 +680,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (leader) tiles.taken(s);
             const int half = t.n / 2;
             const int b_first = rank * half;
-            // bytes of this CTA's half of a stage: whole boxes, also where they hang over an end
+            // Bytes of a half of a stage: whole boxes, also where they hang over an end. Boxes that lie
+            // past the last channel are left out: the sums of what is in their place are not kept.
             const uint32_t b_bytes = kOp == kWgrad ? (half + 63) / 64 * kCrossBlock
                                                    : static_cast<uint32_t>(half) * kBlockK * 2;
-            const uint32_t bytes = Tr::kABytes + b_bytes;
             const int c = t.channel + rank * 128, row = static_cast<int>(t.row) + (kOp == kWgrad ? 0 : b_first);
+            const uint32_t mine = a_bytes<kOp>(g.C - c), both = a_bytes<kOp>(g.C - t.channel) +
+                                                               a_bytes<kOp>(g.C - t.channel - 128) + 2 * b_bytes;
             for (int k = 0; k < t.k; k += kBlockK) {
                 ok = __all_sync(kFullMask, mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop));
                 if (!ok) break;
@@ -632,23 +696,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool tail = kOp == kWgrad && has_tail(t.k - k);
                 // a tail's bytes each CTA counts itself, since it clears them; others CTA 0 counts for both
                 const uint32_t bar = tail ? smem_addr(&s.part[stage]) : peer_addr(&s.full[stage], 0);
-                if (leader) {
+                if (leader && lanes) {
                     if (tail)
-                        mbar_arrive_expect_tx(&s.part[stage], bytes);
+                        mbar_arrive_expect_tx(&s.part[stage], mine + b_bytes);
                     else if (rank == 0)
-                        mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
+                        mbar_arrive_expect_tx(&s.full[stage], both);
                     if constexpr (kOp == kGateUp) {
-                        tma_load_pair_3d(to, a_map, k, c, 2 * t.e, bar);
-                        tma_load_pair_3d(to + 128 * kBlockK * 2, a_map, k, c, 2 * t.e + 1, bar);
+                        if (mine > 0) {
+                            tma_load_pair_3d(to, a_map, k, c, 2 * t.e, bar);
+                            tma_load_pair_3d(to + 128 * kBlockK * 2, a_map, k, c, 2 * t.e + 1, bar);
+                        }
                     } else if constexpr (kOp == kDown) {
-                        tma_load_pair_3d(to, a_map, k, c, t.e, bar);
+                        if (mine > 0) tma_load_pair_3d(to, a_map, k, c, t.e, bar);
                     } else if constexpr (kOp == kWgrad) {
-                        tma_load_pair_2d(to, a_map, c, row + k, bar);
-                        tma_load_pair_2d(to + kCrossBlock, a_map, c + 64, row + k, bar);
+                        if (mine > 0) tma_load_pair_2d(to, a_map, c, row + k, bar);
+                        if (mine > kCrossBlock) tma_load_pair_2d(to + kCrossBlock, a_map, c + 64, row + k, bar);
                     } else {
-                        tma_load_pair_3d(to, a_map, c, k, t.e, bar);
-                        tma_load_pair_3d(to + kCrossBlock, a_map, c + 64, k, t.e, bar);
+                        if (mine > 0) tma_load_pair_3d(to, a_map, c, k, t.e, bar);
+                        if (mine > kCrossBlock) tma_load_pair_3d(to + kCrossBlock, a_map, c + 64, k, t.e, bar);
                     }
+                } else if (leader) {
                     if constexpr (kOp == kWgrad) {
                         tma_load_pair_2d(b_to, b64_map, t.column + b_first, row + k, bar);
                         if (half > 64)
@@ -765,12 +832,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 part ^= 1u << stage;
                 unsigned char* const at = s_stages + static_cast<size_t>(stage) * Tr::kStageBytes;
-                const int lines = 16 - left % 16, b_blocks = (t.n / 2 + 63) / 64;
-                for (int n = lane; n < (2 + b_blocks) * lines * 8; n += 32) {
-                    const int block = n / (lines * 8), line = left + n / 8 % lines;
-                    *reinterpret_cast<uint4*>(at + block * kCrossBlock + line * 128 + n % 8 * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
+                const int end = (left + 15) / 16 * 16, blocks_here = 2 + (t.n / 2 + 63) / 64;
+                for (int block = 0; block < blocks_here; ++block)
+                    for (int line = left + lane / 8; line < end; line += 4)
+                        *reinterpret_cast<uint4*>(at + block * kCrossBlock + line * 128 + lane % 8 * 16) =
+                            make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(peer_addr(&s.ready[stage], 0));
@@ -778,15 +844,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok || !tiles.ok) s.stop = 1;
         }
     } else {
-        const int half = (warp - kFinish) / 4;
+        const int group = (warp - kFinish) / 4;
         uint32_t slot = 0;
         // A pass without rows while the first sums are made: it brings the code in, which takes
-        // longer than a small tile itself (16 experts of 1024 x 512, 127 tokens: 2 us of 13).
+        // longer than a small tile itself.
         t = {0, 0, 0, 64, 0, 0, 0};
         finish_tile<kOp>(g, b16_map, s, t, tmem, tmem, rank, warp, lane, [] { return true; });
         while (true) {
             const bool more = tiles.next(s, &t);
-            if (!half_agrees(tiles.ok, half)) {
+            if (!group_agrees(tiles.ok, group)) {
                 s.stop = 1;
                 break;
             }
@@ -798,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (uint32_t i = 0; ok && i < slots; ++i)
                     ok = mbar_wait(&s.sums_full[(first + i) % 2], (first + i) / 2 % 2, &s.stop);
-                ok = half_agrees(ok, half);
+                ok = group_agrees(ok, group);
                 tc_fence_after();
                 return ok;
             };
@@ -821,7 +887,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     cluster_sync_relaxed();  // neither CTA's shared or tensor memory is used by the other any more
-    if (warp == kTail) {
+    if (warp == kLastFinish) {
         tc_fence_after();
         tmem_free_pair(tmem, kTmemColumns);
     }
@@ -840,26 +906,25 @@ ep_status_t zero_fill(void* p, size_t bytes, void* stream) {
 }
 
 // A map of bf16 `dims` (innermost first, dense), in boxes of 64 values by `lines`, swizzled for the
-// tensor cores (or of 32, as patches are).
-ep_status_t map_of(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t lines,
-                   uint32_t values = 64) {
+// tensor cores.
+ep_status_t map_of(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t lines) {
     const uint64_t dims[3] = {d0, d1, d2}, strides[2] = {d0 * 2, d0 * d1 * 2};
-    const uint32_t box[3] = {values, lines, 1};
+    const uint32_t box[3] = {64, lines, 1};
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d2 == 0 ? 2 : 3, base, dims, strides, box,
-                             values == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                             CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int kOp>
 ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, const CUtensorMap& b16, void* stream) {
     using Tr = Traits<kOp>;
     static std::atomic<int> ready[kMaxDevices];
-    const size_t behind = sizeof(Shared) + (kOp == kWgrad ? 0 : sizeof(int) * static_cast<size_t>(g.E));
+    const size_t behind = sizeof(Shared<kOp>) + (kOp == kWgrad ? 0 : sizeof(int) * static_cast<size_t>(g.E));
     g.stages = static_cast<int>((kSmemMost - behind) / Tr::kStageBytes);
     if (g.stages > kMostStages) g.stages = kMostStages;
     const ep_status_t st = ensure_dynamic_smem(ready, expert_kernel<kOp>, static_cast<int>(kSmemMost));
     if (st != EP_OK) return st;
     const dim3 grid(static_cast<unsigned>(sm_count() / 2 * 2));
-    return launch_dependent(expert_kernel<kOp>, grid, dim3(kThreads), g.stages * Tr::kStageBytes + behind,
+    return launch_dependent(expert_kernel<kOp>, grid, dim3(Tr::kThreads), g.stages * Tr::kStageBytes + behind,
                             as_stream(stream), a, b64, b16, g);
 }
 
@@ -1003,7 +1068,7 @@ ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* e
     CUtensorMap a, b, out;
     ep_status_t st = map_of(&a, rows, J, n, 0, 64);
     if (st == EP_OK) st = map_of(&b, dout, I, n, 0, 64);
-    if (st == EP_OK) st = map_of(&out, dw, J, I, E, 16, 32);
+    if (st == EP_OK) st = map_of(&out, dw, J, I, E, 16);
     return st != EP_OK ? st : launch<kWgrad>(g, a, b, out, stream);
 }
 

@@ -25,8 +25,8 @@ __device__ __forceinline__ ExpertRows expert_rows(const int32_t* offsets, int e,
 
 // act(v) = v * s, s = sigmoid(p(v)); both activations are of this form, so that their
 // derivative is s + v * s * (1 - s) * p'(v). The exponential and the reciprocal are the fast
-// ones (a few 2^-22 relative): what comes out is rounded to bf16, 2^-9. exp overflows to
-// infinity where p < -88, whose reciprocal is 0: the right limit.
+// ones (a few 2^-22 relative): what comes out is rounded to bf16. exp overflows to infinity where
+// p < -88, whose reciprocal is 0: the right limit.
 struct Gate {
     float s, slope;  // sigmoid(p(v)), p'(v)
 };
@@ -40,7 +40,9 @@ __device__ __forceinline__ Gate gate_of(float v) {
         p = kA * (v + kB * v * v2);
         slope = kA * (1.0f + 3.0f * kB * v2);
     }
-    return {__fdividef(1.0f, 1.0f + __expf(-p)), slope};
+    float s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-p)));
+    return {s, slope};
 }
 
 // bf16_rn(amax / 448), 0 below 2^-100 (so that its reciprocal is finite)

@@ -151,39 +151,38 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
         : "memory");
 }
 
-// ---------------------------------------------------------------------------- 32 x 32 sums a warp
-// A warp's 32 lanes of tensor memory by 32 columns, as the fragments of 8 x 8 matrices that
-// stmatrix and ldmatrix move: v[16 h + 4 q + i] is lane 16 h + 8 (i / 2) + t / 4, column
-// 8 q + 2 (t % 4) + i % 2, for thread t of the warp.
+// ---------------------------------------------------------------------------- 32 x 16 sums a warp
+// A warp's 32 lanes of tensor memory by 16 columns, as the fragments of 8 x 8 matrices that
+// stmatrix and ldmatrix move: v[8 h + 4 q + i] is lane 16 h + 8 (i / 2) + t / 4, column
+// 8 q + 2 (t % 4) + i % 2, for thread t of the warp; or packed, w[4 q + b] holds two columns,
+// 8 q + 2 (t % 4) and the next, of lane 8 b + t / 4.
+constexpr int kChunk = 16;
+
+__device__ __forceinline__ constexpr int fragment(int q, int b) { return 8 * (b / 2) + 4 * q + 2 * (b % 2); }
 
 __device__ __forceinline__ void tmem_load_half(float* v, uint32_t at) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(at));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(at));
 }
-__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at) {
+__device__ __forceinline__ void tmem_load(float (&v)[16], uint32_t at) {
     tmem_load_half(v, at);
-    tmem_load_half(v + 16, at + (16u << 16));
+    tmem_load_half(v + 8, at + (16u << 16));
 }
 // until the loads are done; the values are used only after it
-__device__ __forceinline__ void tmem_load_wait(float (&v)[32]) {
+__device__ __forceinline__ void tmem_load_wait(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
-                   "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
-                   "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
-                   "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15])
                  :
                  : "memory");
 }
 
-// Between fragments and rows: a warp's patch of shared memory, 32 rows (columns of the sums) of
+// Between fragments and rows: a warp's patch of shared memory, 16 rows (columns of the sums) of
 // 32 channels (lanes) of 16 bits, 64 bytes each. A row's four 16-byte vectors change places with
 // the row, so that both the eight rows of a matrix and two whole rows fall on all banks.
-constexpr uint32_t kPatchBytes = 32 * 64;
+constexpr uint32_t kPatchBytes = kChunk * 64;
 
 __device__ __forceinline__ uint32_t patch_vector(uint32_t patch, int row, int vector) {
     return patch + row * 64 + ((vector ^ (row / 2 % 4)) * 16);
@@ -196,19 +195,23 @@ __device__ __forceinline__ uint32_t matrix_place(uint32_t patch, int q, int lane
 __device__ __forceinline__ uint32_t row_place(uint32_t patch, int q, int lane) {
     return patch_vector(patch, lane / 4, lane % 4) + q * 512;
 }
-// w[4 q + b]: two columns (8 q + 2 (t % 4) and the next) of lane 8 b + t / 4; from row 8 kFrom to 8 kTo
-template <int kFrom = 0, int kTo = 4>
-__device__ __forceinline__ void patch_put(uint32_t patch, const uint32_t (&w)[16], int lane) {
-#pragma unroll
-    for (int q = kFrom; q < kTo; ++q)
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                         matrix_place(patch, q, lane)),
-                     "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
-                     : "memory");
+// The same for a patch that two warps share, 16 rows of 64 channels, 128 bytes each, in the places
+// of the 128-byte swizzle; `side`: which 32 channels.
+__device__ __forceinline__ uint32_t wide_matrix_place(uint32_t patch, int q, int side, int lane) {
+    return patch + (8 * q + lane % 8) * 128 + (((4 * side + lane / 8) ^ (lane % 8)) * 16);
 }
-__device__ __forceinline__ void patch_get(uint32_t (&w)[16], uint32_t patch, int lane) {
+__device__ __forceinline__ void matrices_put(uint32_t at, const uint32_t (&w)[8], int q) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[4 * q]),
+                 "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                 : "memory");
+}
+__device__ __forceinline__ void patch_put(uint32_t patch, const uint32_t (&w)[8], int lane) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q) matrices_put(matrix_place(patch, q, lane), w, q);
+}
+__device__ __forceinline__ void patch_get(uint32_t (&w)[8], uint32_t patch, int lane) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[4 * q]), "=r"(w[4 * q + 1]), "=r"(w[4 * q + 2]), "=r"(w[4 * q + 3])
                      : "r"(matrix_place(patch, q, lane))
