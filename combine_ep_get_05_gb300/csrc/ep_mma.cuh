@@ -40,12 +40,13 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
+// Arrivals at a barrier of either CTA (a cluster address). Neither is a release to the cluster, which
+// waits until the SM's stores have reached L2, some 2000 cycles: the first orders the CTA's accesses,
+// for shared memory that fence_proxy_async_smem has handed to the tensor cores; the second none, for
+// tensor memory, which tcgen05's own fences order.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-
-// The same without order for the thread's memory accesses, for what tcgen05's own fences order: a
-// release to the cluster waits until the thread's stores have reached L2, some 2000 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
