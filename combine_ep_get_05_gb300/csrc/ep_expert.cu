@@ -49,6 +49,8 @@ struct ExpertArgs {
     int C;  // output channels, along the lanes (one half of them in kGateUp and kDownBwd)
     int K;  // products of a sum (kWgrad: output rows, along the columns)
     int E, R, max_rows;
+    int epr;        // experts a rank
+    float inv_epr;  // 1 / epr
     int stages;
     const uint16_t* pre;
     const uint8_t* pre_q;
@@ -116,17 +118,23 @@ __device__ __forceinline__ int rows_each(int count, int tiles) { return ((count 
 // eight: the rows that are at work at a time, and the weights that they share, stay in L2.
 __device__ __forceinline__ void tile_of(const ExpertArgs& g, int choice, int e, const ExpertRows& r, uint32_t l,
                                         Tile* tile) {
-    const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
-    const int tiles = row_tiles(r.count, choice), each = rows_each(r.count, tiles);
-    const uint32_t group = l / (8 * across);
-    l -= group * 8 * across;
-    const uint32_t left = tiles - group * 8, width = left < 8 ? left : 8;
-    const int i = static_cast<int>(group * 8 + l % width);
+    const int tiles = row_tiles(r.count, choice);
+    tile->row = r.first;
+    tile->rows = r.count;
+    tile->channel = static_cast<int>(l * 256);
+    if (tiles > 1) {
+        const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
+        const int each = rows_each(r.count, tiles);
+        const uint32_t group = l / (8 * across);
+        l -= group * 8 * across;
+        const uint32_t left = tiles - group * 8, width = left < 8 ? left : 8;
+        const int i = static_cast<int>(group * 8 + l % width);
+        tile->row += static_cast<long long>(i) * each;
+        tile->rows = r.count - i * each < each ? r.count - i * each : each;
+        tile->channel = static_cast<int>(l / width * 256);
+    }
     tile->e = e;
-    tile->row = r.first + static_cast<long long>(i) * each;
-    tile->rows = r.count - i * each < each ? r.count - i * each : each;
     tile->n = (tile->rows + 31) / 32 * 32;
-    tile->channel = static_cast<int>(l / width * 256);
     tile->column = 0;
     tile->k = g.K;
 }
@@ -140,7 +148,7 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared<kOp>& 
         if (t >= static_cast<uint32_t>(g.E) * across * down) return false;
         const int e = static_cast<int>(t / (across * down));
         const uint32_t l = t - e * (across * down);
-        const ExpertRows r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        const ExpertRows r = expert_rows(g.offsets, e, g.epr, g.inv_epr, g.max_rows);
         tile->e = e;
         tile->row = r.first;
         tile->k = r.count;
@@ -159,7 +167,7 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared<kOp>& 
         else
             hi = mid;
     }
-    tile_of(g, s.choice, lo, expert_rows(g.offsets, lo, g.E / g.R, g.max_rows), t - s.prefix[lo] * across, tile);
+    tile_of(g, s.choice, lo, expert_rows(g.offsets, lo, g.epr, g.inv_epr, g.max_rows), t - s.prefix[lo] * across, tile);
     return true;
 }
 
@@ -176,7 +184,7 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
     ExpertRows r = {0, 0, false};
     int sum[4] = {0, 0, 0, 0};
     for (int e = first; e < last; ++e) {
-        r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        r = expert_rows(g.offsets, e, g.epr, g.inv_epr, g.max_rows);
         if (r.dropped && blockIdx.x == 0) raise_flag(g.status, EP_FLAG_CAPACITY);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] += row_tiles(r.count, i);
@@ -208,7 +216,7 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
     }
     before += upto - mine;
     for (int e = first; e < last; ++e) {
-        if (per > 1) r = expert_rows(g.offsets, e, g.E / g.R, g.max_rows);
+        if (per > 1) r = expert_rows(g.offsets, e, g.epr, g.inv_epr, g.max_rows);
         const uint32_t begin = static_cast<uint32_t>(before) * across;
         s.prefix[e] = before;
         before += row_tiles(r.count, choice);
@@ -636,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         }
         if (blockIdx.x == 0)
             for (int e = tid; e < g.E; e += Tr::kThreads)
-                if (expert_rows(g.offsets, e, g.E / g.R, g.max_rows).dropped) raise_flag(g.status, EP_FLAG_CAPACITY);
+                if (expert_rows(g.offsets, e, g.epr, g.inv_epr, g.max_rows).dropped) raise_flag(g.status, EP_FLAG_CAPACITY);
     } else {
         plan_tiles<kOp>(g, s, pair, pairs);
     }
@@ -918,6 +926,8 @@ template <int kOp>
 ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, const CUtensorMap& b16, void* stream) {
     using Tr = Traits<kOp>;
     static std::atomic<int> ready[kMaxDevices];
+    g.epr = g.E / g.R;
+    g.inv_epr = 1.0f / static_cast<float>(g.epr);
     const size_t behind = sizeof(Shared<kOp>) + (kOp == kWgrad ? 0 : sizeof(int) * static_cast<size_t>(g.E));
     g.stages = static_cast<int>((kSmemMost - behind) / Tr::kStageBytes);
     if (g.stages > kMostStages) g.stages = kMostStages;

@@ -13,9 +13,12 @@ struct ExpertRows {
     bool dropped;  // some lay past the slab's end
 };
 
-// Rows of expert e, whatever the offsets hold: never outside slab e / epr.
-__device__ __forceinline__ ExpertRows expert_rows(const int32_t* offsets, int e, int epr, int max_rows) {
-    const int r = e / epr;
+// Rows of expert e, whatever the offsets hold: never outside slab e / epr. The quotient is exact by
+// way of inv_epr = 1.0f / epr: (e + 0.5) / epr, at most 8192 / epr, is 0.5 / epr away from an integer
+// and the product no more than 2^-22 of it off.
+__device__ __forceinline__ ExpertRows expert_rows(const int32_t* offsets, int e, int epr, float inv_epr,
+                                                  int max_rows) {
+    const int r = static_cast<int>((static_cast<float>(e) + 0.5f) * inv_epr);
     const long long base = offsets[r * epr];
     const long long a = offsets[e] - base, b = offsets[e + 1] - base;
     const long long lo = a < 0 ? 0 : (a > max_rows ? max_rows : a);
