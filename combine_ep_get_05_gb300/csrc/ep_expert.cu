@@ -938,6 +938,13 @@ ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, c
                             as_stream(stream), a, b64, b16, g);
 }
 
+// Slabs so small that experts can have few rows only are taken by the kernel for them.
+bool few_rows(const ExpertArgs& g) { return static_cast<long long>(g.R) * g.max_rows <= 2ll * g.E || g.R * g.max_rows <= 8; }
+FewRows few(const ExpertArgs& g, const void* x, const void* w) {
+    return {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), g.offsets, g.act, g.C, g.K, g.E,
+            g.max_rows, g.E / g.R, 1.0f / static_cast<float>(g.E / g.R), g.out, g.status};
+}
+
 // Rows of the slabs as the operand along the columns: in boxes of 64 rows and of 16.
 ep_status_t row_maps(CUtensorMap* b64, CUtensorMap* b16, const void* rows, uint64_t width, const ExpertArgs& g) {
     const uint64_t n = static_cast<uint64_t>(g.R) * g.max_rows;
@@ -973,6 +980,7 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
     g.out_q = pre_q;
     g.out_scales = static_cast<uint16_t*>(pre_scales);
     g.status = status;
+    if (pre == nullptr && pre_q == nullptr && few_rows(g)) return launch_few_rows(few(g, x, w_gate_up), true, stream);
     CUtensorMap a, b64, b16;
     ep_status_t st = map_of(&a, w_gate_up, H, F, 2ull * E, 128);
     if (st == EP_OK) st = row_maps(&b64, &b16, x, H, g);
@@ -994,6 +1002,7 @@ ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* exp
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(y);
     g.status = status;
+    if (few_rows(g)) return launch_few_rows(few(g, h, w_down), false, stream);
     CUtensorMap a, b64, b16;
     ep_status_t st = map_of(&a, w_down, F, H, E, 128);
     if (st == EP_OK) st = row_maps(&b64, &b16, h, F, g);

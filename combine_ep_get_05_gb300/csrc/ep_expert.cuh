@@ -6,6 +6,17 @@
 
 namespace ep {
 
+// The products x W^T (or act(x Wg^T) * (x Wu^T)) of calls with few rows (ep_expert_few.cu).
+struct FewRows {
+    const uint16_t *x, *w;
+    const int32_t* offsets;
+    int act, C, K, E, max_rows, epr;
+    float inv_epr;  // 1 / epr
+    uint16_t* out;
+    int32_t* status;
+};
+ep_status_t launch_few_rows(const FewRows& g, bool gated, void* stream);
+
 // The rows [first, first + count) of an expert in the slabs seen as one array of rows.
 struct ExpertRows {
     long long first;
