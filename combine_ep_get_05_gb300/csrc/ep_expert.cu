@@ -938,8 +938,6 @@ ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, c
                             as_stream(stream), a, b64, b16, g);
 }
 
-// Slabs so small that experts can have few rows only are taken by the kernel for them.
-bool few_rows(const ExpertArgs& g) { return static_cast<long long>(g.R) * g.max_rows <= 2ll * g.E || g.R * g.max_rows <= 8; }
 FewRows few(const ExpertArgs& g, const void* x, const void* w) {
     return {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), g.offsets, g.act, g.C, g.K, g.E,
             g.max_rows, g.E / g.R, 1.0f / static_cast<float>(g.E / g.R), g.out, g.status};
@@ -980,7 +978,8 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
     g.out_q = pre_q;
     g.out_scales = static_cast<uint16_t*>(pre_scales);
     g.status = status;
-    if (pre == nullptr && pre_q == nullptr && few_rows(g)) return launch_few_rows(few(g, x, w_gate_up), true, stream);
+    const int few_at_once = pre == nullptr && pre_q == nullptr ? few_rows_at_once(E, R, max_rows, true) : 0;
+    if (few_at_once > 0) return launch_few_rows(few(g, x, w_gate_up), true, few_at_once, stream);
     CUtensorMap a, b64, b16;
     ep_status_t st = map_of(&a, w_gate_up, H, F, 2ull * E, 128);
     if (st == EP_OK) st = row_maps(&b64, &b16, x, H, g);
@@ -1002,7 +1001,8 @@ ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* exp
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(y);
     g.status = status;
-    if (few_rows(g)) return launch_few_rows(few(g, h, w_down), false, stream);
+    const int few_at_once = few_rows_at_once(E, R, max_rows, false);
+    if (few_at_once > 0) return launch_few_rows(few(g, h, w_down), false, few_at_once, stream);
     CUtensorMap a, b64, b16;
     ep_status_t st = map_of(&a, w_down, F, H, E, 128);
     if (st == EP_OK) st = row_maps(&b64, &b16, h, F, g);

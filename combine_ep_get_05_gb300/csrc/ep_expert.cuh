@@ -15,7 +15,18 @@ struct FewRows {
     uint16_t* out;
     int32_t* status;
 };
-ep_status_t launch_few_rows(const FewRows& g, bool gated, void* stream);
+ep_status_t launch_few_rows(const FewRows& g, bool gated, int at_once, void* stream);
+
+// Rows of an expert that the kernel for few rows takes at once (8 or 16), 0 where the general one is
+// the faster, by what the slabs can hold: an expert's rows are known to the GPU only. us of the
+// gated product, few against general: 256 experts of 7168 x 2048, slabs of 1 row an expert 71.8
+// against 76.5, 4 rows 259 against 284, 8 rows (16 at once) 491 against 505, and 2175 against 2126
+// where they are half filled; 16 experts of 1024 x 512, 1 row 2.9 against 8.7; one expert of
+// 7168 x 2048 with 8 rows 12.2 against 40, 16 rows 13.4, 32 rows 22.6, 64 rows 41. The product that
+// is not gated: 7.9, 9.6, 15.5 and 27.9 against 12.4 for that one expert with 8 to 64 rows; 64 experts
+// of 2048 x 1024, slabs of 4 rows an expert, 29.5 against 32.7. Slabs of more than 64 rows stay
+// with the general kernel whatever E: all rows may be one expert's.
+int few_rows_at_once(int E, int R, int max_rows, bool gated);
 
 // The rows [first, first + count) of an expert in the slabs seen as one array of rows.
 struct ExpertRows {

@@ -3,8 +3,8 @@
 // GPU with it.
 //
 // A unit of work is 32 output channels of an expert (in the gated product, 16 and their gate and
-// up) by eight of its rows: m16n8k16 products with the weights as A. A warp takes every
-// eighth 64 k of a unit; a thread loads 16 bytes of four weight rows and of one row of x, 64 bytes a
+// up) by eight or sixteen of its rows: m16n8k16 products with the weights as A. A warp takes every
+// eighth 64 k of a unit; a thread loads 16 bytes of four weight rows and of one or two rows of x, 64 bytes a
 // row over four lanes, and uses them as fragments as they are: the products of a sum may be taken
 // in any order of k as long as A's and B's is the same. The sums of the eight warps are added in
 // shared memory, in order.
@@ -19,24 +19,26 @@ namespace {
 using namespace ep;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kChannels = 16, kRows = 8, kStep = 64;
+constexpr int kChannels = 16, kStep = 64;
 
 // One warp's 64 k of a unit, in two parts of 32: weight rows g and g + 8 of its two halves of 16
-// (gate and up, or the first and the last) and row g of x; g = lane / 4, k = 8 (lane % 4) and the
-// next 7 of each part.
+// (gate and up, or the first and the last) and row g of each eight of x; g = lane / 4, k =
+// 8 (lane % 4) and the next 7 of each part.
 constexpr int kHalves = 2;
-constexpr int kVectors = 2 * (2 * kHalves + 1);  // 16 bytes each, of a thread and step
-template <bool kGated>
+
+template <bool kGated, int kGroups>
 struct Ring {
     static constexpr int kSlice = kGated ? kChannels : kHalves * kChannels;  // channels of a unit
-    static constexpr int kStages = kGated ? 5 : 4;
+    static constexpr int kRows = 8 * kGroups;
+    static constexpr int kVectors = 2 * (2 * kHalves + kGroups);  // 16 bytes each, of a thread and step
+    static constexpr int kStages = kGated && kGroups == 1 ? 5 : 4;
     static constexpr int kBytes = kStages * kVectors * kThreads * 16;
+    // sums by turns, where there is room: the next need not wait for these to be read
+    static constexpr int kTurns = !kGated && kGroups == 1 ? 2 : 1;
 };
-template <bool kGated>
+template <typename Ring>
 struct Sums {
-    // by turns, where there is room: the next sums need not wait for these to be read
-    static constexpr int kTurns = kGated ? 1 : 2;
-    float v[kTurns][kWarps][kHalves][kChannels][kRows + 1];
+    float v[Ring::kTurns][kWarps][kHalves][kChannels][Ring::kRows + 1];
     int found[kWarps];
 };
 
@@ -49,7 +51,7 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Where a CTA is: a slice of an expert's channels, eight of its rows, and the warp's 64 k.
+// Where a CTA is: a slice of an expert's channels, some of its rows, and the warp's 64 k.
 struct Place {
     int expert, slice;  // the how manieth of those that have rows; of its slices
     int row0, step;
@@ -71,11 +73,12 @@ __device__ __forceinline__ void copy_or_zero(uint32_t to, const void* from, bool
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
-template <bool kGated>
+template <bool kGated, int kGroups>
 __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
-    using Tr = Ring<kGated>;
+    using Tr = Ring<kGated, kGroups>;
+    constexpr int kRows = Tr::kRows, kVectors = Tr::kVectors;
     extern __shared__ __align__(16) unsigned char s_ring[];
-    Sums<kGated>& s = *reinterpret_cast<Sums<kGated>*>(s_ring + Tr::kBytes);
+    Sums<Tr>& s = *reinterpret_cast<Sums<Tr>*>(s_ring + Tr::kBytes);
     uint16_t* const s_expert = reinterpret_cast<uint16_t*>(&s + 1);  // [E] those that have rows
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     allow_dependents();
@@ -144,9 +147,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
                         copy_or_zero(to, there ? p.w + line * K + k : p.w, there);
                         to += kThreads * 16;
                     }
-                const bool there = k < K && p.row0 + row < p.count;
-                copy_or_zero(to, there ? g.x + static_cast<size_t>(p.first + p.row0 + row) * K + k : g.x, there);
-                to += kThreads * 16;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const int n = p.row0 + 8 * j + row;
+                    const bool there = k < K && n < p.count;
+                    copy_or_zero(to, there ? g.x + static_cast<size_t>(p.first + n) * K + k : g.x, there);
+                    to += kThreads * 16;
+                }
             }
         }
         cp_async_commit();  // an empty group past the end
@@ -162,20 +169,25 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
         load(front, i);
         if (front.expert < experts) advance(front);
     }
-    float sum[kHalves][4] = {};
+    float sum[kHalves][kGroups][4] = {};
     int stage = 0, turn = 0;
     while (here.expert < experts) {
         cp_async_wait<Tr::kStages - 2>();
         const uint32_t from = mine + stage * (kVectors * kThreads * 16);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t at = from + i * (2 * kHalves + 1) * kThreads * 16;
-            const uint4 x = lds_v4(at + 2 * kHalves * kThreads * 16);
+            const uint32_t at = from + i * (2 * kHalves + kGroups) * kThreads * 16;
+            uint4 x[kGroups];
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) x[j] = lds_v4(at + (2 * kHalves + j) * kThreads * 16);
 #pragma unroll
             for (int half = 0; half < kHalves; ++half) {
                 const uint4 a = lds_v4(at + 2 * half * kThreads * 16), b = lds_v4(at + (2 * half + 1) * kThreads * 16);
-                mma(sum[half], a.x, b.x, a.y, b.y, x.x, x.y);
-                mma(sum[half], a.z, b.z, a.w, b.w, x.z, x.w);
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    mma(sum[half][j], a.x, b.x, a.y, b.y, x[j].x, x[j].y);
+                    mma(sum[half][j], a.z, b.z, a.w, b.w, x[j].z, x[j].w);
+                }
             }
         }
         // the stage before this one, read a step ago, is filled again
@@ -183,17 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
         if (front.expert < experts) advance(front);
         if (here.step == steps - 1) {
 #pragma unroll
-            for (int half = 0; half < kHalves; ++half) {
-                float(*const to)[kRows + 1] = s.v[turn][warp][half];
-                to[row][lane % 4 * 2] = sum[half][0];
-                to[row][lane % 4 * 2 + 1] = sum[half][1];
-                to[row + 8][lane % 4 * 2] = sum[half][2];
-                to[row + 8][lane % 4 * 2 + 1] = sum[half][3];
-                sum[half][0] = sum[half][1] = sum[half][2] = sum[half][3] = 0.0f;
-            }
+            for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    float(*const to)[kRows + 1] = s.v[turn][warp][half];
+                    float(&v)[4] = sum[half][j];
+                    const int n = 8 * j + lane % 4 * 2;
+                    to[row][n] = v[0];
+                    to[row][n + 1] = v[1];
+                    to[row + 8][n] = v[2];
+                    to[row + 8][n + 1] = v[3];
+                    v[0] = v[1] = v[2] = v[3] = 0.0f;
+                }
             __syncthreads();
-            const int r = tid / Tr::kSlice, c = tid % Tr::kSlice, channel = here.slice * Tr::kSlice + c;
-            if (r < kRows && here.row0 + r < here.count && channel < C) {
+            const int c = tid % Tr::kSlice, channel = here.slice * Tr::kSlice + c;
+            for (int r = tid / Tr::kSlice; r < kRows && here.row0 + r < here.count; r += kThreads / Tr::kSlice) {
+                if (channel >= C) break;
                 float v = 0.0f, up = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
@@ -204,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
                 g.out[static_cast<size_t>(here.first + here.row0 + r) * C + channel] =
                     static_cast<uint16_t>(pack_bf16x2_rn(v, 0.0f));
             }
-            if (Sums<kGated>::kTurns == 1)
+            if (Tr::kTurns == 1)
                 __syncthreads();
             else
                 turn ^= 1;
@@ -214,24 +231,32 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
     }
 }
 
-template <bool kGated>
+template <bool kGated, int kGroups>
 ep_status_t launch(const FewRows& g, void* stream) {
+    using Tr = Ring<kGated, kGroups>;
     static std::atomic<int> ready[kMaxDevices];
-    constexpr size_t most = Ring<kGated>::kBytes + sizeof(Sums<kGated>) + 2 * 8192;
+    constexpr size_t fixed = Tr::kBytes + sizeof(Sums<Tr>), most = fixed + 2 * 8192;
     static_assert(most <= 227 * 1024);
-    const ep_status_t st = ensure_dynamic_smem(ready, few_rows_kernel<kGated>, static_cast<int>(most));
+    const ep_status_t st = ensure_dynamic_smem(ready, few_rows_kernel<kGated, kGroups>, static_cast<int>(most));
     if (st != EP_OK) return st;
-    return launch_dependent(few_rows_kernel<kGated>, dim3(static_cast<unsigned>(sm_count())), dim3(kThreads),
-                            Ring<kGated>::kBytes + sizeof(Sums<kGated>) + 2 * static_cast<size_t>(g.E),
-                            as_stream(stream), g);
+    return launch_dependent(few_rows_kernel<kGated, kGroups>, dim3(static_cast<unsigned>(sm_count())), dim3(kThreads),
+                            fixed + 2 * static_cast<size_t>(g.E), as_stream(stream), g);
 }
 
 }  // namespace
 
 namespace ep {
 
-ep_status_t launch_few_rows(const FewRows& g, bool gated, void* stream) {
-    return gated ? launch<true>(g, stream) : launch<false>(g, stream);
+int few_rows_at_once(int E, int R, int max_rows, bool gated) {
+    const long long all = static_cast<long long>(R) * max_rows;
+    if (max_rows <= 8 || (all <= 4ll * E && max_rows <= 64)) return 8;
+    if (max_rows <= 16 || (gated && all <= 6ll * E && max_rows <= 64)) return 16;
+    return 0;
+}
+
+ep_status_t launch_few_rows(const FewRows& g, bool gated, int at_once, void* stream) {
+    if (at_once == 8) return gated ? launch<true, 1>(g, stream) : launch<false, 1>(g, stream);
+    return gated ? launch<true, 2>(g, stream) : launch<false, 2>(g, stream);
 }
 
 }  // namespace ep
