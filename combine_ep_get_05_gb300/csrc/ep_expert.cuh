@@ -17,15 +17,16 @@ struct FewRows {
 };
 ep_status_t launch_few_rows(const FewRows& g, bool gated, int at_once, void* stream);
 
-// Rows of an expert that the kernel for few rows takes at once (8 or 16), 0 where the general one is
-// the faster, by what the slabs can hold: an expert's rows are known to the GPU only. us of the
-// gated product, few against general: 256 experts of 7168 x 2048, slabs of 1 row an expert 71.8
-// against 76.5, 4 rows 259 against 284, 8 rows (16 at once) 491 against 505, and 2175 against 2126
-// where they are half filled; 16 experts of 1024 x 512, 1 row 2.9 against 8.7; one expert of
-// 7168 x 2048 with 8 rows 12.2 against 40, 16 rows 13.4, 32 rows 22.6, 64 rows 41. The product that
-// is not gated: 7.9, 9.6, 15.5 and 27.9 against 12.4 for that one expert with 8 to 64 rows; 64 experts
-// of 2048 x 1024, slabs of 4 rows an expert, 29.5 against 32.7. Slabs of more than 64 rows stay
-// with the general kernel whatever E: all rows may be one expert's.
+// Rows of an expert that the kernel for few rows takes at once (8, 16 or 32), 0 where the general
+// one is the faster, by what the slabs can hold: an expert's rows are known to the GPU only. us, few
+// against general. Slabs of up to 4 rows an expert: 256 experts of 7168 x 2048, one token 71.8
+// against 76.5 (gated) and 36.6 against 41, four tokens 259 against 284 and 127 against 138; 64 of
+// 2048 x 1024, 16 tokens 55.1 against 62.6 and 29.1 against 32.6. Of 5 or 6 and up, gated, 16 at once:
+// 16 of 1024 x 512 with 4 rows each 10.3 against 11.8, 32 of 4096 x 2048 158 against 166, but 256 of
+// 7168 x 2048 in slabs of 8 rows an expert, half filled, 2175 against 2126; not gated 88.6 against
+// 85.5. One expert of 7168 x 2048: 8 rows 12.2 against 40 and 8.2 against 12.3, 16 rows 13.4 and 9.5,
+// 32 rows, 32 at once, 16.8 and 12.7, 64 rows 30.4 and 22, 96 rows 44 and 31. Slabs of more than 64
+// rows stay with the general kernel whatever E: all of them may be one expert's.
 int few_rows_at_once(int E, int R, int max_rows, bool gated);
 
 // The rows [first, first + count) of an expert in the slabs seen as one array of rows.

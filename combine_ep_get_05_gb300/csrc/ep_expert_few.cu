@@ -3,8 +3,8 @@
 // GPU with it.
 //
 // A unit of work is 32 output channels of an expert (in the gated product, 16 and their gate and
-// up) by eight or sixteen of its rows: m16n8k16 products with the weights as A. A warp takes every
-// eighth 64 k of a unit; a thread loads 16 bytes of four weight rows and of one or two rows of x, 64 bytes a
+// up) by 8, 16 or 32 of its rows: m16n8k16 products with the weights as A. A warp takes every
+// eighth 64 k of a unit; a thread loads 16 bytes of four weight rows and of one to four rows of x, 64 bytes a
 // row over four lanes, and uses them as fragments as they are: the products of a sum may be taken
 // in any order of k as long as A's and B's is the same. The sums of the eight warps are added in
 // shared memory, in order.
@@ -31,7 +31,7 @@ struct Ring {
     static constexpr int kSlice = kGated ? kChannels : kHalves * kChannels;  // channels of a unit
     static constexpr int kRows = 8 * kGroups;
     static constexpr int kVectors = 2 * (2 * kHalves + kGroups);  // 16 bytes each, of a thread and step
-    static constexpr int kStages = kGated && kGroups == 1 ? 5 : 4;
+    static constexpr int kStages = kGroups == 4 ? 3 : kGated && kGroups == 1 ? 5 : 4;
     static constexpr int kBytes = kStages * kVectors * kThreads * 16;
     // sums by turns, where there is room: the next need not wait for these to be read
     static constexpr int kTurns = !kGated && kGroups == 1 ? 2 : 1;
@@ -235,7 +235,7 @@ template <bool kGated, int kGroups>
 ep_status_t launch(const FewRows& g, void* stream) {
     using Tr = Ring<kGated, kGroups>;
     static std::atomic<int> ready[kMaxDevices];
-    constexpr size_t fixed = Tr::kBytes + sizeof(Sums<Tr>), most = fixed + 2 * 8192;
+    constexpr size_t fixed = Tr::kBytes + sizeof(Sums<Tr>), most = fixed + 2 * (kGroups == 4 ? 8 : 8192);  // 32 at once: for one or two experts
     static_assert(most <= 227 * 1024);
     const ep_status_t st = ensure_dynamic_smem(ready, few_rows_kernel<kGated, kGroups>, static_cast<int>(most));
     if (st != EP_OK) return st;
@@ -250,11 +250,13 @@ namespace ep {
 int few_rows_at_once(int E, int R, int max_rows, bool gated) {
     const long long all = static_cast<long long>(R) * max_rows;
     if (max_rows <= 8 || (all <= 4ll * E && max_rows <= 64)) return 8;
+    if (max_rows > 16 && E <= 2 && max_rows <= (gated ? 64 : 32)) return 32;
     if (max_rows <= 16 || (gated && all <= 6ll * E && max_rows <= 64)) return 16;
     return 0;
 }
 
 ep_status_t launch_few_rows(const FewRows& g, bool gated, int at_once, void* stream) {
+    if (at_once == 32) return gated ? launch<true, 4>(g, stream) : launch<false, 4>(g, stream);
     if (at_once == 8) return gated ? launch<true, 1>(g, stream) : launch<false, 1>(g, stream);
     return gated ? launch<true, 2>(g, stream) : launch<false, 2>(g, stream);
 }

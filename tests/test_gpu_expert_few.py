@@ -33,7 +33,10 @@ CASES = [
     ([8], 1, 8, 520, 1000),             # one pass of eight rows
     ([7], 1, 9, 4096, 24),              # sixteen at once, seven there
     ([16], 1, 16, 136, 264),
-    ([17], 1, 17, 136, 264),            # the general kernel
+    ([17], 1, 17, 136, 264),            # 32 at once
+    ([29, 4], 1, 32, 520, 104),         # dropped rows
+    ([50], 1, 64, 264, 48),             # two passes; down: the general kernel
+    ([65], 1, 65, 136, 264),            # the general kernel
     ([3, 0, 12, 1], 1, 16, 2048, 80),
     ([20, 0, 0, 0], 4, 16, 72, 40),     # dropped rows
     ([0, 0, 0, 0, 0, 0, 0, 64], 8, 64, 264, 48),   # general: 512 rows of room
