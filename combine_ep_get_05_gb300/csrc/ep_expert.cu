@@ -445,37 +445,70 @@ __device__ __forceinline__ void load_kept(Kept& kept, const ExpertArgs& g, size_
 __device__ __forceinline__ void pair_sync(int warp) {
     asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + kGroups + (warp - kFinish) / 2) : "memory");
 }
-// 16 rows of two warps' 64 channels as one tensor copy, from one of two patches that are filled in
-// turn: rows and channels past the map's ends are left out. The copies' rows cost alike whatever
-// their length (a tile's sums of 64-byte rows, a patch a warp, took twice as long), and plain
-// 16-byte stores longer still.
-__device__ __forceinline__ void store_patch(const CUtensorMap& map, int x, int y, int z, const uint32_t (&w)[8],
-                                            unsigned char* patch, const Window& win, int warp, int lane) {
-    const int side = warp % 2;
-    const bool sends = side == 0 && lane == 0;
-    if (sends) bulk_wait_read<1>();
-    pair_sync(warp);
+// Two neighbouring warps' 64 channels leave together, 16 rows at a time, as one tensor copy from one
+// of two patches that are filled in turn: rows and channels past the map's ends are left out. (A
+// patch a warp, rows of 64 bytes, took twice as long, and plain 16-byte stores longer still: a copy's
+// rows cost alike whatever their length.) `turn` outlives a tile: a patch is filled again when all
+// copies but the newest, which is the other's, have read theirs.
+struct Outlet {
+    unsigned char* patches;  // two of 16 rows of 128 bytes, the pair's
+    int turn = 0;
+
+    __device__ __forceinline__ unsigned char* patch() const { return patches + turn * 2 * kPatchBytes; }
+    __device__ __forceinline__ void fill(const uint32_t (&w)[8], int warp, int lane) const {
+        pair_sync(warp);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) matrices_put(wide_matrix_place(smem_addr(patch), q, side, lane), w, q);
-    fence_proxy_async_smem();
-    pair_sync(warp);
-    if (sends && win.rows > 0 && win.channels > 0) {
-        tma_store_3d(map, x, y, z, patch);
-        bulk_commit();
+        for (int q = 0; q < 2; ++q)
+            matrices_put(wide_matrix_place(smem_addr(patch()), q, warp % 2, lane), w, q);
+        fence_proxy_async_smem();
+        pair_sync(warp);
     }
-}
+    // one chunk, from row y on
+    __device__ __forceinline__ void send(const CUtensorMap& map, int x, int y, int z, const uint32_t (&w)[8], int warp,
+                                         int lane) {
+        const bool sends = warp % 2 == 0 && lane == 0;
+        if (sends) bulk_wait_read<1>();
+        fill(w, warp, lane);
+        if (sends) {
+            tma_store_3d(map, x, y, z, patch());
+            bulk_commit();
+        }
+        turn ^= 1;
+    }
+    // zeros, from every kGroups-th chunk of the rows y0 .. y0 + rows on, `skip` rows left out
+    __device__ __forceinline__ void send_zeros(const CUtensorMap& map, int x, int y0, int z, int skip, int rows, int warp,
+                                               int lane) {
+        const bool sends = warp % 2 == 0 && lane == 0;
+        if (sends) bulk_wait_read_all();
+        const uint32_t none[8] = {};
+        fill(none, warp, lane);
+        if (sends) {
+            for (int y = skip; y < rows; y += kGroups * kChunk) tma_store_3d(map, x, y0 + y, z, patch());
+            bulk_commit();
+        }
+        turn ^= 1;
+    }
+};
 
 // One warp's part of a tile: 32 channels, every fourth 16 columns. `ready`, called before the sums
 // are read, waits for them; false: give up.
 template <int kOp, typename Ready>
 __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorMap& out_map, Shared<kOp>& s, const Tile& t,
-                                            uint32_t sums, uint32_t ups, int rank, int warp, int lane, Ready ready) {
+                                            uint32_t sums, uint32_t ups, int rank, int warp, int lane, Outlet& outlet, Ready ready) {
     const int group = (warp - kFinish) / 4, quarter = warp % 4;
     const int channel = t.channel + rank * 128 + quarter * 32;  // the warp's first
     const size_t C = static_cast<size_t>(g.C);
     const uint32_t patch = smem_addr(s.patch[warp - kFinish]);
     sums += static_cast<uint32_t>(quarter * 32) << 16;
     ups += static_cast<uint32_t>(quarter * 32) << 16;
+    const int pair_channel = channel & ~63;
+    if constexpr (kOp == kWgrad) {
+        if (t.k == 0) {  // an expert without rows
+            if (pair_channel < g.C && t.rows > group * kChunk)
+                outlet.send_zeros(out_map, pair_channel, t.column, t.e, group * kChunk, t.rows, warp, lane);
+            return true;
+        }
+    }
     Kept kept;
     if constexpr (kOp == kDownBwd)  // on its way while the sums are made
         load_kept(kept, g, static_cast<size_t>(t.row) + group * kChunk, channel, {t.rows - group * kChunk, g.C - channel}, lane);
@@ -559,9 +592,8 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
             if (c0 + kGroups * kChunk < t.n) load_kept(kept, g, row + kGroups * kChunk, channel, {t.rows - c0 - kGroups * kChunk, g.C - channel}, lane);
         } else if constexpr (kOp == kWgrad) {
             pack(w, v);
-            store_patch(out_map, channel, t.column + c0, t.e, w,
-                        s.patch[(warp - kFinish) / 2 * 4 + buffer * 2], win, warp, lane);
-            buffer ^= 1;
+            if (win.rows > 0 && pair_channel < g.C)
+                outlet.send(out_map, pair_channel, t.column + c0, t.e, w, warp, lane);
         } else {
             pack(w, v);
             store_rows(g.out + row * C + channel, C, w, win, patch, lane);
@@ -856,8 +888,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         uint32_t slot = 0;
         // A pass without rows while the first sums are made: it brings the code in, which takes
         // longer than a small tile itself.
+        Outlet outlet = {s.patch[(warp - kFinish) / 2 * 2 * Tr::kPatches]};
         t = {0, 0, 0, 64, 0, 0, 0};
-        finish_tile<kOp>(g, b16_map, s, t, tmem, tmem, rank, warp, lane, [] { return true; });
+        finish_tile<kOp>(g, b16_map, s, t, tmem, tmem, rank, warp, lane, outlet, [] { return true; });
         while (true) {
             const bool more = tiles.next(s, &t);
             if (!group_agrees(tiles.ok, group)) {
@@ -877,7 +910,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 return ok;
             };
             if (!finish_tile<kOp>(g, b16_map, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots),
-                                  rank, warp, lane, ready)) {
+                                  rank, warp, lane, outlet, ready)) {
                 s.stop = 1;
                 break;
             }

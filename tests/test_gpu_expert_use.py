@@ -410,3 +410,24 @@ def test_helpers_on_another_stream():
     check_down_bwd(y, w2, up.pre, rows, "silu", dpre, h)
     check_gate_up_bwd(dpre, w1, rows, dx)
     check_wgrad(dpre, x, rows, dw)
+
+
+@pytest.mark.parametrize("I,J", [(16, 64), (40, 72), (104, 520), (232, 200), (264, 1000)])
+def test_weights_gradient_of_many_small_tiles(I, J):
+    """Tiles that follow one another at once, with every number of chunks a group of warps can have, experts
+    without rows among them: none of the sums that are on their way out is overwritten."""
+    g = torch.Generator().manual_seed(I)
+    counts = torch.randint(-2, 4, (2400,), generator=g).clamp(min=0).tolist()
+    rows = Rows(counts, 8, max(sum(counts[r * 300:(r + 1) * 300]) for r in range(8)))
+    dout, x = normal(1, 8, rows.max_rows, I), normal(2, 8, rows.max_rows, J)
+    dw = torch.full((2400, I, J), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        ep.ep_expert_wgrad(dout, x, rows.offsets, dw)
+    want = torch.zeros((2400, I, J), dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    flat = [(e, r * rows.max_rows + p) for e, (r, a, b) in enumerate(rows.spans) for p in range(a, b)]
+    e, p = torch.tensor(flat, device="cuda").unbind(1)
+    d, v = dout.view(-1, I)[p].double(), x.view(-1, J)[p].double()
+    want.index_add_(0, e, d[:, :, None] * v[:, None, :])
+    size.index_add_(0, e, (d[:, :, None] * v[:, None, :]).abs())
+    assert bool(((dw.double() - want).abs() <= 2.0 ** -8 * want.abs() + 3 * 2.0 ** -23 * size).all())
