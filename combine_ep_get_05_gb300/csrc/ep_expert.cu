@@ -112,13 +112,25 @@ struct Tiles {
 __device__ __forceinline__ int row_tiles(int count, int choice) {
     return static_cast<int>((static_cast<uint32_t>(count) + (kMostN >> choice) - 1) >> (kMostNLog - choice));
 }
+// The choice for one expert. A gated tile of more than 128 rows has all of tensor memory, and its sums
+// are finished before the next one's can begin; two of 128 rows take turns, but read the weights
+// twice (from L2). Short sums cost less than their finish, so they take turns. us with tiles of up to
+// 128 rows, of up to 256 (F = 2048, the 8-bit checkpoint): 16 experts of 2048 rows, H = 512 138, 191,
+// 1024 194, 259, 2048 346, 390; 256 of 128 rows, H = 512 213, 244, 1024 381, 390, 2048 738, 720, 3584
+// 1276, 1226; 128 uneven ones of H = 4096 alike, 256 of 128 rows, H = 7168 2505, 2355.
+template <int kOp>
+__device__ __forceinline__ int choice_of(const ExpertArgs& g, int count, int choice) {
+    const bool turns = g.K <= 1024 || (g.K <= 2048 && count > kMostN);
+    return kOp == kGateUp && choice == 0 && turns ? 1 : choice;
+}
 __device__ __forceinline__ int rows_each(int count, int tiles) { return ((count + tiles - 1) / tiles + 31) & ~31; }
 
 // Tile l of an expert that has r.count rows. Eight tiles of rows with all channels, then the next
 // eight: the rows that are at work at a time, and the weights that they share, stay in L2.
+template <int kOp>
 __device__ __forceinline__ void tile_of(const ExpertArgs& g, int choice, int e, const ExpertRows& r, uint32_t l,
                                         Tile* tile) {
-    const int tiles = row_tiles(r.count, choice);
+    const int tiles = row_tiles(r.count, choice_of<kOp>(g, r.count, choice));
     tile->row = r.first;
     tile->rows = r.count;
     tile->channel = static_cast<int>(l * 256);
@@ -167,7 +179,7 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared<kOp>& 
         else
             hi = mid;
     }
-    tile_of(g, s.choice, lo, expert_rows(g.offsets, lo, g.epr, g.inv_epr, g.max_rows), t - s.prefix[lo] * across, tile);
+    tile_of<kOp>(g, s.choice, lo, expert_rows(g.offsets, lo, g.epr, g.inv_epr, g.max_rows), t - s.prefix[lo] * across, tile);
     return true;
 }
 
@@ -187,7 +199,7 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
         r = expert_rows(g.offsets, e, g.epr, g.inv_epr, g.max_rows);
         if (r.dropped && blockIdx.x == 0) raise_flag(g.status, EP_FLAG_CAPACITY);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(r.count, i);
+        for (int i = 0; i < 4; ++i) sum[i] += row_tiles(r.count, choice_of<kOp>(g, r.count, i));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -219,10 +231,10 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
         if (per > 1) r = expert_rows(g.offsets, e, g.epr, g.inv_epr, g.max_rows);
         const uint32_t begin = static_cast<uint32_t>(before) * across;
         s.prefix[e] = before;
-        before += row_tiles(r.count, choice);
+        before += row_tiles(r.count, choice_of<kOp>(g, r.count, choice));
         if (begin <= pair && pair < before * across) {
             Tile t;
-            tile_of(g, choice, e, r, pair - begin, &t);
+            tile_of<kOp>(g, choice, e, r, pair - begin, &t);
             s.tile[0] = t;
         }
         if (e == g.E - 1) s.prefix[g.E] = before;
