@@ -4,10 +4,19 @@
 // One kernel for all five. The operand with the output's channels (the weights; in their own
 // gradient, the rows that were multiplied with them) lies along the tensor cores' 256 lanes
 // of a pair of CTAs, the expert's rows along the columns, of which a product takes any
-// multiple of 32: an expert with 140 rows costs 160 columns, not two tiles of 128 rows. Each
-// CTA of a persistent grid has a warp that copies tensor boxes into a ring of stages, one (of
-// the pair) that multiplies them into tensor memory, and eight that finish the sums of one
-// tile while the next is multiplied.
+// multiple of 32: an expert with 140 rows costs 160 columns, not two tiles of 128 rows. A tile
+// is 256 channels by up to 256 rows, K long: 128 flops a byte that comes from L2.
+//
+// The grid is persistent, a CTA an SM. In a CTA two warps copy tensor boxes into a ring of 4 to 6
+// stages of 64 k, one (of the pair) multiplies them into tensor memory, one plans tiles ahead, and
+// sixteen finish the sums of one tile while the next is multiplied: 32 lanes by 16 columns at a time
+// as fragments of 8 x 8, through a patch of shared memory into rows of 16-byte vectors.
+//
+// With few rows an expert the weights' stream bounds it, with many the tensor cores' power: 4096
+// tokens top-8 of 256 experts of 7168 x 2048, gated with the 8-bit checkpoint 2.34 ms (6.7 TB/s), down
+// 1.19 ms (6.8), back through the activation 1.24 ms (6.9); 16384 tokens of 128 uneven experts of
+// 4096 x 2048 2.1 to 2.4 ms a product (1.8 to 2.1 PFLOP/s). A product takes 128 cycles however few its
+// columns: 64 k of a tile no less than 513.
 #include "ep_expert.cuh"
 #include "ep_mma.cuh"
 
@@ -91,14 +100,21 @@ struct Shared : Planned {  // behind the stages
     int prefix[1];  // [E + 1] tiles of rows before each expert's (but kWgrad)
 };
 
-// The tiles of a role, in order. next() is false where there are no more, or a wait gave up (`ok`);
+// A wait gave up: every other one of the CTA ends soon, and the caller hears of it.
+__device__ __forceinline__ void give_up(const ExpertArgs& g, Planned& s) {
+    s.stop = 1;
+    raise_flag(g.status, EP_FLAG_TIMEOUT);
+}
+
+// The tiles of a role, in order, for a whole warp. next() is false where there are no more, or a wait
+// gave up (`ok`);
 // taken(), by one thread after all of the role's have read the tile, lets its place be used again.
 struct Tiles {
     uint32_t at = kTiles - 1, phase = 1;
     bool ok = true;
     __device__ __forceinline__ bool next(Planned& s, Tile* t) {
         if (++at == kTiles) at = 0, phase ^= 1;
-        ok = mbar_wait(&s.tile_full[at], phase, &s.stop);
+        ok = __all_sync(kFullMask, mbar_wait(&s.tile_full[at], phase, &s.stop));
         if (!ok) return false;
         *t = s.tile[at];
         return t->e >= 0;
@@ -649,8 +665,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
     const int rank = static_cast<int>(cluster_rank());
     const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
+    // The next kernel may settle as places become free: it takes none from this one, whose CTAs have all
+    // begun by then.
+    allow_dependents();
     // by warps that have few experts to plan, while the others ask for theirs
-    allow_dependents();  // every CTA of the grid is resident: the next kernel takes no place from it
     if (tid == (kLastFinish - 1) * 32) {
         for (int i = 0; i < kMostStages; ++i) {
             mbar_init(&s.full[i], 1);
@@ -710,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 more = tile_at<kOp>(g, s, i, &t);
                 if (!more) t.e = -1;
                 if (!mbar_wait(&s.tile_empty[at], phase ^ 1, &s.stop)) {
-                    s.stop = 1;
+                    give_up(g, s);
                     break;
                 }
                 s.tile[at] = t;
@@ -720,8 +738,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         }
     } else if (warp == kProducer || warp == Tr::kColumnProducer) {
         // One warp copies the operand along the lanes (and counts the bytes of both), the other the one
-        // along the columns: a stage's copies take one thread longer to issue than to multiply. The whole
-        // warp keeps the books, so that they stay uniform; one lane issues.
+        // along the columns: one thread issued a stage's copies in 440 to 670 cycles, and they are
+        // multiplied in 512. The whole warp keeps the books, so that they stay uniform; one lane issues.
         const bool leader = elected(), lanes = warp == kProducer;
         int stage = 0;
         uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
@@ -791,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             }
         }
         ok = ok && tiles.ok;
-        if (!ok) s.stop = 1;
+        if (!ok) give_up(g, s);
         // The last use of every stage is waited for: by its release, or where something gave up, by
         // its bytes, so that no copy and no arrival is on its way when the CTA ends.
         const int used = issued < static_cast<uint32_t>(g.stages) ? static_cast<int>(issued) : g.stages;
@@ -804,10 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             else if (rank == 0)
                 mbar_wait(&s.full[stage], (full >> stage & 1) ^ 1, nullptr);
         }
-        if (!ok) {
-            s.stop = 1;
-            raise_flag(g.status, EP_FLAG_TIMEOUT);
-        }
+        if (!ok) give_up(g, s);
     } else if (warp == kMultiplier) {
         if (rank == 0) {
             const bool leader = elected();
@@ -861,9 +876,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 if (leader)
                     for (uint32_t i = 0; i < slots; ++i) mma_commit_pair(&s.sums_full[(first + i) % 2]);
             }
-            if (!ok || !tiles.ok) {  // the products that were begun still read shared memory
-                s.stop = 1;
-                if (leader) mma_commit_pair(&s.drain);
+            ok = ok && tiles.ok;
+            // the other CTA's last arrivals must not come when this one has ended
+            for (uint32_t i = slot < 2 ? 0 : slot - 2; ok && i < slot; ++i)
+                ok = __all_sync(kFullMask, mbar_wait<true>(&s.sums_empty[i % 2], i / 2 % 2, &s.stop));
+            if (!ok) {  // the products that were begun still read shared memory
+                give_up(g, s);
+                if (leader) mma_commit(&s.drain);
                 mbar_wait(&s.drain, 0, nullptr);
             }
         }
@@ -893,7 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(peer_addr(&s.ready[stage], 0));
             }
-            if (!ok || !tiles.ok) s.stop = 1;
+            if (!ok || !tiles.ok) give_up(g, s);
         }
     } else {
         const int group = (warp - kFinish) / 4;
@@ -906,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         while (true) {
             const bool more = tiles.next(s, &t);
             if (!group_agrees(tiles.ok, group)) {
-                s.stop = 1;
+                give_up(g, s);
                 break;
             }
             if (!more) break;
@@ -923,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             };
             if (!finish_tile<kOp>(g, b16_map, s, t, tmem + first % 2 * kSlotColumns, up_sums(tmem, first, slots),
                                   rank, warp, lane, outlet, ready)) {
-                s.stop = 1;
+                give_up(g, s);
                 break;
             }
             if (t.k > 0) {

@@ -143,6 +143,11 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
+// arrives on this CTA's barrier when the thread's products so far are done
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
 // arrives on the barrier, in both CTAs, when the thread's products so far are done
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
     asm volatile(
