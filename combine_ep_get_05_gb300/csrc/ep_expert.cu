@@ -69,13 +69,13 @@ struct ExpertArgs {
     int32_t* status;
 };
 
-// A tile: 256 channels (128 a CTA) of up to kMostN rows of an expert; in kWgrad, of up to
-// kMostN rows of its gradient.
+// A tile: 256 channels (128 a CTA), or the last 128 or fewer (64 a CTA), of up to kMostN rows of an
+// expert; in kWgrad, of up to kMostN rows of its gradient.
 struct Tile {
     long long row;  // first row of the slabs; kWgrad: the expert's
     int e;          // -1: there are no more tiles
     int rows;       // rows that are there (columns of the sums that are kept)
-    int n;          // columns that are multiplied: a multiple of 32
+    int m, n;       // lanes of the pair, 256 or 128; columns that are multiplied, a multiple of 32
     int channel;    // first of the pair's
     int column;     // kWgrad: first row of dw[e]
     int k;          // products of a sum
@@ -141,6 +141,14 @@ __device__ __forceinline__ int choice_of(const ExpertArgs& g, int count, int cho
 }
 __device__ __forceinline__ int rows_each(int count, int tiles) { return ((count + tiles - 1) / tiles + 31) & ~31; }
 
+// Lanes of a tile: the last 128 channels or fewer take 128, half of the copies, products and sums (64
+// experts of 104 channels, gated, 8192 tokens 137 us instead of 168; their gradient of weights, 512
+// tokens, 22.5 instead of 33.4; 16 experts of 128 channels 97 instead of 102). Not with the 8-bit
+// checkpoint, whose blocks of 128 channels have to be one CTA's.
+__device__ __forceinline__ int lanes_of(const ExpertArgs& g, int channel) {
+    return g.C - channel <= 128 && g.out_q == nullptr ? 128 : 256;
+}
+
 // Tile l of an expert that has r.count rows. Eight tiles of rows with all channels, then the next
 // eight: the rows that are at work at a time, and the weights that they share, stay in L2.
 template <int kOp>
@@ -162,6 +170,7 @@ __device__ __forceinline__ void tile_of(const ExpertArgs& g, int choice, int e, 
         tile->channel = static_cast<int>(l / width * 256);
     }
     tile->e = e;
+    tile->m = lanes_of(g, tile->channel);
     tile->n = (tile->rows + 31) / 32 * 32;
     tile->column = 0;
     tile->k = g.K;
@@ -183,6 +192,7 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared<kOp>& 
         tile->channel = static_cast<int>(l % across * 256);
         tile->column = static_cast<int>(l / across * 256);
         tile->rows = g.K - tile->column < 256 ? g.K - tile->column : 256;
+        tile->m = lanes_of(g, tile->channel);
         tile->n = (tile->rows + 31) / 32 * 32;
         return true;
     }
@@ -503,15 +513,15 @@ struct Outlet {
         }
         turn ^= 1;
     }
-    // zeros, from every kGroups-th chunk of the rows y0 .. y0 + rows on, `skip` rows left out
-    __device__ __forceinline__ void send_zeros(const CUtensorMap& map, int x, int y0, int z, int skip, int rows, int warp,
+    // zeros, every kGroups-th chunk of the rows from y to y_end
+    __device__ __forceinline__ void send_zeros(const CUtensorMap& map, int x, int y, int y_end, int z, int warp,
                                                int lane) {
         const bool sends = warp % 2 == 0 && lane == 0;
         if (sends) bulk_wait_read_all();
         const uint32_t none[8] = {};
         fill(none, warp, lane);
         if (sends) {
-            for (int y = skip; y < rows; y += kGroups * kChunk) tma_store_3d(map, x, y0 + y, z, patch());
+            for (; y < y_end; y += kGroups * kChunk) tma_store_3d(map, x, y, z, patch());
             bulk_commit();
         }
         turn ^= 1;
@@ -524,7 +534,10 @@ template <int kOp, typename Ready>
 __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorMap& out_map, Shared<kOp>& s, const Tile& t,
                                             uint32_t sums, uint32_t ups, int rank, int warp, int lane, Outlet& outlet, Ready ready) {
     const int group = (warp - kFinish) / 4, quarter = warp % 4;
-    const int channel = t.channel + rank * 128 + quarter * 32;  // the warp's first
+    // the warp's first channel; its columns of tensor memory and the first of the tile's that they are
+    const bool narrow = t.m == 128;
+    const int channel = t.channel + (narrow ? rank * 64 + quarter % 2 * 32 : rank * 128 + quarter * 32);
+    const int columns = narrow ? t.n / 2 : t.n, from = narrow ? quarter / 2 * columns : 0;
     const size_t C = static_cast<size_t>(g.C);
     const uint32_t patch = smem_addr(s.patch[warp - kFinish]);
     sums += static_cast<uint32_t>(quarter * 32) << 16;
@@ -532,19 +545,21 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
     const int pair_channel = channel & ~63;
     if constexpr (kOp == kWgrad) {
         if (t.k == 0) {  // an expert without rows
-            if (pair_channel < g.C && t.rows > group * kChunk)
-                outlet.send_zeros(out_map, pair_channel, t.column, t.e, group * kChunk, t.rows, warp, lane);
+            const int first = from + group * kChunk, end = t.rows < from + columns ? t.rows : from + columns;
+            if (pair_channel < g.C && first < end)
+                outlet.send_zeros(out_map, pair_channel, t.column + first, t.column + end, t.e, warp, lane);
             return true;
         }
     }
     Kept kept;
     if constexpr (kOp == kDownBwd)  // on its way while the sums are made
-        load_kept(kept, g, static_cast<size_t>(t.row) + group * kChunk, channel, {t.rows - group * kChunk, g.C - channel}, lane);
+        load_kept(kept, g, static_cast<size_t>(t.row) + from + group * kChunk, channel,
+                  {t.rows - from - group * kChunk, g.C - channel}, lane);
     if (!ready()) return false;
     int buffer = 0;
-    for (int c0 = group * kChunk; c0 < t.n; c0 += kGroups * kChunk) {
-        const Window win = {t.rows - c0, g.C - channel};
-        const size_t row = static_cast<size_t>(t.row) + c0;
+    for (int c0 = group * kChunk; c0 < columns; c0 += kGroups * kChunk) {
+        const Window win = {t.rows - from - c0, g.C - channel};
+        const size_t row = static_cast<size_t>(t.row) + from + c0;
         uint32_t w[8];
         float v[16];
         if (t.k > 0) {
@@ -617,11 +632,12 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
             store_rows(dpre, 2 * C, w, win, patch, lane);
             store_rows(dpre + C, 2 * C, dup, win, patch, lane);
             if (g.out != nullptr) store_rows(g.out + row * C + channel, C, h, win, patch, lane);
-            if (c0 + kGroups * kChunk < t.n) load_kept(kept, g, row + kGroups * kChunk, channel, {t.rows - c0 - kGroups * kChunk, g.C - channel}, lane);
+            if (c0 + kGroups * kChunk < columns)
+                load_kept(kept, g, row + kGroups * kChunk, channel, {win.rows - kGroups * kChunk, win.channels}, lane);
         } else if constexpr (kOp == kWgrad) {
             pack(w, v);
             if (win.rows > 0 && pair_channel < g.C)
-                outlet.send(out_map, pair_channel, t.column + c0, t.e, w, warp, lane);
+                outlet.send(out_map, pair_channel, t.column + from + c0, t.e, w, warp, lane);
         } else {
             pack(w, v);
             store_rows(g.out + row * C + channel, C, w, win, patch, lane);
@@ -645,19 +661,23 @@ __device__ __forceinline__ uint32_t up_sums(uint32_t tmem, uint32_t first, uint3
     return slots == 2 ? tmem + (first + 1) % 2 * kSlotColumns : tmem + first % 2 * kSlotColumns + kSlotColumns / 2;
 }
 
-// bytes of a CTA's part of the operand along the lanes that lie before the last channel
+// bytes of a CTA's part of the operand along the lanes of a tile, m / 2 lines or rows, as far as they lie
+// before the last channel
 template <int kOp>
-__device__ __forceinline__ uint32_t a_bytes(int channels) {
-    if (!Traits<kOp>::kAAcross) return channels > 0 ? Traits<kOp>::kABytes : 0;
-    return channels > 64 ? 2 * kCrossBlock : channels > 0 ? kCrossBlock : 0;
+__device__ __forceinline__ uint32_t a_bytes(int channels, int m) {
+    if (channels <= 0) return 0;
+    if (!Traits<kOp>::kAAcross) return m == 256 ? Traits<kOp>::kABytes : Traits<kOp>::kABytes / 2;
+    return m == 256 && channels > 64 ? 2 * kCrossBlock : kCrossBlock;
 }
 
-// `a`: the operand along the lanes, `b64` and `b16`: the one along the columns, in boxes of 64 rows
-// (or lines of k) and of 16; in kWgrad, `b16` is the output, in boxes of a warp's patch.
+// `a`: the operand along the lanes, in boxes of 128 rows, or of 64 lines of k, and `a64` in boxes of 64
+// rows; `b64` and `b16`: the one along the columns, in boxes of 64 rows (or lines of k) and of 16; in
+// kWgrad, `b16` is the output, in boxes of two warps' patch.
 template <int kOp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThreads, 1)
-    expert_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b64_map,
-                  const __grid_constant__ CUtensorMap b16_map, ExpertArgs g) {
+    expert_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap a64_map,
+                  const __grid_constant__ CUtensorMap b64_map, const __grid_constant__ CUtensorMap b16_map,
+                  ExpertArgs g) {
     using Tr = Traits<kOp>;
     extern __shared__ __align__(1024) unsigned char s_stages[];
     Shared<kOp>& s = *reinterpret_cast<Shared<kOp>*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
@@ -754,9 +774,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             // past the last channel are left out: the sums of what is in their place are not kept.
             const uint32_t b_bytes = kOp == kWgrad ? (half + 63) / 64 * kCrossBlock
                                                    : static_cast<uint32_t>(half) * kBlockK * 2;
-            const int c = t.channel + rank * 128, row = static_cast<int>(t.row) + (kOp == kWgrad ? 0 : b_first);
-            const uint32_t mine = a_bytes<kOp>(g.C - c), both = a_bytes<kOp>(g.C - t.channel) +
-                                                               a_bytes<kOp>(g.C - t.channel - 128) + 2 * b_bytes;
+            const int c = t.channel + rank * (t.m / 2), row = static_cast<int>(t.row) + (kOp == kWgrad ? 0 : b_first);
+            const uint32_t mine = a_bytes<kOp>(g.C - c, t.m);
+            const uint32_t both = a_bytes<kOp>(g.C - t.channel, t.m) + a_bytes<kOp>(g.C - t.channel - t.m / 2, t.m) +
+                                  2 * b_bytes;
             for (int k = 0; k < t.k; k += kBlockK) {
                 ok = __all_sync(kFullMask, mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop));
                 if (!ok) break;
@@ -772,12 +793,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                     else if (rank == 0)
                         mbar_arrive_expect_tx(&s.full[stage], both);
                     if constexpr (kOp == kGateUp) {
+                        const CUtensorMap& map = t.m == 256 ? a_map : a64_map;
                         if (mine > 0) {
-                            tma_load_pair_3d(to, a_map, k, c, 2 * t.e, bar);
-                            tma_load_pair_3d(to + 128 * kBlockK * 2, a_map, k, c, 2 * t.e + 1, bar);
+                            tma_load_pair_3d(to, map, k, c, 2 * t.e, bar);
+                            tma_load_pair_3d(to + 128 * kBlockK * 2, map, k, c, 2 * t.e + 1, bar);
                         }
                     } else if constexpr (kOp == kDown) {
-                        if (mine > 0) tma_load_pair_3d(to, a_map, k, c, t.e, bar);
+                        if (mine > 0) tma_load_pair_3d(to, t.m == 256 ? a_map : a64_map, k, c, t.e, bar);
                     } else if constexpr (kOp == kWgrad) {
                         if (mine > 0) tma_load_pair_2d(to, a_map, c, row + k, bar);
                         if (mine > kCrossBlock) tma_load_pair_2d(to + kCrossBlock, a_map, c + 64, row + k, bar);
@@ -842,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 if (!ok) break;
                 slot += slots;
                 tc_fence_after();
-                const uint32_t desc = product_desc(t.n, Tr::kAAcross, Tr::kBAcross);
+                const uint32_t desc = product_desc(t.m, t.n, Tr::kAAcross, Tr::kBAcross);
                 const uint32_t sums = tmem + first % 2 * kSlotColumns, ups = up_sums(tmem, first, slots);
                 for (int k = 0; k < t.k; k += kBlockK) {
                     const bool tail = kOp == kWgrad && has_tail(t.k - k);
@@ -920,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         // A pass without rows while the first sums are made: it brings the code in, which takes
         // longer than a small tile itself.
         Outlet outlet = {s.patch[(warp - kFinish) / 2 * 2 * Tr::kPatches]};
-        t = {0, 0, 0, 64, 0, 0, 0};
+        t = {0, 0, 0, 256, 64, 0, 0, 0};
         finish_tile<kOp>(g, b16_map, s, t, tmem, tmem, rank, warp, lane, outlet, [] { return true; });
         while (true) {
             const bool more = tiles.next(s, &t);
@@ -987,7 +1009,8 @@ ep_status_t map_of(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
 }
 
 template <int kOp>
-ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, const CUtensorMap& b16, void* stream) {
+ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& a64, const CUtensorMap& b64,
+                   const CUtensorMap& b16, void* stream) {
     using Tr = Traits<kOp>;
     static std::atomic<int> ready[kMaxDevices];
     g.epr = g.E / g.R;
@@ -999,7 +1022,7 @@ ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& b64, c
     if (st != EP_OK) return st;
     const dim3 grid(static_cast<unsigned>(sm_count() / 2 * 2));
     return launch_dependent(expert_kernel<kOp>, grid, dim3(Tr::kThreads), g.stages * Tr::kStageBytes + behind,
-                            as_stream(stream), a, b64, b16, g);
+                            as_stream(stream), a, a64, b64, b16, g);
 }
 
 FewRows few(const ExpertArgs& g, const void* x, const void* w) {
@@ -1044,10 +1067,11 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
     g.status = status;
     const int few_at_once = pre == nullptr && pre_q == nullptr ? few_rows_at_once(E, R, max_rows, true) : 0;
     if (few_at_once > 0) return launch_few_rows(few(g, x, w_gate_up), true, few_at_once, stream);
-    CUtensorMap a, b64, b16;
+    CUtensorMap a, a64, b64, b16;
     ep_status_t st = map_of(&a, w_gate_up, H, F, 2ull * E, 128);
+    if (st == EP_OK) st = map_of(&a64, w_gate_up, H, F, 2ull * E, 64);
     if (st == EP_OK) st = row_maps(&b64, &b16, x, H, g);
-    return st != EP_OK ? st : launch<kGateUp>(g, a, b64, b16, stream);
+    return st != EP_OK ? st : launch<kGateUp>(g, a, a64, b64, b16, stream);
 }
 
 ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* expert_offsets, int32_t H, int32_t F,
@@ -1067,10 +1091,11 @@ ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* exp
     g.status = status;
     const int few_at_once = few_rows_at_once(E, R, max_rows, false);
     if (few_at_once > 0) return launch_few_rows(few(g, h, w_down), false, few_at_once, stream);
-    CUtensorMap a, b64, b16;
+    CUtensorMap a, a64, b64, b16;
     ep_status_t st = map_of(&a, w_down, F, H, E, 128);
+    if (st == EP_OK) st = map_of(&a64, w_down, F, H, E, 64);
     if (st == EP_OK) st = row_maps(&b64, &b16, h, F, g);
-    return st != EP_OK ? st : launch<kDown>(g, a, b64, b16, stream);
+    return st != EP_OK ? st : launch<kDown>(g, a, a64, b64, b16, stream);
 }
 
 ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* pre, const uint8_t* pre_q,
@@ -1103,7 +1128,7 @@ ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* p
     CUtensorMap a, b64, b16;
     ep_status_t st = map_of(&a, w_down, F, H, E, 64);
     if (st == EP_OK) st = row_maps(&b64, &b16, dy, H, g);
-    return st != EP_OK ? st : launch<kDownBwd>(g, a, b64, b16, stream);
+    return st != EP_OK ? st : launch<kDownBwd>(g, a, a, b64, b16, stream);
 }
 
 ep_status_t ep_expert_gate_up_bwd(const void* dpre, const void* w_gate_up, const int32_t* expert_offsets, int32_t H,
@@ -1126,7 +1151,7 @@ ep_status_t ep_expert_gate_up_bwd(const void* dpre, const void* w_gate_up, const
     CUtensorMap a, b64, b16;
     ep_status_t st = map_of(&a, w_gate_up, H, 2ull * F, E, 64);
     if (st == EP_OK) st = row_maps(&b64, &b16, dpre, 2ull * F, g);
-    return st != EP_OK ? st : launch<kGateUpBwd>(g, a, b64, b16, stream);
+    return st != EP_OK ? st : launch<kGateUpBwd>(g, a, a, b64, b16, stream);
 }
 
 ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* expert_offsets, int32_t I, int32_t J,
@@ -1152,7 +1177,7 @@ ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* e
     ep_status_t st = map_of(&a, rows, J, n, 0, 64);
     if (st == EP_OK) st = map_of(&b, dout, I, n, 0, 64);
     if (st == EP_OK) st = map_of(&out, dw, J, I, E, 16);
-    return st != EP_OK ? st : launch<kWgrad>(g, a, b, out, stream);
+    return st != EP_OK ? st : launch<kWgrad>(g, a, a, b, out, stream);
 }
 
 }  // extern "C"

@@ -3,7 +3,8 @@
 //
 // A pair multiplies M = 256 rows of A (128 from each CTA's shared memory) with N columns of B
 // (N/2 from each), 16 k at a time, into tensor memory: CTA 0 holds rows 0 .. 127, CTA 1 rows
-// 128 .. 255, a row a lane, a column a 32-bit column. Operands lie in shared memory as 128-byte
+// 128 .. 255, a row a lane, a column a 32-bit column. With M = 128 each CTA has 64 rows of A, and of the
+// sums lanes 0 .. 63 hold their columns 0 .. N/2 - 1, lanes 64 .. 127 the others. Operands lie in shared memory as 128-byte
 // swizzled tensor copies leave them, in one of two ways:
 //   along k:       rows of 64 k (128 bytes), 8 rows an atom of 1024 bytes
 //   across k:      blocks of 64 rows of the operand: 64 lines of one k each, 64 values a line
@@ -130,10 +131,10 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool across) {
 }
 constexpr uint64_t kStepAlong = 32 >> 4, kStepAcross = 2048 >> 4;  // a descriptor's, per 16 k
 
-// Instruction descriptor: bf16 operands, fp32 sums, M = 256, N columns; bits 15 and 16: A, B across k.
-__device__ __forceinline__ uint32_t product_desc(int n, bool a_across, bool b_across) {
+// Instruction descriptor: bf16 operands, fp32 sums, M = m (128 or 256), N = n; bits 15 and 16: A, B across k.
+__device__ __forceinline__ uint32_t product_desc(int m, int n, bool a_across, bool b_across) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (a_across ? 1u << 15 : 0u) | (b_across ? 1u << 16 : 0u) |
-           static_cast<uint32_t>(n >> 3) << 17 | (256u >> 4) << 24;
+           static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 // D (+)= A B^T over 16 k; one thread of CTA 0, for the pair
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
