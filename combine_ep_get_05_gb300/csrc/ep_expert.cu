@@ -369,37 +369,14 @@ __device__ __forceinline__ void load_codes(uint4 (&v)[2], const uint8_t* from, s
         v[q].y = c.y;
     }
 }
-// codes into fragments of fp16 (every code is one), times their scales; scale: lane j has row j's
-__device__ __forceinline__ void spread_codes(float (&v)[16], const uint4 (&c)[2], float scale, uint32_t patch,
-                                             int lane) {
+// codes into fragments of fp16 (every code is one)
+__device__ __forceinline__ void spread_codes(uint32_t (&w)[8], const uint4 (&c)[2], uint32_t patch, int lane) {
     uint4 f[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
         f[q] = make_uint4(e4m3x2_to_f16x2(c[q].x), e4m3x2_to_f16x2(c[q].x >> 16), e4m3x2_to_f16x2(c[q].y),
                           e4m3x2_to_f16x2(c[q].y >> 16));
-    uint32_t w[8];
     spread(w, f, patch, lane);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const float s0 = __shfl_sync(kFullMask, scale, 8 * q + lane % 4 * 2);
-        const float s1 = __shfl_sync(kFullMask, scale, 8 * q + lane % 4 * 2 + 1);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int i = fragment(q, b);
-            v[i] = f16_to_f32(w[4 * q + b] & 0xffffu) * s0;
-            v[i + 1] = f16_to_f32(w[4 * q + b] >> 16) * s1;
-        }
-    }
-}
-__device__ __forceinline__ void unpack(float (&v)[16], const uint32_t (&w)[8]) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int i = fragment(q, b);
-            v[i] = bf16_lo(w[4 * q + b]);
-            v[i + 1] = bf16_hi(w[4 * q + b]);
-        }
 }
 
 // max |v| of every column over the warp's lanes, NaN apart, into to[column]
@@ -422,28 +399,48 @@ __device__ __forceinline__ void activate(float (&v)[16], const float (&up)[16]) 
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = v[j] * gate_of<kGelu>(v[j]).s * up[j];
 }
-// dh, gate and up into dgate, dup and h, packed
-template <bool kGelu>
+// dh, gate and up (fragments of bf16, or of fp16 times their rows' scales, of which lane j has row j's)
+// into dgate, dup and h, packed
+template <bool kGelu, bool kCodes>
 __device__ __forceinline__ void activate_bwd(uint32_t (&dgate)[8], uint32_t (&dup)[8], uint32_t (&h)[8],
-                                             const float (&dh)[16], const float (&gate)[16], const float (&up)[16]) {
+                                             const float (&dh)[16], const uint32_t (&gates)[8],
+                                             const uint32_t (&ups)[8], float gate_scale, float up_scale, int lane) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2; ++q) {
+        float gs[2], us[2];
+        if (kCodes) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                gs[j] = __shfl_sync(kFullMask, gate_scale, 8 * q + lane % 4 * 2 + j);
+                us[j] = __shfl_sync(kFullMask, up_scale, 8 * q + lane % 4 * 2 + j);
+            }
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
+            const uint32_t wg = gates[4 * q + b], wu = ups[4 * q + b];
             float dg[2], du[2], hh[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int i = fragment(q, b) + j;
-                const Gate a = gate_of<kGelu>(gate[i]);
-                const float act = gate[i] * a.s;
-                dg[j] = dh[i] * up[i] * (a.s + act * (1.0f - a.s) * a.slope);
-                du[j] = dh[i] * act;
-                hh[j] = act * up[i];
+                float gate, up;
+                if (kCodes) {
+                    gate = f16_to_f32(j == 0 ? wg & 0xffffu : wg >> 16) * gs[j];
+                    up = f16_to_f32(j == 0 ? wu & 0xffffu : wu >> 16) * us[j];
+                } else {
+                    gate = j == 0 ? bf16_lo(wg) : bf16_hi(wg);
+                    up = j == 0 ? bf16_lo(wu) : bf16_hi(wu);
+                }
+                const float d = dh[fragment(q, b) + j];
+                const Gate a = gate_of<kGelu>(gate);
+                const float act = gate * a.s;
+                dg[j] = d * up * (a.s + act * (1.0f - a.s) * a.slope);
+                du[j] = d * act;
+                hh[j] = act * up;
             }
             dgate[4 * q + b] = pack_bf16x2_rn(dg[0], dg[1]);
             dup[4 * q + b] = pack_bf16x2_rn(du[0], du[1]);
             h[4 * q + b] = pack_bf16x2_rn(hh[0], hh[1]);
         }
+    }
 }
 
 // true in all 128 threads of a group of finishing warps, or in none
@@ -613,21 +610,23 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
             pack(w, v);
             store_rows(g.out + row * C + channel, C, w, win, patch, lane);
         } else if constexpr (kOp == kDownBwd) {
-            float gate[16], up[16];
+            uint32_t gates[8], ups[8], dup[8], h[8];
+            const bool gelu = g.act == EP_ACT_GELU;
             if (g.pre != nullptr) {
-                spread(w, kept.gate, patch, lane);
-                unpack(gate, w);
-                spread(w, kept.up, patch, lane);
-                unpack(up, w);
+                spread(gates, kept.gate, patch, lane);
+                spread(ups, kept.up, patch, lane);
+                if (gelu)
+                    activate_bwd<true, false>(w, dup, h, v, gates, ups, 1.0f, 1.0f, lane);
+                else
+                    activate_bwd<false, false>(w, dup, h, v, gates, ups, 1.0f, 1.0f, lane);
             } else {
-                spread_codes(gate, kept.gate, kept.gate_scale, patch, lane);
-                spread_codes(up, kept.up, kept.up_scale, patch, lane);
+                spread_codes(gates, kept.gate, patch, lane);
+                spread_codes(ups, kept.up, patch, lane);
+                if (gelu)
+                    activate_bwd<true, true>(w, dup, h, v, gates, ups, kept.gate_scale, kept.up_scale, lane);
+                else
+                    activate_bwd<false, true>(w, dup, h, v, gates, ups, kept.gate_scale, kept.up_scale, lane);
             }
-            uint32_t dup[8], h[8];
-            if (g.act == EP_ACT_GELU)
-                activate_bwd<true>(w, dup, h, v, gate, up);
-            else
-                activate_bwd<false>(w, dup, h, v, gate, up);
             uint16_t* const dpre = g.out_pre + row * 2 * C + channel;
             store_rows(dpre, 2 * C, w, win, patch, lane);
             store_rows(dpre + C, 2 * C, dup, win, patch, lane);
