@@ -397,7 +397,7 @@ __device__ __forceinline__ void column_max(float* to, const float (&v)[16], int 
 template <bool kGelu>
 __device__ __forceinline__ void activate(float (&v)[16], const float (&up)[16]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = v[j] * gate_of<kGelu>(v[j]).s * up[j];
+    for (int j = 0; j < 16; ++j) v[j] = v[j] * sigmoid_of<kGelu>(v[j]) * up[j];
 }
 // dh, gate and up (fragments of bf16, or of fp16 times their rows' scales, of which lane j has row j's)
 // into dgate, dup and h, packed
@@ -430,9 +430,8 @@ __device__ __forceinline__ void activate_bwd(uint32_t (&dgate)[8], uint32_t (&du
                     up = j == 0 ? bf16_lo(wu) : bf16_hi(wu);
                 }
                 const float d = dh[fragment(q, b) + j];
-                const Gate a = gate_of<kGelu>(gate);
-                const float act = gate * a.s;
-                dg[j] = d * up * (a.s + act * (1.0f - a.s) * a.slope);
+                const float sig = sigmoid_of<kGelu>(gate), act = gate * sig;
+                dg[j] = d * up * slope_of<kGelu>(gate, act, sig);
                 du[j] = d * act;
                 hh[j] = act * up;
             }

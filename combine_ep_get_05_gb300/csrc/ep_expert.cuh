@@ -49,26 +49,26 @@ __device__ __forceinline__ ExpertRows expert_rows(const int32_t* offsets, int e,
     return {static_cast<long long>(r) * max_rows + lo, static_cast<int>(hi - lo), b > max_rows && b > a};
 }
 
-// act(v) = v * s, s = sigmoid(p(v)); both activations are of this form, so that their
-// derivative is s + v * s * (1 - s) * p'(v). The exponential and the reciprocal are the fast
-// ones (a few 2^-22 relative): what comes out is rounded to bf16. exp overflows to infinity where
-// p < -88, whose reciprocal is 0: the right limit.
-struct Gate {
-    float s, slope;  // sigmoid(p(v)), p'(v)
-};
+// act(v) = v * s, s = sigmoid(p(v)); both activations are of this form, so that their derivative is
+// s + v * s * (1 - s) * p'(v). The sigmoid is 1 / (1 + 2^(-p log2 e)) by the GPU's fast power and
+// reciprocal (a few 2^-22 relative each, the exponent's rounding |p| 2^-24 more): what comes out is
+// rounded to bf16. The power is infinite where p < -88, and its reciprocal 0: the right limit.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // p(v) = A (v + B v^3), A = 2 sqrt(2 / pi)
 
 template <bool kGelu>
-__device__ __forceinline__ Gate gate_of(float v) {
-    float p = v, slope = 1.0f;
-    if (kGelu) {
-        constexpr float kA = 1.5957691216057308f, kB = 0.044715f;  // 2 sqrt(2 / pi)
-        const float v2 = v * v;
-        p = kA * (v + kB * v * v2);
-        slope = kA * (1.0f + 3.0f * kB * v2);
-    }
-    float s;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-p)));
-    return {s, slope};
+__device__ __forceinline__ float sigmoid_of(float v) {
+    const float m = kGelu ? v * fmaf(-kGeluA * kGeluB * kLog2e, v * v, -kGeluA * kLog2e) : v * -kLog2e;
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
+// act'(v) from act(v) and the sigmoid
+template <bool kGelu>
+__device__ __forceinline__ float slope_of(float v, float act, float s) {
+    const float q = kGelu ? act * fmaf(3.0f * kGeluA * kGeluB, v * v, kGeluA) : act;
+    return s + fmaf(-q, s, q);
 }
 
 // bf16_rn(amax / 448), 0 below 2^-100 (so that its reciprocal is finite)

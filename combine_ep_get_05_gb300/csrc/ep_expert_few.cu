@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(FewRows g) {
                     v += s.v[turn][w][c / kChannels][c % kChannels][r];
                     if (kGated) up += s.v[turn][w][1][c][r];
                 }
-                if (kGated) v = v * (g.act == EP_ACT_GELU ? gate_of<true>(v).s : gate_of<false>(v).s) * up;
+                if (kGated) v = v * (g.act == EP_ACT_GELU ? sigmoid_of<true>(v) : sigmoid_of<false>(v)) * up;
                 g.out[static_cast<size_t>(here.first + here.row0 + r) * C + channel] =
                     static_cast<uint16_t>(pack_bf16x2_rn(v, 0.0f));
             }
