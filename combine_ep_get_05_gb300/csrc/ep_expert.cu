@@ -159,15 +159,19 @@ __device__ __forceinline__ void tile_of(const ExpertArgs& g, int choice, int e, 
     tile->rows = r.count;
     tile->channel = static_cast<int>(l * 256);
     if (tiles > 1) {
-        const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256;
         const int each = rows_each(r.count, tiles);
-        const uint32_t group = l / (8 * across);
-        l -= group * 8 * across;
-        const uint32_t left = tiles - group * 8, width = left < 8 ? left : 8;
-        const int i = static_cast<int>(group * 8 + l % width);
+        uint32_t before = 0, width = tiles;
+        if (tiles > 8) {
+            const uint32_t across = (static_cast<uint32_t>(g.C) + 255) / 256, group = l / (8 * across);
+            l -= group * 8 * across;
+            before = group * 8;
+            width = tiles - before < 8 ? tiles - before : 8;
+        }
+        const uint32_t slice = l / width;
+        const int i = static_cast<int>(before + l - slice * width);
         tile->row += static_cast<long long>(i) * each;
         tile->rows = r.count - i * each < each ? r.count - i * each : each;
-        tile->channel = static_cast<int>(l / width * 256);
+        tile->channel = static_cast<int>(slice * 256);
     }
     tile->e = e;
     tile->m = lanes_of(g, tile->channel);
@@ -235,17 +239,18 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
     __syncthreads();
     // lane w of every warp has warp w's sum of the choice
     static_assert(kThreads <= 32 * 32);
-    int choice = 0, mine = sum[0], others = 0;
-    uint32_t total = 0;
+    int others[4], choice = 3;
+    uint32_t total[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        others = lane < kThreads / 32 ? s.scan[i][lane] : 0;
-        total = __reduce_add_sync(kFullMask, static_cast<unsigned>(others));
-        choice = i;
-        mine = sum[i];
-        if (total * across >= pairs) break;
-    }
-    int before = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(lane < warp ? others : 0)));
+    for (int i = 0; i < 4; ++i) others[i] = lane < kThreads / 32 ? s.scan[i][lane] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total[i] = __reduce_add_sync(kFullMask, static_cast<unsigned>(others[i]));
+    int mine = sum[3], theirs = others[3];
+    uint32_t tiles = total[3];
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+        if (total[i] * across >= pairs) choice = i, mine = sum[i], theirs = others[i], tiles = total[i];
+    int before = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(lane < warp ? theirs : 0)));
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -267,7 +272,7 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
     }
     if (tid == 0) {
         s.choice = choice;
-        if (pair >= total * across) s.tile[0].e = -1;
+        if (pair >= tiles * across) s.tile[0].e = -1;
     }
 }
 
