@@ -15,8 +15,8 @@
 // With few rows an expert the weights' stream bounds it, with many the tensor cores' power: 4096
 // tokens top-8 of 256 experts of 7168 x 2048, gated with the 8-bit checkpoint 2.34 ms (6.7 TB/s), down
 // 1.19 ms (6.8), back through the activation 1.24 ms (6.9); 16384 tokens of 128 uneven experts of
-// 4096 x 2048 2.1 to 2.4 ms a product (1.8 to 2.1 PFLOP/s). A product takes 128 cycles however few its
-// columns: 64 k of a tile no less than 513.
+// 4096 x 2048 2.1 to 2.4 ms a product (1.8 to 2.1 PFLOP/s). With few rows and few tiles the warp that
+// multiplies bounds it, 146 ns for 64 k.
 #include "ep_expert.cuh"
 #include "ep_mma.cuh"
 
@@ -107,16 +107,26 @@ __device__ __forceinline__ void give_up(const ExpertArgs& g, Planned& s) {
 }
 
 // The tiles of a role, in order, for a whole warp. next() is false where there are no more, or a wait
-// gave up (`ok`);
-// taken(), by one thread after all of the role's have read the tile, lets its place be used again.
+// gave up (`ok`); taken(), by one thread after all of the role's have read the tile, lets its place be used
+// again. kUniform: for warps that feed the units, whose instructions take what is known to be uniform.
 struct Tiles {
     uint32_t at = kTiles - 1, phase = 1;
     bool ok = true;
+    template <bool kUniform = false>
     __device__ __forceinline__ bool next(Planned& s, Tile* t) {
         if (++at == kTiles) at = 0, phase ^= 1;
         ok = __all_sync(kFullMask, mbar_wait(&s.tile_full[at], phase, &s.stop));
         if (!ok) return false;
         *t = s.tile[at];
+        if (kUniform) {
+            t->row = uniform(t->row);
+            t->e = uniform(t->e);
+            t->m = uniform(t->m);
+            t->n = uniform(t->n);
+            t->channel = uniform(t->channel);
+            t->column = uniform(t->column);
+            t->k = uniform(t->k);
+        }
         return t->e >= 0;
     }
     __device__ __forceinline__ void taken(Planned& s) { mbar_arrive(&s.tile_empty[at]); }
@@ -684,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
     using Tr = Traits<kOp>;
     extern __shared__ __align__(1024) unsigned char s_stages[];
     Shared<kOp>& s = *reinterpret_cast<Shared<kOp>*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
-    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = uniform(tid / 32);
     const int rank = static_cast<int>(cluster_rank());
     const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
@@ -738,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
     __syncthreads();
     cluster_wait();
     tc_fence_after();
-    const uint32_t tmem = s.tmem;
+    const uint32_t tmem = uniform(s.tmem);
 
     Tile t;
     Tiles tiles;
@@ -767,8 +777,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         int stage = 0;
         uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
         uint32_t issued = 0;
+        const uint32_t counted = peer_addr(&s.full[0], 0);
         bool ok = true;
-        while (ok && tiles.next(s, &t)) {
+        while (ok && tiles.next<true>(s, &t)) {
             __syncwarp();
             if (leader) tiles.taken(s);
             const int half = t.n / 2;
@@ -782,14 +793,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             const uint32_t both = a_bytes<kOp>(g.C - t.channel, t.m) + a_bytes<kOp>(g.C - t.channel - t.m / 2, t.m) +
                                   2 * b_bytes;
             for (int k = 0; k < t.k; k += kBlockK) {
-                ok = __all_sync(kFullMask, mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop));
+                ok = warp_wait(&s.empty[stage], empty >> stage & 1, &s.stop);
                 if (!ok) break;
                 empty ^= 1u << stage;
                 const uint32_t to = smem_addr(s_stages) + stage * Tr::kStageBytes;
                 const uint32_t b_to = to + Tr::kABytes;
                 const bool tail = kOp == kWgrad && has_tail(t.k - k);
                 // a tail's bytes each CTA counts itself, since it clears them; others CTA 0 counts for both
-                const uint32_t bar = tail ? smem_addr(&s.part[stage]) : peer_addr(&s.full[stage], 0);
+                const uint32_t bar = tail ? smem_addr(&s.part[stage]) : counted + stage * 8;
                 if (leader && lanes) {
                     if (tail)
                         mbar_arrive_expect_tx(&s.part[stage], mine + b_bytes);
@@ -853,10 +864,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             const bool leader = elected();
             int stage = 0;
             uint32_t full = 0, ready = 0, slot = 0;
+            constexpr uint32_t kUp = 128 * kBlockK * 2 >> 4;
+            const uint32_t first_a = operand_low(smem_addr(s_stages), Tr::kAAcross);
+            const uint32_t first_b = operand_low(smem_addr(s_stages) + Tr::kABytes, Tr::kBAcross);
             bool ok = true;
-            constexpr uint64_t kAStep = Tr::kAAcross ? kStepAcross : kStepAlong;
-            constexpr uint64_t kBStep = Tr::kBAcross ? kStepAcross : kStepAlong;
-            while (ok && tiles.next(s, &t)) {
+            constexpr uint32_t kAStep = Tr::kAAcross ? kStepAcross : kStepAlong;
+            constexpr uint32_t kBStep = Tr::kBAcross ? kStepAcross : kStepAlong;
+            while (ok && tiles.next<true>(s, &t)) {
                 __syncwarp();
                 if (leader) tiles.taken(s);
                 if (t.k == 0) continue;
@@ -869,29 +883,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 tc_fence_after();
                 const uint32_t desc = product_desc(t.m, t.n, Tr::kAAcross, Tr::kBAcross);
                 const uint32_t sums = tmem + first % 2 * kSlotColumns, ups = up_sums(tmem, first, slots);
-                for (int k = 0; k < t.k; k += kBlockK) {
-                    const bool tail = kOp == kWgrad && has_tail(t.k - k);
-                    if (tail) {
-                        ok = mbar_wait<true>(&s.ready[stage], ready >> stage & 1, &s.stop);
-                        ready ^= 1u << stage;
-                    } else {
-                        ok = mbar_wait(&s.full[stage], full >> stage & 1, &s.stop);
-                        full ^= 1u << stage;
-                    }
-                    ok = __all_sync(kFullMask, ok);
+                // Whole stages without a branch between their products, on values that the compiler knows to
+                // be uniform: 64 k take 146 ns (N = 32; products 70, barriers and loop 76), and took 229 with
+                // branches and values of each lane's own.
+                int k = 0;
+                for (; k + kBlockK <= t.k; k += kBlockK) {
+                    ok = warp_wait(&s.full[stage], full >> stage & 1, &s.stop);
                     if (!ok) break;
+                    full ^= 1u << stage;
                     tc_fence_after();
-                    const uint32_t from = smem_addr(s_stages) + stage * Tr::kStageBytes;
-                    const uint64_t a = operand_desc(from, Tr::kAAcross);
-                    const uint64_t up = operand_desc(from + 128 * kBlockK * 2, Tr::kAAcross);
-                    const uint64_t b = operand_desc(from + Tr::kABytes, Tr::kBAcross);
-                    const int left = t.k - k;
+                    const uint32_t a = first_a + stage * (Tr::kStageBytes >> 4);
+                    const uint32_t b = first_b + stage * (Tr::kStageBytes >> 4);
                     if (leader) {
 #pragma unroll
                         for (int j = 0; j < kBlockK / 16; ++j) {
-                            if (j * 16 >= left) break;
                             mma_pair(sums, a + j * kAStep, b + j * kBStep, desc, j > 0 || k > 0);
-                            if (Tr::kGated) mma_pair(ups, up + j * kAStep, b + j * kBStep, desc, j > 0 || k > 0);
+                            if (Tr::kGated) mma_pair(ups, a + kUp + j * kAStep, b + j * kBStep, desc, j > 0 || k > 0);
+                        }
+                        mma_commit_pair(&s.empty[stage]);
+                    }
+                    if (++stage == g.stages) stage = 0;
+                }
+                if (ok && k < t.k) {  // the rest
+                    if (kOp == kWgrad && has_tail(t.k - k)) {
+                        ok = warp_wait<true>(&s.ready[stage], ready >> stage & 1, &s.stop);
+                        ready ^= 1u << stage;
+                    } else {
+                        ok = warp_wait(&s.full[stage], full >> stage & 1, &s.stop);
+                        full ^= 1u << stage;
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t a = first_a + stage * (Tr::kStageBytes >> 4), b = first_b + stage * (Tr::kStageBytes >> 4);
+                    if (leader) {
+                        for (; k < t.k; k += 16, a += kAStep, b += kBStep) {
+                            mma_pair(sums, a, b, desc, k > 0);
+                            if (Tr::kGated) mma_pair(ups, a + kUp, b, desc, k > 0);
                         }
                         mma_commit_pair(&s.empty[stage]);
                     }

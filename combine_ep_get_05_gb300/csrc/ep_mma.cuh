@@ -17,6 +17,11 @@ namespace ep {
 constexpr int kBlockK = 64;                    // k of a stage: 128 bytes of bf16
 constexpr uint32_t kCrossBlock = 64 * 64 * 2;  // bytes of a block of 64 rows by 64 k, across k
 
+// a value that all lanes hold, so that the compiler knows it, too
+template <class T>
+__device__ __forceinline__ T uniform(T v) {
+    return __shfl_sync(0xffffffffu, v, 0);
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -91,6 +96,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     return false;
 }
 
+// the same for a whole warp
+template <bool kCluster = false>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* stop) {
+    if (__all_sync(0xffffffffu, mbar_try<kCluster>(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, stop));
+}
+
 // tensor loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)
 __device__ __forceinline__ void tma_load_pair_2d(uint32_t dst, const CUtensorMap& map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -123,13 +135,12 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // Shared-memory operand descriptor: address and strides in units of 16 bytes, version 1, 128-byte
 // swizzle. Along k an atom of 8 rows follows another every 1024 bytes (and 16 k are 32 bytes
 // further); across k, 8 lines of k are 1024 bytes and a block of 64 rows kCrossBlock (and 16 k
-// are 16 lines, 2048 bytes, further).
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool across) {
-    const uint64_t leading = across ? kCrossBlock >> 4 : 1;
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | leading << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
+// are 16 lines, 2048 bytes, further). The lower half has what changes from product to product.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, bool across) {
+    return (addr & 0x3ffffu) >> 4 | (across ? kCrossBlock >> 4 : 1u) << 16;
 }
-constexpr uint64_t kStepAlong = 32 >> 4, kStepAcross = 2048 >> 4;  // a descriptor's, per 16 k
+constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
+constexpr uint32_t kStepAlong = 32 >> 4, kStepAcross = 2048 >> 4;  // a descriptor's, per 16 k
 
 // Instruction descriptor: bf16 operands, fp32 sums, M = m (128 or 256), N = n; bits 15 and 16: A, B across k.
 __device__ __forceinline__ uint32_t product_desc(int m, int n, bool a_across, bool b_across) {
@@ -137,11 +148,11 @@ __device__ __forceinline__ uint32_t product_desc(int m, int n, bool a_across, bo
            static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 // D (+)= A B^T over 16 k; one thread of CTA 0, for the pair
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
         : "memory");
 }
 // arrives on this CTA's barrier when the thread's products so far are done
