@@ -7,7 +7,7 @@
 // multiple of 32: an expert with 140 rows costs 160 columns, not two tiles of 128 rows. A tile
 // is 256 channels by up to 256 rows, K long: 128 flops a byte that comes from L2.
 //
-// The grid is persistent, a CTA an SM. In a CTA two warps copy tensor boxes into a ring of 4 to 6
+// The grid is persistent, a CTA an SM. In a CTA two warps copy tensor boxes into a ring of 4 to 11
 // stages of 64 k, one (of the pair) multiplies them into tensor memory, one plans tiles ahead, and
 // sixteen finish the sums of one tile while the next is multiplied: 32 lanes by 16 columns at a time
 // as fragments of 8 x 8, through a patch of shared memory into rows of 16-byte vectors.
@@ -32,7 +32,7 @@ constexpr int kProducer = 0, kMultiplier = 1, kTail = 2, kScheduler = 3, kFinish
 constexpr int kFinishWarps = 4 * kGroups, kLastFinish = kFinish + kFinishWarps - 1;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSlotColumns = 256;  // of tensor memory: two tiles at a time
-constexpr int kMostStages = 8;
+constexpr int kMostStages = 12;
 constexpr int kTiles = 4;  // that are planned ahead
 constexpr int kMostNLog = 8, kMostN = 1 << kMostNLog;  // rows of an expert a tile
 constexpr size_t kSmemMost = 227 * 1024;
@@ -44,7 +44,8 @@ struct Traits {
     static constexpr bool kBAcross = kOp == kWgrad;
     static constexpr uint32_t kABytes = (kGated ? 2 : 1) * 128 * kBlockK * 2;
     static constexpr uint32_t kBBytes = kMostN / 2 * kBlockK * 2;
-    static constexpr uint32_t kStageBytes = kABytes + kBBytes;  // of one CTA
+    // of one CTA, with tiles of up to kMostN >> choice rows
+    static constexpr __host__ __device__ uint32_t stage_bytes(int choice) { return kABytes + (kBBytes >> choice); }
     static constexpr int kPatches = kOp == kWgrad ? 2 : 1;      // a finishing warp (kWgrad: four of a pair)
     // the second warp that copies in: the tails' place where there are none (20 warps leave 96
     // registers a thread, 21 no more than 80)
@@ -60,7 +61,8 @@ struct ExpertArgs {
     int E, R, max_rows;
     int epr;        // experts a rank
     float inv_epr;  // 1 / epr
-    int stages;
+    uint32_t ring;    // bytes of the stages
+    uint32_t stages;  // a byte a choice of rows a tile (Planned): how many
     const uint16_t* pre;
     const uint8_t* pre_q;
     const uint16_t* pre_scales;
@@ -100,6 +102,19 @@ struct Shared : Planned {  // behind the stages
     int prefix[1];  // [E + 1] tiles of rows before each expert's (but kWgrad)
 };
 
+// The stages. What a tile's rows leave of one goes to further ones: with few tiles the bytes on their way
+// bound the copies (one expert of 7168 x 2048, 96 rows, gated: 38 us with 4 stages, 31 with 6).
+template <int kOp>
+struct Ring {
+    uint32_t bytes;  // of a stage
+    int stages;
+    __device__ __forceinline__ Ring(const ExpertArgs& g, const Planned& s) {
+        const int choice = kOp == kWgrad ? 0 : uniform(s.choice);
+        bytes = Traits<kOp>::stage_bytes(choice);
+        stages = static_cast<int>(g.stages >> 8 * choice & 255);
+    }
+};
+
 // A wait gave up: every other one of the CTA ends soon, and the caller hears of it.
 __device__ __forceinline__ void give_up(const ExpertArgs& g, Planned& s) {
     s.stop = 1;
@@ -108,18 +123,19 @@ __device__ __forceinline__ void give_up(const ExpertArgs& g, Planned& s) {
 
 // The tiles of a role, in order, for a whole warp. next() is false where there are no more, or a wait
 // gave up (`ok`); taken(), by one thread after all of the role's have read the tile, lets its place be used
-// again. kUniform: for warps that feed the units, whose instructions take what is known to be uniform.
+// again. kUniform: with a tile that the compiler knows to be the same for the warp.
 struct Tiles {
     uint32_t at = kTiles - 1, phase = 1;
     bool ok = true;
     template <bool kUniform = false>
     __device__ __forceinline__ bool next(Planned& s, Tile* t) {
         if (++at == kTiles) at = 0, phase ^= 1;
-        ok = __all_sync(kFullMask, mbar_wait(&s.tile_full[at], phase, &s.stop));
+        ok = warp_wait(&s.tile_full[at], phase, &s.stop);
         if (!ok) return false;
         *t = s.tile[at];
         if (kUniform) {
             t->row = uniform(t->row);
+            t->rows = uniform(t->rows);
             t->e = uniform(t->e);
             t->m = uniform(t->m);
             t->n = uniform(t->n);
@@ -224,8 +240,10 @@ __device__ __forceinline__ bool tile_at(const ExpertArgs& g, const Shared<kOp>& 
 }
 
 // The number of tiles of rows before each expert's, by all threads, and the pair's first tile, by
-// the thread that meets it. A tile has 256 rows at most, or 128, 64 or 32 where the tiles would not
-// fill the GPU otherwise.
+// the thread that meets it. A tile has 256 rows at most, or 128, 64 or 32 where all tiles are at work
+// at once even then: more of them draw more, but a second round costs as much as the first (one expert
+// of 7168 x 2048, 512 rows, gated: 64 tiles 39 us, 128 of half the rows 66; 96 rows back through the
+// up-projection: 56 tiles 17 us, 84 26).
 template <int kOp>
 __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, uint32_t pair, uint32_t pairs) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
@@ -249,17 +267,17 @@ __device__ __forceinline__ void plan_tiles(const ExpertArgs& g, Shared<kOp>& s, 
     __syncthreads();
     // lane w of every warp has warp w's sum of the choice
     static_assert(kThreads <= 32 * 32);
-    int others[4], choice = 3;
+    int others[4], choice = 0;
     uint32_t total[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) others[i] = lane < kThreads / 32 ? s.scan[i][lane] : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) total[i] = __reduce_add_sync(kFullMask, static_cast<unsigned>(others[i]));
-    int mine = sum[3], theirs = others[3];
-    uint32_t tiles = total[3];
+    int mine = sum[0], theirs = others[0];
+    uint32_t tiles = total[0];
 #pragma unroll
-    for (int i = 2; i >= 0; --i)
-        if (total[i] * across >= pairs) choice = i, mine = sum[i], theirs = others[i], tiles = total[i];
+    for (int i = 1; i < 4; ++i)
+        if (total[i] * across <= pairs) choice = i, mine = sum[i], theirs = others[i], tiles = total[i];
     int before = static_cast<int>(__reduce_add_sync(kFullMask, static_cast<unsigned>(lane < warp ? theirs : 0)));
     int upto = mine;
 #pragma unroll
@@ -693,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                   ExpertArgs g) {
     using Tr = Traits<kOp>;
     extern __shared__ __align__(1024) unsigned char s_stages[];
-    Shared<kOp>& s = *reinterpret_cast<Shared<kOp>*>(s_stages + static_cast<size_t>(g.stages) * Tr::kStageBytes);
+    Shared<kOp>& s = *reinterpret_cast<Shared<kOp>*>(s_stages + g.ring);
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = uniform(tid / 32);
     const int rank = static_cast<int>(cluster_rank());
     const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -706,8 +724,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         for (int i = 0; i < kMostStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
-            mbar_init(&s.part[i], 1);
-            mbar_init(&s.ready[i], 2);
+            if (kOp == kWgrad) {
+                mbar_init(&s.part[i], 1);
+                mbar_init(&s.ready[i], 2);
+            }
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.sums_full[i], 1);
@@ -777,6 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         int stage = 0;
         uint32_t empty = ~0u, full = 0, part = 0, last_part = 0;  // a bit a stage: parities; its last use
         uint32_t issued = 0;
+        const Ring<kOp> ring(g, s);
         const uint32_t counted = peer_addr(&s.full[0], 0);
         bool ok = true;
         while (ok && tiles.next<true>(s, &t)) {
@@ -796,7 +817,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 ok = warp_wait(&s.empty[stage], empty >> stage & 1, &s.stop);
                 if (!ok) break;
                 empty ^= 1u << stage;
-                const uint32_t to = smem_addr(s_stages) + stage * Tr::kStageBytes;
+                const uint32_t to = smem_addr(s_stages) + stage * ring.bytes;
                 const uint32_t b_to = to + Tr::kABytes;
                 const bool tail = kOp == kWgrad && has_tail(t.k - k);
                 // a tail's bytes each CTA counts itself, since it clears them; others CTA 0 counts for both
@@ -841,16 +862,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                     last_part &= ~(1u << stage);
                 }
                 ++issued;
-                if (++stage == g.stages) stage = 0;
+                if (++stage == ring.stages) stage = 0;
             }
         }
         ok = ok && tiles.ok;
         if (!ok) give_up(g, s);
         // The last use of every stage is waited for: by its release, or where something gave up, by
         // its bytes, so that no copy and no arrival is on its way when the CTA ends.
-        const int used = issued < static_cast<uint32_t>(g.stages) ? static_cast<int>(issued) : g.stages;
+        const int used = issued < static_cast<uint32_t>(ring.stages) ? static_cast<int>(issued) : ring.stages;
         for (int i = 0; i < used; ++i) {
-            stage = stage == 0 ? g.stages - 1 : stage - 1;
+            stage = stage == 0 ? ring.stages - 1 : stage - 1;
             if (ok && !mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop)) ok = false;
             if (ok) continue;
             if (last_part >> stage & 1)
@@ -864,6 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             const bool leader = elected();
             int stage = 0;
             uint32_t full = 0, ready = 0, slot = 0;
+            const Ring<kOp> ring(g, s);
             constexpr uint32_t kUp = 128 * kBlockK * 2 >> 4;
             const uint32_t first_a = operand_low(smem_addr(s_stages), Tr::kAAcross);
             const uint32_t first_b = operand_low(smem_addr(s_stages) + Tr::kABytes, Tr::kBAcross);
@@ -892,8 +914,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                     if (!ok) break;
                     full ^= 1u << stage;
                     tc_fence_after();
-                    const uint32_t a = first_a + stage * (Tr::kStageBytes >> 4);
-                    const uint32_t b = first_b + stage * (Tr::kStageBytes >> 4);
+                    const uint32_t a = first_a + stage * (ring.bytes >> 4);
+                    const uint32_t b = first_b + stage * (ring.bytes >> 4);
                     if (leader) {
 #pragma unroll
                         for (int j = 0; j < kBlockK / 16; ++j) {
@@ -902,7 +924,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                         }
                         mma_commit_pair(&s.empty[stage]);
                     }
-                    if (++stage == g.stages) stage = 0;
+                    if (++stage == ring.stages) stage = 0;
                 }
                 if (ok && k < t.k) {  // the rest
                     if (kOp == kWgrad && has_tail(t.k - k)) {
@@ -914,7 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                     }
                     if (!ok) break;
                     tc_fence_after();
-                    uint32_t a = first_a + stage * (Tr::kStageBytes >> 4), b = first_b + stage * (Tr::kStageBytes >> 4);
+                    uint32_t a = first_a + stage * (ring.bytes >> 4), b = first_b + stage * (ring.bytes >> 4);
                     if (leader) {
                         for (; k < t.k; k += 16, a += kAStep, b += kBStep) {
                             mma_pair(sums, a, b, desc, k > 0);
@@ -922,7 +944,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                         }
                         mma_commit_pair(&s.empty[stage]);
                     }
-                    if (++stage == g.stages) stage = 0;
+                    if (++stage == ring.stages) stage = 0;
                 }
                 if (!ok) break;
                 if (leader)
@@ -942,6 +964,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         if constexpr (kOp == kWgrad) {
             // k is an expert's rows: what lies behind the last of them in their last 16, other experts'
             // rows or whatever a slab's end holds, is cleared before it is multiplied
+            const Ring<kOp> ring(g, s);
             uint32_t blocks = 0, part = 0;
             bool ok = true;
             while (ok && tiles.next(s, &t)) {
@@ -950,11 +973,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 blocks += static_cast<uint32_t>((t.k + kBlockK - 1) / kBlockK);
                 const int left = t.k % kBlockK;
                 if (!has_tail(left)) continue;
-                const uint32_t stage = (blocks - 1) % static_cast<uint32_t>(g.stages);
+                const uint32_t stage = (blocks - 1) % static_cast<uint32_t>(ring.stages);
                 ok = __all_sync(kFullMask, mbar_wait(&s.part[stage], part >> stage & 1, &s.stop));
                 if (!ok) break;
                 part ^= 1u << stage;
-                unsigned char* const at = s_stages + static_cast<size_t>(stage) * Tr::kStageBytes;
+                unsigned char* const at = s_stages + static_cast<size_t>(stage) * ring.bytes;
                 const int end = (left + 15) / 16 * 16, blocks_here = 2 + (t.n / 2 + 63) / 64;
                 for (int block = 0; block < blocks_here; ++block)
                     for (int line = left + lane / 8; line < end; line += 4)
@@ -969,19 +992,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
     } else {
         const int group = (warp - kFinish) / 4;
         uint32_t slot = 0;
-        // A pass without rows while the first sums are made: it brings the code in, which takes
-        // longer than a small tile itself.
+        // The first pass has no rows, while the first sums are made: it brings the code in, which takes
+        // longer than a small tile itself (and is there once: 16 experts of 1024 x 512, 127 tokens back
+        // through the activation 8.45 us, with a second copy of the code for this pass 9.2).
         Outlet outlet = {s.patch[(warp - kFinish) / 2 * 2 * Tr::kPatches]};
         t = {0, 0, 0, 256, 64, 0, 0, 0};
-        finish_tile<kOp>(g, b16_map, s, t, tmem, tmem, rank, warp, lane, outlet, [] { return true; });
-        while (true) {
-            const bool more = tiles.next(s, &t);
-            if (!group_agrees(tiles.ok, group)) {
-                give_up(g, s);
-                break;
+        for (bool begun = false;; begun = true) {
+            if (begun) {
+                const bool more = tiles.next<true>(s, &t);
+                if (!group_agrees(tiles.ok, group)) {
+                    give_up(g, s);
+                    break;
+                }
+                if (!more) break;
+                if (lane == 0) tiles.taken(s);
             }
-            if (!more) break;
-            if (lane == 0) tiles.taken(s);
             const uint32_t first = slot, slots = slots_of<kOp>(t);
             const auto ready = [&] {
                 if (t.k == 0) return true;
@@ -1046,12 +1071,16 @@ ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& a64, c
     g.epr = g.E / g.R;
     g.inv_epr = 1.0f / static_cast<float>(g.epr);
     const size_t behind = sizeof(Shared<kOp>) + (kOp == kWgrad ? 0 : sizeof(int) * static_cast<size_t>(g.E));
-    g.stages = static_cast<int>((kSmemMost - behind) / Tr::kStageBytes);
-    if (g.stages > kMostStages) g.stages = kMostStages;
+    g.ring = static_cast<uint32_t>((kSmemMost - behind) / 1024 * 1024);
+    g.stages = 0;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t n = g.ring / Traits<kOp>::stage_bytes(i);
+        g.stages |= (n < kMostStages ? n : kMostStages) << 8 * i;
+    }
     const ep_status_t st = ensure_dynamic_smem(ready, expert_kernel<kOp>, static_cast<int>(kSmemMost));
     if (st != EP_OK) return st;
     const dim3 grid(static_cast<unsigned>(sm_count() / 2 * 2));
-    return launch_dependent(expert_kernel<kOp>, grid, dim3(Tr::kThreads), g.stages * Tr::kStageBytes + behind,
+    return launch_dependent(expert_kernel<kOp>, grid, dim3(Tr::kThreads), g.ring + behind,
                             as_stream(stream), a, a64, b64, b16, g);
 }
 
