@@ -115,3 +115,25 @@ def test_wgrad(counts, R, M, H, F):
         ep.ep_expert_wgrad(dout, x, rows.offsets, dw, status)
         check_wgrad(dout, x, rows, dw)
     flags(rows, status)
+
+
+# One round of tiles takes them 32 rows high, then 64, 128 and 256, with as many stages as fit.
+@pytest.mark.parametrize("counts", [[40], [1100], [2300], [4600], [5000], [900, 700], [33, 1, 65, 200]],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_tiles_of_every_height(counts):
+    H, F = 1544, 512
+    rows, status = Rows(counts, 1, sum(counts) + 3), zero_status()
+    (w13, w2), x = weights(rows.E, H, F), slab(rows, 1, H)
+    h, q, s = out(rows, F), out(rows, 2 * F, torch.float8_e4m3fn), out(rows, 2 * F // 128)
+    ep.ep_expert_gate_up(x, w13, rows.offsets, ACTS["silu"], h, None, q, s, status)
+    check_gate_up(x, w13, rows, "silu", h, None, q, s)
+    a, y = slab(rows, 2, F), out(rows, H)
+    ep.ep_expert_down(a, w2, rows.offsets, y, status)
+    check_down(a, w2, rows, y)
+    dy, pre, dpre = slab(rows, 3, H, 0.1), slab(rows, 4, 2 * F, 3.0), out(rows, 2 * F)
+    ep.ep_expert_down_bwd(dy, w2, pre, None, None, rows.offsets, ACTS["silu"], dpre, None, status)
+    check_down_bwd(dy, w2, pre, rows, "silu", dpre)
+    d, dx = slab(rows, 5, 2 * F, 0.1), out(rows, H)
+    ep.ep_expert_gate_up_bwd(d, w13, rows.offsets, dx, status)
+    check_gate_up_bwd(d, w13, rows, dx)
+    flags(rows, status)
