@@ -1124,7 +1124,7 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
     g.out_q = pre_q;
     g.out_scales = static_cast<uint16_t*>(pre_scales);
     g.status = status;
-    const int few_at_once = pre == nullptr && pre_q == nullptr ? few_rows_at_once(E, R, max_rows, true) : 0;
+    const int few_at_once = pre == nullptr && pre_q == nullptr ? few_rows_at_once(E, R, max_rows, 1ll * H * F, true) : 0;
     if (few_at_once > 0) return launch_few_rows(few(g, x, w_gate_up), true, few_at_once, stream);
     CUtensorMap a, a64, b64, b16;
     ep_status_t st = map_of(&a, w_gate_up, H, F, 2ull * E, 128);
@@ -1148,7 +1148,7 @@ ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* exp
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(y);
     g.status = status;
-    const int few_at_once = few_rows_at_once(E, R, max_rows, false);
+    const int few_at_once = few_rows_at_once(E, R, max_rows, 1ll * H * F, false);
     if (few_at_once > 0) return launch_few_rows(few(g, h, w_down), false, few_at_once, stream);
     CUtensorMap a, a64, b64, b16;
     ep_status_t st = map_of(&a, w_down, F, H, E, 128);

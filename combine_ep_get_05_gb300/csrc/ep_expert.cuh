@@ -18,16 +18,20 @@ struct FewRows {
 ep_status_t launch_few_rows(const FewRows& g, bool gated, int at_once, void* stream);
 
 // Rows of an expert that the kernel for few rows takes at once (8, 16 or 32), 0 where the general
-// one is the faster, by what the slabs can hold: an expert's rows are known to the GPU only. us, few
-// against general. Slabs of up to 4 rows an expert: 256 experts of 7168 x 2048, one token 71.8
-// against 76.5 (gated) and 36.6 against 41, four tokens 259 against 284 and 127 against 138; 64 of
-// 2048 x 1024, 16 tokens 55.1 against 62.6 and 29.1 against 32.6. Of 5 or 6 and up, gated, 16 at once:
-// 16 of 1024 x 512 with 4 rows each 10.3 against 11.8, 32 of 4096 x 2048 158 against 166, but 256 of
-// 7168 x 2048 in slabs of 8 rows an expert, half filled, 2175 against 2126; not gated 88.6 against
-// 85.5. One expert of 7168 x 2048: 8 rows 12.2 against 40 and 8.2 against 12.3, 16 rows 13.4 and 9.5,
-// 32 rows, 32 at once, 16.8 and 12.7, 64 rows 30.4 and 22, 96 rows 44 and 31. Slabs of more than 64
-// rows stay with the general kernel whatever E: all of them may be one expert's.
-int few_rows_at_once(int E, int R, int max_rows, bool gated);
+// one is the faster, by what the slabs can hold (an expert's rows are known to the GPU only) and an
+// expert's `weights`, H F. us, few against general, gated and not.
+//   8 at once: 256 experts of 7168 x 2048, two tokens 131 against 135 and 65 against 68, eight 494 against
+//   516 and 240 against 246; 2 rows an expert on average (room for 4) of 32 of 4096 x 2048 141 against 157
+//   and 73 against 78, of 256 of 7168 x 2048 1872 against 1830 and 907 against 910.
+//   16: three of 7168 x 2048, 16 rows, 33 against 37 and 19 against 22. In slabs of 5 rows an expert the
+//   general one: 64 of 2048 x 1024 90 against 84 and 57 against 43.
+//   32: one of 7168 x 2048, 32 rows, 16.7 against 30.7 but 12.2 against 9.3; of 2048 x 1024 6.3 against 10.2
+//   and 4.5 against 5.8, 64 rows 11.1 against 10.3 and 7.4 against 6.0.
+//   16, few experts of little weight: four of 2048 x 1024, 16 rows each, 9.2 against 12.6 and 6.3 against
+//   7.1, two of them 48 and 16 rows 11.6 against 11.8 and 6.9 against 6.5; sixteen of 1024 x 512, 64 rows,
+//   10.0 alike and 7.3 against 6.7.
+// Slabs of more than 64 rows stay with the general kernel whatever E: all of them may be one expert's.
+int few_rows_at_once(int E, int R, int max_rows, long long weights, bool gated);
 
 // The rows [first, first + count) of an expert in the slabs seen as one array of rows.
 struct ExpertRows {

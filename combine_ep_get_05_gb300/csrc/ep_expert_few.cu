@@ -247,11 +247,13 @@ ep_status_t launch(const FewRows& g, void* stream) {
 
 namespace ep {
 
-int few_rows_at_once(int E, int R, int max_rows, bool gated) {
-    const long long all = static_cast<long long>(R) * max_rows;
-    if (max_rows <= 8 || (all <= 4ll * E && max_rows <= 64)) return 8;
-    if (max_rows > 16 && E <= 2 && max_rows <= (gated ? 64 : 32)) return 32;
-    if (max_rows <= 16 || (gated && all <= 6ll * E && max_rows <= 64)) return 16;
+int few_rows_at_once(int E, int R, int max_rows, long long weights, bool gated) {
+    const long long all = static_cast<long long>(R) * max_rows, total = E * weights;
+    if (max_rows <= 8) return 8;
+    if (max_rows <= 64 && all <= 4ll * E && (!gated || all <= E || total <= 512 << 20)) return 8;
+    if (E <= 3 && max_rows <= 16) return 16;
+    if (E <= 2 && max_rows <= 32 && (gated || weights <= 4 << 20)) return 32;
+    if (E <= 8 && max_rows <= 64 && all <= 16ll * E && total <= 8 << 20) return 16;
     return 0;
 }
 

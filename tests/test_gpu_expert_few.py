@@ -35,13 +35,16 @@ CASES = [
     ([16], 1, 16, 136, 264),
     ([17], 1, 17, 136, 264),            # 32 at once
     ([29, 4], 1, 32, 520, 104),         # dropped rows
-    ([50], 1, 64, 264, 48),             # two passes; down: the general kernel
+    ([50], 1, 64, 264, 48),             # the general kernel
+    ([20], 1, 24, 4096, 1032),          # 32 at once; down, heavier: the general kernel
+    ([11, 0, 48, 5], 1, 64, 520, 104),  # light: sixteen at once, three passes
     ([65], 1, 65, 136, 264),            # the general kernel
     ([3, 0, 12, 1], 1, 16, 2048, 80),
+    ([9, 0, 7], 1, 16, 1032, 200),      # sixteen at once
     ([20, 0, 0, 0], 4, 16, 72, 40),     # dropped rows
     ([0, 0, 0, 0, 0, 0, 0, 64], 8, 64, 264, 48),   # general: 512 rows of room
     ([30, 0, 1, 0, 2, 0, 0, 1], 1, 34, 264, 48),   # several passes of eight
-    ([1, 9, 8, 16, 0, 2, 3, 5], 1, 44, 264, 48),   # gated: sixteen at once; down: general
+    ([1, 9, 8, 16, 0, 2, 3, 5], 1, 44, 264, 48),   # sixteen at once
     ([0] * 16, 4, 4, 64, 64),
     ([1] * 152 + [2] * 152, 16, 64, 64, 16),       # more units than CTAs, one slice each
     ([2, 0, 1] * 64, 1, 192, 1024, 8),
