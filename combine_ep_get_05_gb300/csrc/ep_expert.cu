@@ -157,9 +157,9 @@ __device__ __forceinline__ int row_tiles(int count, int choice) {
 // The choice for one expert. A gated tile of more than 128 rows has all of tensor memory, and its sums
 // are finished before the next one's can begin; two of 128 rows take turns, but read the weights
 // twice (from L2). Short sums cost less than their finish, so they take turns. us with tiles of up to
-// 128 rows, of up to 256 (F = 2048, the 8-bit checkpoint): 16 experts of 2048 rows, H = 512 138, 191,
-// 1024 194, 259, 2048 346, 390; 256 of 128 rows, H = 512 213, 244, 1024 381, 390, 2048 738, 720, 3584
-// 1276, 1226; 128 uneven ones of H = 4096 alike, 256 of 128 rows, H = 7168 2505, 2355.
+// 128 rows, of up to 256, 16 experts of 2048 rows, F = 2048, the 8-bit checkpoint: H = 512 129, 175, 1024
+// 187, 241, 2048 331, 366, 4096 635, 633; 128 uneven ones of H = 4096 alike, 256 of 128 rows on average,
+// H = 7168 2505, 2355.
 template <int kOp>
 __device__ __forceinline__ int choice_of(const ExpertArgs& g, int count, int choice) {
     const bool turns = g.K <= 1024 || (g.K <= 2048 && count > kMostN);
