@@ -68,11 +68,15 @@ __device__ __forceinline__ float sigmoid_of(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
     return s;
 }
-// act'(v) from act(v) and the sigmoid
+// act'(v) from act(v) and the sigmoid. What fades, v * (1 - s), is formed before what grows, p': from
+// v = 17 on (5 in GELU) s is 1 and the product 0, while v * p' overflows from 1.2e13 on. p' itself stops
+// growing at 10^4, long after s or 1 - s is 0, so that neither meets an infinity.
 template <bool kGelu>
 __device__ __forceinline__ float slope_of(float v, float act, float s) {
-    const float q = kGelu ? act * fmaf(3.0f * kGeluA * kGeluB, v * v, kGeluA) : act;
-    return s + fmaf(-q, s, q);
+    const float fading = act * (1.0f - s);
+    if (!kGelu) return fading + s;
+    const float c = fminf(fabsf(v), 1e4f);
+    return fmaf(fading, fmaf(3.0f * kGeluA * kGeluB, c * c, kGeluA), s);
 }
 
 // bf16_rn(amax / 448), 0 below 2^-100 (so that its reciprocal is finite)

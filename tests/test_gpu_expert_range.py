@@ -1,0 +1,78 @@
+"""The experts' activations and their gradients over the whole range of bf16: gates far from zero.
+
+One channel of dy selects what a sum is: every other product is zero, so that sums are exact."""
+import pytest
+import torch
+
+import combine_ep_get_05_gb300 as ep
+from expert_cases import ACTS, BF16, Rows, act_of, decode, out
+
+pytestmark = pytest.mark.gpu
+
+# sigmoid: a few 2^-22 from the fast power and reciprocal, and p's own roundings, three of 2^-24 |p| with
+# |p| < 110 where the result is no zero: below 2^-15 in all. Half a step of bf16's smallest numbers is 2^-134.
+NEAR = BF16 + 2.0 ** -14
+SMALLEST = 2.0 ** -134
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ep.build_library()
+
+
+def bf(values):
+    return torch.tensor(values, dtype=torch.float64).to(torch.bfloat16).cuda()
+
+
+def near(got, want, what):
+    got, want = got.double(), want.double()
+    assert bool(torch.isfinite(got).all()), (what, got)
+    over = (got - want).abs() - (NEAR * want.abs() + SMALLEST)
+    i = int(over.argmax())
+    assert float(over.max()) <= 0, (what, float(got.flatten()[i]), float(want.flatten()[i]))
+
+
+FAR = [s * v for v in (0.0, 30.0, 1e4, 1.2e13, 1e15, 1.8e19, 2e19, 1e30, 3e38) for s in (1, -1)]
+
+
+def gradients(gates, ups, act, eight=None):
+    """dgate, dup and h where dh is 1: a row, all of whose channels are given."""
+    F = gates.shape[-1]
+    rows = Rows([1], 1, 1)
+    dy = torch.zeros((1, 1, 8), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((1, 8, F), dtype=torch.bfloat16, device="cuda")
+    dy[0, 0, 0], w[0, 0] = 1.0, 1.0
+    dpre, h = out(rows, 2 * F), out(rows, F)
+    if eight is None:
+        pre, q, s = torch.cat([gates, ups])[None, None].contiguous(), None, None
+    else:
+        pre, (q, s) = None, eight
+    ep.ep_expert_down_bwd(dy, w, pre, q, s, rows.offsets, ACTS[act], dpre, h)
+    return dpre[0, 0, :F], dpre[0, 0, F:], h[0, 0]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradient_at_gates_far_from_zero(act):
+    gates = bf(FAR + [0.0] * (-len(FAR) % 8))
+    dgate, dup, h = gradients(gates, torch.ones_like(gates), act)
+    v, dv = act_of(act, gates.double())
+    near(dgate, dv, "dgate")
+    near(dup, v, "dup")
+    near(h, v, "h")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("scale", [2.0 ** 40, 2.0 ** 60, 2.0 ** 118])
+def test_gradient_at_gates_far_from_zero_from_the_8_bit_checkpoint(act, scale):
+    q = torch.zeros((1, 1, 256), device="cuda")
+    q[0, 0, :128] = torch.arange(128, device="cuda") - 64
+    q[0, 0, 128:] = 1.0
+    q, s = q.to(torch.float8_e4m3fn), bf([[[scale, 1.0]]])
+    gates = decode(q, s)[0, 0, :128]
+    dgate, dup, h = gradients(gates, None, act, (q, s))
+    v, dv = act_of(act, gates)
+    near(dgate, dv, "dgate")
+    near(dup, v, "dup")
+    near(h, v, "h")
