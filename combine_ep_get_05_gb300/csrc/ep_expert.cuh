@@ -54,21 +54,23 @@ __device__ __forceinline__ ExpertRows expert_rows(const int32_t* offsets, int e,
 }
 
 // act(v) = v * s, s = sigmoid(p(v)); both activations are of this form, so that their derivative is
-// s + v * s * (1 - s) * p'(v). The sigmoid is 1 / (1 + 2^(-p log2 e)) by the GPU's fast power and
-// reciprocal (a few 2^-22 relative each, the exponent's rounding |p| 2^-24 more): what comes out is
-// rounded to bf16. The power is infinite where p < -88, and its reciprocal 0: the right limit.
-constexpr float kLog2e = 1.4426950408889634f;
+// s + v * s * (1 - s) * p'(v). The sigmoid is 1 / (1 + e), e = 2^(-p log2 e), by the GPU's fast power and
+// reciprocal (a few 2^-22 relative each, the exponent's rounding, max(|p|, 11) 2^-24, more): what comes out
+// is rounded to bf16. The sum is made times 2^-16, so that neither it nor its reciprocal leaves fp32's
+// range before v * s falls below bf16's smallest number, at p = -98 (1 + e alone overflows from -88 on, where
+// v * s is still a normal number).
+constexpr float kLog2e = 1.4426950408889634f, kSumExponent = -16.0f, kSumScale = 0x1p-16f;
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // p(v) = A (v + B v^3), A = 2 sqrt(2 / pi)
 
 template <bool kGelu>
 __device__ __forceinline__ float sigmoid_of(float v) {
-    const float m = kGelu ? v * fmaf(-kGeluA * kGeluB * kLog2e, v * v, -kGeluA * kLog2e) : v * -kLog2e;
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-    return s;
+    const float m = kGelu ? fmaf(-kGeluA * kGeluB * kLog2e, v * v, -kGeluA * kLog2e) : -kLog2e;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(v, m, kSumExponent)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + kSumScale));
+    return r * kSumScale;
 }
-// act'(v) from act(v) and the sigmoid. What fades, v * (1 - s), is formed before what grows, p': from
+// act'(v) from act(v) and the sigmoid. What fades, v * s * (1 - s), is formed before what grows, p': from
 // v = 17 on (5 in GELU) s is 1 and the product 0, while v * p' overflows from 1.2e13 on. p' itself stops
 // growing at 10^4, long after s or 1 - s is 0, so that neither meets an infinity.
 template <bool kGelu>

@@ -1,6 +1,9 @@
-"""The experts' activations and their gradients over the whole range of bf16: gates far from zero.
+"""The experts' activations and their gradients over the whole range of bf16: gates far
+from zero, outputs near the smallest numbers.
 
-One channel of dy selects what a sum is: every other product is zero, so that sums are exact."""
+One channel of x, or of dy, selects what a sum is: every other product is zero, so that sums are exact."""
+import math
+
 import pytest
 import torch
 
@@ -76,3 +79,43 @@ def test_gradient_at_gates_far_from_zero_from_the_8_bit_checkpoint(act, scale):
     near(dgate, dv, "dgate")
     near(dup, v, "dup")
     near(h, v, "h")
+
+
+def act_below(name, v):
+    """The same as act_of, for v far below zero, where 1 + tanh(u) cancels in 64 bits, too: it is 2 sigmoid(2u)."""
+    a = 2 * math.sqrt(2 / math.pi)
+    p, dp = (v, 1.0) if name == "silu" else (a * (v + 0.044715 * v ** 3), a * (1 + 3 * 0.044715 * v * v))
+    s, rest = 1 / (1 + torch.exp(-p)), 1 / (1 + torch.exp(p))
+    return v * s, s + v * s * rest * dp
+
+
+# p(v) from about -80 to -104: the activation falls to bf16's smallest number
+LOW = {"silu": [-80 - 0.5 * i for i in range(48)], "gelu": [-9.5 - i / 16 for i in range(24)]}
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("path", ["few", "general", "8bit"])
+def test_activation_down_to_the_smallest_numbers(act, path):
+    gates = bf(LOW[act])
+    n, F = len(gates), 128
+    rows = Rows([n], 1, 64 if path == "few" else n)
+    x = torch.zeros((1, rows.max_rows, 8), dtype=torch.bfloat16, device="cuda")
+    x[0, :n, 0], x[0, :n, 1] = gates, 1.0
+    w = torch.zeros((1, 2 * F, 8), dtype=torch.bfloat16, device="cuda")
+    w[0, :F, 0], w[0, F:, 1] = 1.0, 1.0
+    h = out(rows, F)
+    pre = out(rows, 2 * F) if path == "general" else None
+    q, s = (out(rows, 2 * F, torch.float8_e4m3fn), out(rows, 2)) if path == "8bit" else (None, None)
+    ep.ep_expert_gate_up(x, w, rows.offsets, ACTS[act], h, pre, q, s)
+    v, _ = act_below(act, gates.double())
+    near(h[0, :n], v[:, None].expand(n, F), "h")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradient_down_to_the_smallest_numbers(act):
+    gates = bf(LOW[act])
+    dgate, dup, h = gradients(gates, torch.ones_like(gates), act)
+    v, dv = act_below(act, gates.double())
+    near(dup, v, "dup")
+    near(h, v, "h")
+    near(dgate, dv, "dgate")
