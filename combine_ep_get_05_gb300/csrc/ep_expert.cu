@@ -95,10 +95,16 @@ struct Planned {
     int scan[4][32];  // of the plan: a warp's tiles, for each choice
 };
 
+// The reciprocals of the scales of 16 rows' gates and, from 16 on, up-projections, a warp's own.
+struct Reciprocals {
+    float high[2 * kChunk], low[2 * kChunk];
+};
+
 template <int kOp>
 struct Shared : Planned {  // behind the stages
     alignas(1024) unsigned char patch[kFinishWarps * Traits<kOp>::kPatches][kPatchBytes];
     float amax[kOp == kGateUp ? kGroups * 2 * 4 : 1][2 * kChunk];  // [group, buffer, warp][gate and up]
+    alignas(8) Reciprocals rcp[kOp == kGateUp ? kFinishWarps : 1];
     int prefix[1];  // [E + 1] tiles of rows before each expert's (but kWgrad)
 };
 
@@ -352,31 +358,29 @@ __device__ __forceinline__ void pack(uint32_t (&w)[8], const float (&v)[16]) {
         }
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+// codes of v0, v1 by their reciprocals
+__device__ __forceinline__ uint32_t pair_codes(float v0, float v1, const float2& high, const float2& low) {
+    float q0, q1;
+    asm("{\n .reg .b64 v, h, l;\n mov.b64 v, {%2, %3};\n mov.b64 h, {%4, %5};\n mov.b64 l, {%6, %7};\n"
+        " mul.rn.f32x2 l, v, l;\n fma.rn.f32x2 v, v, h, l;\n mov.b64 {%0, %1}, v;\n}\n"
+        : "=f"(q0), "=f"(q1)
+        : "f"(v0), "f"(v1), "f"(high.x), "f"(high.y), "f"(low.x), "f"(low.y));
+    return pack_e4m3x2_rn_sat(q0, q1);
 }
-__device__ __forceinline__ uint32_t codes_of_f16x2(uint32_t two) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(two));
-    return r;
-}
-
-// Codes of 16 rows of one block of 128 channels, of which the warp has 32; rcp: lane j has row j's.
-// The quotients go through the patch as fp16, whose 11 bits leave the rounding to 4 as it is but
-// beside a midpoint of codes (by 2^-12 of the value).
-__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const float (&v)[16], float rcp,
-                                            const Window& win, uint32_t patch, int lane) {
+// Codes of 16 rows of one block of 128 channels, of which the warp has 32, by the reciprocals from `side`
+// on. They go through the patch as 16-bit values.
+__device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const float (&v)[16], const Reciprocals& rcp,
+                                            int side, const Window& win, uint32_t patch, int lane) {
     uint32_t w[8];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const float r0 = __shfl_sync(kFullMask, rcp, 8 * q + lane % 4 * 2);
-        const float r1 = __shfl_sync(kFullMask, rcp, 8 * q + lane % 4 * 2 + 1);
+        const int row = side + 8 * q + lane % 4 * 2;  // and the next
+        const float2 high = *reinterpret_cast<const float2*>(rcp.high + row);
+        const float2 low = *reinterpret_cast<const float2*>(rcp.low + row);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int i = fragment(q, b);
-            w[4 * q + b] = pack_f16x2_rn(v[i] * r0, v[i + 1] * r1);
+            w[4 * q + b] = __byte_perm(pair_codes(v[i], v[i + 1], high, low), 0, 0x4140);
         }
     }
     __syncwarp();
@@ -385,10 +389,9 @@ __device__ __forceinline__ void store_codes(uint8_t* to, size_t stride, const fl
     to += lane / 4 * stride + lane % 4 * 8;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const uint4 f = ld_shared_v4(row_place(patch, q, lane));
-        const uint32_t a = codes_of_f16x2(f.x) | codes_of_f16x2(f.y) << 16;
-        const uint32_t b = codes_of_f16x2(f.z) | codes_of_f16x2(f.w) << 16;
-        if (win.has(q, lane)) st_v2(to + 8 * q * stride, a, b);
+        const uint4 c = ld_shared_v4(row_place(patch, q, lane));
+        if (win.has(q, lane))
+            st_v2(to + 8 * q * stride, __byte_perm(c.x, c.y, 0x6420), __byte_perm(c.z, c.w, 0x6420));
     }
 }
 __device__ __forceinline__ void load_codes(uint4 (&v)[2], const uint8_t* from, size_t stride, const Window& win,
@@ -619,21 +622,18 @@ __device__ __forceinline__ bool finish_tile(const ExpertArgs& g, const CUtensorM
                 column_max(amax[quarter], v, lane);
                 column_max(amax[quarter] + kChunk, up, lane);
                 asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
-                float a = 0.0f, b = 0.0f;
+                float a = 0.0f;  // lanes 0 .. 15 have the gate's rows, 16 .. 31 the up-projection's
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a = fmaxf(a, amax[i][lane % kChunk]);
-                    b = fmaxf(b, amax[i][kChunk + lane % kChunk]);
-                }
+                for (int i = 0; i < 4; ++i) a = fmaxf(a, amax[i][lane]);
                 a = checkpoint_scale(a);
-                b = checkpoint_scale(b);
-                if (quarter == 0 && lane < kChunk && lane < win.rows && win.channels > 0) {
-                    uint16_t* const scales = g.out_scales + (row + lane) * (2 * C / 128) + channel / 128;
-                    scales[0] = static_cast<uint16_t>(__float_as_uint(a) >> 16);
-                    scales[C / 128] = static_cast<uint16_t>(__float_as_uint(b) >> 16);
-                }
-                store_codes(g.out_q + row * 2 * C + channel, 2 * C, v, checkpoint_rcp(a), win, patch, lane);
-                store_codes(g.out_q + row * 2 * C + C + channel, 2 * C, up, checkpoint_rcp(b), win, patch, lane);
+                if (quarter == 0 && lane % kChunk < win.rows && win.channels > 0)
+                    g.out_scales[(row + lane % kChunk) * (2 * C / 128) + lane / kChunk * (C / 128) + channel / 128] =
+                        static_cast<uint16_t>(__float_as_uint(a) >> 16);
+                Reciprocals& rcp = s.rcp[warp - kFinish];
+                checkpoint_rcp(a, rcp.high[lane], rcp.low[lane]);
+                __syncwarp();
+                store_codes(g.out_q + row * 2 * C + channel, 2 * C, v, rcp, 0, win, patch, lane);
+                store_codes(g.out_q + row * 2 * C + C + channel, 2 * C, up, rcp, kChunk, win, patch, lane);
             }
             if (g.act == EP_ACT_GELU)
                 activate<true>(v, up);

@@ -574,8 +574,8 @@ ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, co
  * and, for the gradient, a checkpoint of c = (gate | up), 2F channels a row, in one of two forms:
  *   pre[r][p][j]        = bf16_rn(c[j])
  *   pre_scales[r][p][b] = bf16_rn(max |c| over the 128 channels of block b / 448)
- *   pre_q[r][p][j]      = e4m3(c[j] / pre_scales[r][p][b])   (rounded to nearest even by way of
- *                         fp16, saturated)
+ *   pre_q[r][p][j]      = e4m3(c[j] / pre_scales[r][p][b])   (the quotient rounded once, to nearest
+ *                         even, saturated)
  * A block whose scale would be below 2^-100 has scale 0 and zero codes; a NaN becomes a NaN code
  * and takes no part in the maximum; a block with an infinity has scale infinity, zeros, and NaN
  * for the infinities.

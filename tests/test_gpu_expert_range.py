@@ -1,5 +1,5 @@
-"""The experts' activations and their gradients over the whole range of bf16: gates far
-from zero, outputs near the smallest numbers.
+"""The experts' activations, their gradients and the 8-bit checkpoint over the whole range of bf16: gates far
+from zero, outputs near the smallest numbers, quotients beside the midpoints of codes.
 
 One channel of x, or of dy, selects what a sum is: every other product is zero, so that sums are exact."""
 import math
@@ -119,3 +119,51 @@ def test_gradient_down_to_the_smallest_numbers(act):
     near(dup, v, "dup")
     near(h, v, "h")
     near(dgate, dv, "dgate")
+
+
+def midpoints():
+    """Halfway between neighbouring codes from 2^-9 on, ten bits of mantissa and fewer."""
+    codes = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    return (codes[1:] + codes[:-1]) / 2
+
+
+def checkpoint_of(scales, nudge, least=0.0):
+    """Rows whose blocks have the scales, and values at midpoints times them, plus nudge of that size."""
+    m = midpoints()
+    m = m[m >= least]
+    F, n = 128, len(scales)
+    w = torch.zeros((1, 2 * F, 8), dtype=torch.float64)
+    w[0, :len(m), 0] = m
+    w[0, :len(m), 1] = m
+    w[0, F:F + len(m), 0] = -m
+    w[0, F:F + len(m), 1] = -m
+    w[0, 127, 0], w[0, 255, 0] = 448.0, -448.0
+    x = torch.zeros((1, n, 8), dtype=torch.float64)
+    x[0, :, 0] = scales
+    x[0, :, 1] = scales.sign() * torch.exp2(torch.floor(torch.log2(scales))) * nudge
+    assert bool((x == x.to(torch.bfloat16).double()).all()) and bool((w == w.to(torch.bfloat16).double()).all())
+    c = torch.einsum("rh,ch->rc", x[0], w[0])
+    assert bool((c == c.float().double()).all())
+    rows = Rows([n], 1, n)
+    h, q, s = out(rows, F), out(rows, 2 * F, torch.float8_e4m3fn), out(rows, 2)
+    ep.ep_expert_gate_up(x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda(), rows.offsets, 0, h, None, q, s)
+    return c, q[0].cpu(), s[0].cpu().double()
+
+
+def codes_of(c, scales):
+    """E4M3 of the exact quotients: c has 24 bits and a scale 8, so c / scale is exactly a midpoint or farther
+    from it than half a step of fp32, and to round it to fp32 first changes no code."""
+    q = c / scales.repeat_interleave(128, dim=1)
+    return q.clamp(-448, 448).float().to(torch.float8_e4m3fn)
+
+
+MANTISSAS = 1.0 + torch.arange(128, dtype=torch.float64) / 128
+
+
+@pytest.mark.parametrize("exponent", [0, -20, -60, 100])
+@pytest.mark.parametrize("nudge", [0.0, 2.0 ** -11, -2.0 ** -11, 2.0 ** -13, -2.0 ** -13, 2.0 ** -15, -2.0 ** -15])
+def test_codes_are_rounded_once(nudge, exponent):
+    scales = MANTISSAS * 2.0 ** exponent
+    c, q, s = checkpoint_of(scales, nudge)
+    assert torch.equal(s, scales[:, None].expand(-1, 2))
+    assert torch.equal(q.view(torch.uint8), codes_of(c, s).view(torch.uint8))
