@@ -81,10 +81,11 @@ __device__ __forceinline__ float slope_of(float v, float act, float s) {
     return fmaf(fading, fmaf(3.0f * kGeluA * kGeluB, c * c, kGeluA), s);
 }
 
-// bf16_rn(amax / 448), 0 below 2^-100 (so that its reciprocal is finite)
+// bf16_rn(amax / 448), 0 below 2^-117, where the smallest code, 2^-9, would stand for less than fp32's
+// smallest normal number
 __device__ __forceinline__ float checkpoint_scale(float amax) {
     const float scale = bf16_lo(pack_bf16x2_rn(__fdiv_rn(amax, 448.0f), 0.0f));
-    return scale < 0x1p-100f ? 0.0f : scale;
+    return scale < 0x1p-117f ? 0.0f : scale;
 }
 // 1 / scale in two parts, good to 2^-46 together: what a block's values are multiplied by before they become
 // codes. v * high + (v * low), rounded once by the fused multiply-add, is v / scale where that is a midpoint

@@ -576,9 +576,9 @@ ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, co
  *   pre_scales[r][p][b] = bf16_rn(max |c| over the 128 channels of block b / 448)
  *   pre_q[r][p][j]      = e4m3(c[j] / pre_scales[r][p][b])   (the quotient rounded once, to nearest
  *                         even, saturated)
- * A block whose scale would be below 2^-100 has scale 0 and zero codes; a NaN becomes a NaN code
- * and takes no part in the maximum; a block with an infinity has scale infinity, zeros, and NaN
- * for the infinities.
+ * A block whose scale would be below 2^-117 (a code, 2^-9 at least, times a scale is a normal number)
+ * has scale 0 and zero codes; a NaN becomes a NaN code and takes no part in the maximum; a block with
+ * an infinity has scale infinity, zeros, and NaN for the infinities.
  *   x bf16 [R][max_rows][H]; h bf16 [R][max_rows][F]; pre bf16 [R][max_rows][2F] or NULL;
  *   pre_q uint8 [R][max_rows][2F] and pre_scales bf16 [R][max_rows][2F/128]: both or neither,
  *   F % 128 == 0 with them. Either checkpoint, both or none. One launch. */

@@ -1,5 +1,5 @@
 """The experts' activations, their gradients and the 8-bit checkpoint over the whole range of bf16: gates far
-from zero, outputs near the smallest numbers, quotients beside the midpoints of codes.
+from zero, outputs near the smallest numbers, quotients beside the midpoints of codes, small scales.
 
 One channel of x, or of dy, selects what a sum is: every other product is zero, so that sums are exact."""
 import math
@@ -167,3 +167,18 @@ def test_codes_are_rounded_once(nudge, exponent):
     c, q, s = checkpoint_of(scales, nudge)
     assert torch.equal(s, scales[:, None].expand(-1, 2))
     assert torch.equal(q.view(torch.uint8), codes_of(c, s).view(torch.uint8))
+
+
+@pytest.mark.parametrize("exponent", [-92, -101, -116, -117])
+@pytest.mark.parametrize("nudge", [0.0, 2.0 ** -8, -2.0 ** -8])
+def test_codes_of_small_scales(nudge, exponent):
+    """Down to 2^-117, where the smallest code, 2^-9, stands for fp32's smallest normal number."""
+    scales = MANTISSAS * 2.0 ** exponent
+    c, q, s = checkpoint_of(scales, nudge, least=1.0)
+    assert torch.equal(s, scales[:, None].expand(-1, 2))
+    assert torch.equal(q.view(torch.uint8), codes_of(c, s).view(torch.uint8))
+
+
+def test_blocks_below_the_smallest_scale_are_zeros():
+    c, q, s = checkpoint_of(MANTISSAS * 2.0 ** -118, 0.0, least=1.0)
+    assert not s.any() and not q.float().any()
