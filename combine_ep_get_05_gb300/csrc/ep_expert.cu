@@ -1084,6 +1084,21 @@ ep_status_t launch(ExpertArgs g, const CUtensorMap& a, const CUtensorMap& a64, c
                             as_stream(stream), a, a64, b64, b16, g);
 }
 
+// Slabs without any rows: all that is left of a call is the flag, if an expert has rows.
+__global__ void no_room_kernel(const int32_t* offsets, int E, int epr, float inv_epr, int32_t* status) {
+    allow_dependents();
+    grid_dependency_wait();
+    for (int e = static_cast<int>(threadIdx.x); e < E; e += static_cast<int>(blockDim.x))
+        if (expert_rows(offsets, e, epr, inv_epr, 0).dropped) raise_flag(status, EP_FLAG_CAPACITY);
+}
+ep_status_t no_room(const int32_t* offsets, int E, int R, int32_t* status, void* stream) {
+    if (status == nullptr) return EP_OK;
+    if (offsets == nullptr || !aligned16(offsets)) return EP_ERR_INVALID;
+    const int epr = E / R;
+    return launch_dependent(no_room_kernel, dim3(1), dim3(256), 0, as_stream(stream), offsets, E, epr,
+                            1.0f / static_cast<float>(epr), status);
+}
+
 FewRows few(const ExpertArgs& g, const void* x, const void* w) {
     return {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), g.offsets, g.act, g.C, g.K, g.E,
             g.max_rows, g.E / g.R, 1.0f / static_cast<float>(g.E / g.R), g.out, g.status};
@@ -1106,7 +1121,7 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
     if (!valid(E, R, max_rows) || !valid_width(H, kMostWidth) || !valid_width(F, kMostWidth)) return EP_ERR_INVALID;
     if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID;
     if ((pre_q == nullptr) != (pre_scales == nullptr) || (pre_q != nullptr && F % 128 != 0)) return EP_ERR_INVALID;
-    if (max_rows == 0) return EP_OK;
+    if (max_rows == 0) return no_room(expert_offsets, E, R, status, stream);
     if (x == nullptr || w_gate_up == nullptr || expert_offsets == nullptr || h == nullptr) return EP_ERR_INVALID;
     if (!aligned16(x) || !aligned16(w_gate_up) || !aligned16(expert_offsets) || !aligned16(h) ||
         !aligned16_or_null(pre) || !aligned16_or_null(pre_q) || !aligned16_or_null(pre_scales))
@@ -1136,7 +1151,7 @@ ep_status_t ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_
 ep_status_t ep_expert_down(const void* h, const void* w_down, const int32_t* expert_offsets, int32_t H, int32_t F,
                            int32_t E, int32_t R, int32_t max_rows, void* y, int32_t* status, void* stream) {
     if (!valid(E, R, max_rows) || !valid_width(H, kMostWidth) || !valid_width(F, kMostWidth)) return EP_ERR_INVALID;
-    if (max_rows == 0) return EP_OK;
+    if (max_rows == 0) return no_room(expert_offsets, E, R, status, stream);
     if (h == nullptr || w_down == nullptr || expert_offsets == nullptr || y == nullptr) return EP_ERR_INVALID;
     if (!aligned16(h) || !aligned16(w_down) || !aligned16(expert_offsets) || !aligned16(y)) return EP_ERR_INVALID;
     ExpertArgs g = {};
@@ -1164,7 +1179,7 @@ ep_status_t ep_expert_down_bwd(const void* dy, const void* w_down, const void* p
     if (!valid(E, R, max_rows) || !valid_width(H, kMostWidth) || !valid_width(F, kMostWidth)) return EP_ERR_INVALID;
     if (act != EP_ACT_SILU && act != EP_ACT_GELU) return EP_ERR_INVALID;
     if ((pre_q == nullptr) != (pre_scales == nullptr) || (pre_q != nullptr && F % 128 != 0)) return EP_ERR_INVALID;
-    if (max_rows == 0) return EP_OK;
+    if (max_rows == 0) return no_room(expert_offsets, E, R, status, stream);
     if ((pre == nullptr) == (pre_q == nullptr)) return EP_ERR_INVALID;
     if (dy == nullptr || w_down == nullptr || expert_offsets == nullptr || dpre == nullptr) return EP_ERR_INVALID;
     if (!aligned16(dy) || !aligned16(w_down) || !aligned16(expert_offsets) || !aligned16(dpre) ||
@@ -1194,7 +1209,7 @@ ep_status_t ep_expert_gate_up_bwd(const void* dpre, const void* w_gate_up, const
                                   int32_t F, int32_t E, int32_t R, int32_t max_rows, void* dx, int32_t* status,
                                   void* stream) {
     if (!valid(E, R, max_rows) || !valid_width(H, kMostWidth) || !valid_width(F, kMostWidth)) return EP_ERR_INVALID;
-    if (max_rows == 0) return EP_OK;
+    if (max_rows == 0) return no_room(expert_offsets, E, R, status, stream);
     if (dpre == nullptr || w_gate_up == nullptr || expert_offsets == nullptr || dx == nullptr) return EP_ERR_INVALID;
     if (!aligned16(dpre) || !aligned16(w_gate_up) || !aligned16(expert_offsets) || !aligned16(dx))
         return EP_ERR_INVALID;
@@ -1230,7 +1245,10 @@ ep_status_t ep_expert_wgrad(const void* dout, const void* rows, const int32_t* e
     g.max_rows = max_rows;
     g.out = static_cast<uint16_t*>(dw);
     g.status = status;
-    if (max_rows == 0) return zero_fill(dw, static_cast<size_t>(E) * I * J * 2, stream);
+    if (max_rows == 0) {
+        const ep_status_t st = zero_fill(dw, static_cast<size_t>(E) * I * J * 2, stream);
+        return st != EP_OK ? st : no_room(expert_offsets, E, R, status, stream);
+    }
     const uint64_t n = static_cast<uint64_t>(R) * max_rows;
     CUtensorMap a, b, out;
     ep_status_t st = map_of(&a, rows, J, n, 0, 64);

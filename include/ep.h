@@ -557,7 +557,8 @@ ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, co
  *     are the rows p0 <= p < p1 of rank r = e / (E/R), p0 = expert_offsets[e] -
  *     expert_offsets[r*(E/R)], p1 = p0 + the expert's count. Rows past max_rows are dropped
  *     with EP_FLAG_CAPACITY; a count below 0 is taken as 0. Rows of a slab that belong to no
- *     expert are neither used nor written, whatever they hold.
+ *     expert are neither used nor written, whatever they hold. With max_rows = 0 every row is
+ *     dropped: slabs and weights may be NULL then, and expert_offsets, too, where status is.
  *   w_gate_up bf16 [E][2F][H]: F gate rows, then F up rows; w_down bf16 [E][H][F]
  *   1 <= R <= 256, E % R == 0, E <= 8192; H % 8 == 0, F % 8 == 0, both <= 65536;
  *     max_rows >= 0, R * max_rows < 2^31. All arrays of one call are distinct ones.
