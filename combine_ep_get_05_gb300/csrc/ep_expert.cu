@@ -171,7 +171,10 @@ __device__ __forceinline__ int choice_of(const ExpertArgs& g, int count, int cho
     const bool turns = g.K <= 1024 || (g.K <= 2048 && count > kMostN);
     return kOp == kGateUp && choice == 0 && turns ? 1 : choice;
 }
-__device__ __forceinline__ int rows_each(int count, int tiles) { return ((count + tiles - 1) / tiles + 31) & ~31; }
+__device__ __forceinline__ int rows_each(int count, int tiles) {
+    const uint32_t n = static_cast<uint32_t>(tiles);
+    return static_cast<int>(((static_cast<uint32_t>(count) + n - 1) / n + 31) & ~31u);
+}
 
 // Lanes of a tile: the last 128 channels or fewer take 128, half of the copies, products and sums (64
 // experts of 104 channels, gated, 8192 tokens 137 us instead of 168; their gradient of weights, 512
@@ -1042,9 +1045,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
     }
 }
 
+// Rows of all slabs, so that 32 bits hold a row, the end of a stage or of a tile of rows that begins there,
+// and the last coordinate of a box of its copies.
+constexpr long long kMostRows = (1ll << 31) - 512;
 bool valid(int E, int R, int max_rows) {
     return R >= 1 && R <= 256 && E >= 1 && E <= 8192 && E % R == 0 && max_rows >= 0 &&
-           static_cast<long long>(R) * max_rows < (1ll << 31);
+           static_cast<long long>(R) * max_rows <= kMostRows;
 }
 bool valid_width(int n, int most) { return n >= 8 && n <= most && n % 8 == 0; }
 constexpr int kMostWidth = 65536;

@@ -561,7 +561,7 @@ ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, co
  *     dropped: slabs and weights may be NULL then, and expert_offsets, too, where status is.
  *   w_gate_up bf16 [E][2F][H]: F gate rows, then F up rows; w_down bf16 [E][H][F]
  *   1 <= R <= 256, E % R == 0, E <= 8192; H % 8 == 0, F % 8 == 0, both <= 65536;
- *     max_rows >= 0, R * max_rows < 2^31. All arrays of one call are distinct ones.
+ *     max_rows >= 0, R * max_rows <= 2^31 - 512. All arrays of one call are distinct ones.
  *   Products of bf16 values are summed in fp32 by the tensor cores (whose additions
  *   truncate: the sum of K products is good to about K * 2^-30 of its terms' size) in an order
  *   that depends on the sizes only; what follows is fp32, and each output is rounded once.
