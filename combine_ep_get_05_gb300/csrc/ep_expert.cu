@@ -90,7 +90,7 @@ struct Planned {
     uint64_t sums_full[2], sums_empty[2], tile_full[kTiles], tile_empty[kTiles], drain;
     Tile tile[kTiles];
     uint32_t tmem;
-    int stop;    // a wait gave up
+    Watch watch;
     int choice;  // kMostN >> choice rows a tile, of this call
     int scan[4][32];  // of the plan: a warp's tiles, for each choice
 };
@@ -123,7 +123,7 @@ struct Ring {
 
 // A wait gave up: every other one of the CTA ends soon, and the caller hears of it.
 __device__ __forceinline__ void give_up(const ExpertArgs& g, Planned& s) {
-    s.stop = 1;
+    s.watch.stop = 1;
     raise_flag(g.status, EP_FLAG_TIMEOUT);
 }
 
@@ -136,7 +136,7 @@ struct Tiles {
     template <bool kUniform = false>
     __device__ __forceinline__ bool next(Planned& s, Tile* t) {
         if (++at == kTiles) at = 0, phase ^= 1;
-        ok = warp_wait(&s.tile_full[at], phase, &s.stop);
+        ok = warp_wait(&s.tile_full[at], phase, &s.watch);
         if (!ok) return false;
         *t = s.tile[at];
         if (kUniform) {
@@ -743,7 +743,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         }
         mbar_init(&s.drain, 1);
         mbar_init_fence();
-        s.stop = 0;
+        s.watch = {0, 0};
     }
     if (warp == kLastFinish) tmem_alloc_pair(&s.tmem, kTmemColumns);
     if (tid == (kLastFinish - 2) * 32) {
@@ -783,7 +783,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             for (uint32_t i = pair + pairs; more; i += pairs) {
                 more = tile_at<kOp>(g, s, i, &t);
                 if (!more) t.e = -1;
-                if (!mbar_wait(&s.tile_empty[at], phase ^ 1, &s.stop)) {
+                if (!mbar_wait(&s.tile_empty[at], phase ^ 1, &s.watch)) {
                     give_up(g, s);
                     break;
                 }
@@ -817,7 +817,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             const uint32_t both = a_bytes<kOp>(g.C - t.channel, t.m) + a_bytes<kOp>(g.C - t.channel - t.m / 2, t.m) +
                                   2 * b_bytes;
             for (int k = 0; k < t.k; k += kBlockK) {
-                ok = warp_wait(&s.empty[stage], empty >> stage & 1, &s.stop);
+                ok = warp_wait(&s.empty[stage], empty >> stage & 1, &s.watch);
                 if (!ok) break;
                 empty ^= 1u << stage;
                 const uint32_t to = smem_addr(s_stages) + stage * ring.bytes;
@@ -865,6 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                     last_part &= ~(1u << stage);
                 }
                 ++issued;
+                if (leader && lanes) *static_cast<volatile uint32_t*>(&s.watch.stages) = issued;
                 if (++stage == ring.stages) stage = 0;
             }
         }
@@ -875,7 +876,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
         const int used = issued < static_cast<uint32_t>(ring.stages) ? static_cast<int>(issued) : ring.stages;
         for (int i = 0; i < used; ++i) {
             stage = stage == 0 ? ring.stages - 1 : stage - 1;
-            if (ok && !mbar_wait(&s.empty[stage], empty >> stage & 1, &s.stop)) ok = false;
+            if (ok && !mbar_wait(&s.empty[stage], empty >> stage & 1, &s.watch)) ok = false;
             if (ok) continue;
             if (last_part >> stage & 1)
                 mbar_wait(&s.part[stage], (part >> stage & 1) ^ 1, nullptr);
@@ -902,7 +903,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 const uint32_t first = slot, slots = slots_of<kOp>(t);
                 for (uint32_t i = 0; ok && i < slots; ++i)
                     ok = __all_sync(kFullMask, mbar_wait<true>(&s.sums_empty[(slot + i) % 2],
-                                                               ((slot + i) / 2 % 2) ^ 1, &s.stop));
+                                                               ((slot + i) / 2 % 2) ^ 1, &s.watch));
                 if (!ok) break;
                 slot += slots;
                 tc_fence_after();
@@ -913,7 +914,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 // branches and values of each lane's own.
                 int k = 0;
                 for (; k + kBlockK <= t.k; k += kBlockK) {
-                    ok = warp_wait(&s.full[stage], full >> stage & 1, &s.stop);
+                    ok = warp_wait(&s.full[stage], full >> stage & 1, &s.watch);
                     if (!ok) break;
                     full ^= 1u << stage;
                     tc_fence_after();
@@ -931,10 +932,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 }
                 if (ok && k < t.k) {  // the rest
                     if (kOp == kWgrad && has_tail(t.k - k)) {
-                        ok = warp_wait<true>(&s.ready[stage], ready >> stage & 1, &s.stop);
+                        ok = warp_wait<true>(&s.ready[stage], ready >> stage & 1, &s.watch);
                         ready ^= 1u << stage;
                     } else {
-                        ok = warp_wait(&s.full[stage], full >> stage & 1, &s.stop);
+                        ok = warp_wait(&s.full[stage], full >> stage & 1, &s.watch);
                         full ^= 1u << stage;
                     }
                     if (!ok) break;
@@ -956,7 +957,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
             ok = ok && tiles.ok;
             // the other CTA's last arrivals must not come when this one has ended
             for (uint32_t i = slot < 2 ? 0 : slot - 2; ok && i < slot; ++i)
-                ok = __all_sync(kFullMask, mbar_wait<true>(&s.sums_empty[i % 2], i / 2 % 2, &s.stop));
+                ok = __all_sync(kFullMask, mbar_wait<true>(&s.sums_empty[i % 2], i / 2 % 2, &s.watch));
             if (!ok) {  // the products that were begun still read shared memory
                 give_up(g, s);
                 if (leader) mma_commit(&s.drain);
@@ -977,7 +978,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 const int left = t.k % kBlockK;
                 if (!has_tail(left)) continue;
                 const uint32_t stage = (blocks - 1) % static_cast<uint32_t>(ring.stages);
-                ok = __all_sync(kFullMask, mbar_wait(&s.part[stage], part >> stage & 1, &s.stop));
+                ok = __all_sync(kFullMask, mbar_wait(&s.part[stage], part >> stage & 1, &s.watch));
                 if (!ok) break;
                 part ^= 1u << stage;
                 unsigned char* const at = s_stages + static_cast<size_t>(stage) * ring.bytes;
@@ -1015,7 +1016,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<kOp>::kThread
                 if (t.k == 0) return true;
                 bool ok = true;
                 for (uint32_t i = 0; ok && i < slots; ++i)
-                    ok = mbar_wait(&s.sums_full[(first + i) % 2], (first + i) / 2 % 2, &s.stop);
+                    ok = mbar_wait(&s.sums_full[(first + i) % 2], (first + i) / 2 % 2, &s.watch);
                 ok = group_agrees(ok, group);
                 tc_fence_after();
                 return ok;

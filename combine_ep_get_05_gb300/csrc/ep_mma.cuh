@@ -79,17 +79,26 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
             : "memory");
     return done != 0;
 }
-// Waits until the phase is over; gives up after about 2 s, or once *stop is set, and returns false.
+// What a CTA's waits look at (shared memory): whether one of them gave up, and how many stages have been
+// filled so far, since a wait may be for a tile of any number of stages.
+struct Watch {
+    int stop;
+    uint32_t stages;
+};
+// Waits until the phase is over; gives up, and returns false, after about 2 s in which no stage was filled,
+// or once the watch says so. Without a watch: after about 2 s.
 template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* stop) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile Watch* watch) {
     unsigned long long start = 0;
+    uint32_t stages = 0;
     for (uint32_t i = 0; i < (1u << 26); ++i) {
         if (mbar_try<kCluster>(bar, parity)) return true;
         if ((i & 63u) != 63u) continue;
-        if (stop != nullptr && *stop != 0) break;
+        if (watch != nullptr && watch->stop != 0) break;
         const unsigned long long now = globaltimer_ns();
-        if (start == 0)
-            start = now;
+        const uint32_t filled = watch != nullptr ? watch->stages : 0;
+        if (start == 0 || filled != stages)
+            start = now, stages = filled, i = 0;
         else if (now - start > 2000000000ull)
             break;
     }
@@ -98,9 +107,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
 
 // the same for a whole warp
 template <bool kCluster = false>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* stop) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile Watch* watch) {
     if (__all_sync(0xffffffffu, mbar_try<kCluster>(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, stop));
+    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, watch));
 }
 
 // tensor loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)

@@ -53,3 +53,18 @@ def test_rows(slabs, offsets):
         close(out[0, a:b], v * c[:, 8:], bound, ("h", a))
     assert not out[0, 300:10 ** 6].any() and not out[0, MOST - 10 ** 6:MOST - 300].any()
     assert ep.read_flags(status) == 0
+
+
+def test_weights_gradient_of_one_long_tile(slabs, offsets):
+    """One tile, whose finishing warps wait several seconds for its sums: no wait gives up while stages are
+    filled. Rows that are zero in one operand add nothing."""
+    x, out = slabs
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out.zero_()
+    for i, (a, b) in enumerate(PLACES):
+        out[0, a + 7:b] = normal(i + 11, b - a - 7, 8)
+    dw = torch.full((1, 8, 8), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_wgrad(out, x, offsets, dw, status)
+    d, v = (torch.cat([t[0, a:b] for a, b in PLACES]) for t in (out, x))
+    close(dw[0], *product(d.T, v.T), "dw")
+    assert ep.read_flags(status) == 0
