@@ -46,15 +46,16 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
-// Arrivals at a barrier of either CTA (a cluster address). Neither is a release to the cluster, which
-// waits until the SM's stores have reached L2, some 2000 cycles: the first orders the CTA's accesses,
-// for shared memory that fence_proxy_async_smem has handed to the tensor cores; the second none, for
-// tensor memory, which tcgen05's own fences order.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
+// Arrivals at a barrier of either CTA (a cluster address). The first is a release to the cluster for what
+// was written to this CTA's shared memory, and for that only: one for all memory waits until the SM's
+// stores have reached L2, some 2000 cycles. The second orders nothing, for tensor memory, which tcgen05's
+// own fences order.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    mbar_arrive_cluster_relaxed(addr);
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
