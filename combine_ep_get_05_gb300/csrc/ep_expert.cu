@@ -418,7 +418,7 @@ __device__ __forceinline__ void spread_codes(uint32_t (&w)[8], const uint4 (&c)[
     spread(w, f, patch, lane);
 }
 
-// max |v| of every column over the warp's lanes, NaN apart, into to[column]
+// max |v| of every column over the warp's lanes, NaN apart, into to[column]; NaN where there is nothing else
 __device__ __forceinline__ void column_max(float* to, const float (&v)[16], int lane) {
 #pragma unroll
     for (int q = 0; q < 2; ++q)
@@ -426,7 +426,6 @@ __device__ __forceinline__ void column_max(float* to, const float (&v)[16], int 
         for (int i = 0; i < 2; ++i) {
             float m = fmaxf(fmaxf(fabsf(v[4 * q + i]), fabsf(v[4 * q + 2 + i])),
                             fmaxf(fabsf(v[8 + 4 * q + i]), fabsf(v[8 + 4 * q + 2 + i])));
-            m = m == m ? m : 0.0f;  // all of them NaN
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
             if (lane < 4) to[8 * q + 2 * lane + i] = m;

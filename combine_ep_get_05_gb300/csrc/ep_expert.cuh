@@ -2,7 +2,7 @@
 // and its derivative, the 8-bit checkpoint's scale and codes. Internal header.
 #pragma once
 
-#include "ep_common.cuh"
+#include "ep_quant.cuh"
 
 namespace ep {
 
@@ -84,17 +84,19 @@ __device__ __forceinline__ float slope_of(float v, float act, float s) {
 // bf16_rn(amax / 448), 0 below 2^-117, where the smallest code, 2^-9, would stand for less than fp32's
 // smallest normal number
 __device__ __forceinline__ float checkpoint_scale(float amax) {
-    const float scale = bf16_lo(pack_bf16x2_rn(__fdiv_rn(amax, 448.0f), 0.0f));
+    const float scale = bf16_lo(pack_bf16x2_rn(scale_of(amax), 0.0f));
     return scale < 0x1p-117f ? 0.0f : scale;
 }
-// 1 / scale in two parts, good to 2^-46 together: what a block's values are multiplied by before they become
-// codes. v * high + (v * low), rounded once by the fused multiply-add, is v / scale where that is a midpoint
-// of codes, and stays on its side of every other midpoint: with 24 bits of v and 8 of the scale a quotient
-// beside a midpoint is at least 2^-24 of it away. So the codes are the quotient's, rounded once. (One product
-// by the rounded reciprocal, and by way of fp16, took 135 us instead of 141 where the finish bounds it, 16
-// experts of 2048 rows, H = 512, F = 2048, alike from H = 1024 on, and gave the farther code beside midpoints.)
+// 1 / scale in two parts, the GPU's fast reciprocal and what it is off by, good to 2^-44 together: what a
+// block's values are multiplied by before they become codes. v * high + (v * low), rounded once by the fused
+// multiply-add, is v / scale where that is a midpoint of codes, and stays on its side of every other
+// midpoint: with 24 bits of v and 8 of the scale a quotient beside a midpoint is at least 2^-24 of it away. So
+// the codes are the quotient's, rounded once. (One product by the rounded reciprocal, and by way of fp16, gave
+// the farther code beside midpoints, and took 132 us instead of 135 where the finish bounds it: 16 experts of
+// 2048 rows, H = 512, F = 2048.)
 __device__ __forceinline__ void checkpoint_rcp(float scale, float& high, float& low) {
-    high = scale == 0.0f ? 0.0f : __frcp_rn(scale);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(high) : "f"(scale));
+    if (scale == 0.0f) high = 0.0f;
     low = high == 0.0f ? 0.0f : fmaf(-high, scale, 1.0f) * high;  // 0 for an infinite scale, too
 }
 
