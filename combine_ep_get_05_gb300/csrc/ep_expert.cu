@@ -8,14 +8,14 @@
 // is 256 channels by up to 256 rows, K long: 128 flops a byte that comes from L2.
 //
 // The grid is persistent, a CTA an SM. In a CTA two warps copy tensor boxes into a ring of 4 to 11
-// stages of 64 k, one (of the pair) multiplies them into tensor memory, one plans tiles ahead, and
+// stages of 64 k (3 in the gated product of more than 2048 experts, whose plan takes their place), one (of the pair) multiplies them into tensor memory, one plans tiles ahead, and
 // sixteen finish the sums of one tile while the next is multiplied: 32 lanes by 16 columns at a time
 // as fragments of 8 x 8, through a patch of shared memory into rows of 16-byte vectors.
 //
 // With few rows an expert the weights' stream bounds it, with many the tensor cores' power: 4096
 // tokens top-8 of 256 experts of 7168 x 2048, gated with the 8-bit checkpoint 2.34 ms (6.7 TB/s), down
 // 1.19 ms (6.8), back through the activation 1.24 ms (6.9); 16384 tokens of 128 uneven experts of
-// 4096 x 2048 2.1 to 2.4 ms a product (1.8 to 2.1 PFLOP/s). With few rows and few tiles the warp that
+// 4096 x 2048 2.1 to 2.5 ms a product (1.75 to 2.1 PFLOP/s). With few rows and few tiles the warp that
 // multiplies bounds it, 146 ns for 64 k.
 #include "ep_expert.cuh"
 #include "ep_mma.cuh"
@@ -163,9 +163,9 @@ __device__ __forceinline__ int row_tiles(int count, int choice) {
 // The choice for one expert. A gated tile of more than 128 rows has all of tensor memory, and its sums
 // are finished before the next one's can begin; two of 128 rows take turns, but read the weights
 // twice (from L2). Short sums cost less than their finish, so they take turns. us with tiles of up to
-// 128 rows, of up to 256, 16 experts of 2048 rows, F = 2048, the 8-bit checkpoint: H = 512 129, 175, 1024
-// 187, 241, 2048 331, 366, 4096 635, 633; 128 uneven ones of H = 4096 alike, 256 of 128 rows on average,
-// H = 7168 2505, 2355.
+// 128 rows, of up to 256, 16 experts of 2048 rows, F = 2048, the 8-bit checkpoint: H = 512 137, 186, 1024
+// 190, 254, 2048 336, 386, 4096 645, 680; 128 uneven ones of H = 4096 1995, 2002, with the bf16 checkpoint
+// 2075, 2020; 256 of 128 rows on average, H = 7168 2534, 2362.
 template <int kOp>
 __device__ __forceinline__ int choice_of(const ExpertArgs& g, int count, int choice) {
     const bool turns = g.K <= 1024 || (g.K <= 2048 && count > kMostN);

@@ -562,11 +562,13 @@ ep_status_t ep_rmsnorm_bwd(const void* dy, const void* z, const void* weight, co
  *   w_gate_up bf16 [E][2F][H]: F gate rows, then F up rows; w_down bf16 [E][H][F]
  *   1 <= R <= 256, E % R == 0, E <= 8192; H % 8 == 0, F % 8 == 0, both <= 65536;
  *     max_rows >= 0, R * max_rows <= 2^31 - 512. All arrays of one call are distinct ones.
- *   Products of bf16 values are summed in fp32 by the tensor cores (whose additions
- *   truncate: the sum of K products is good to about K * 2^-30 of its terms' size) in an order
- *   that depends on the sizes only; what follows is fp32, and each output is rounded once.
- *   Results are deterministic. EP_FLAG_TIMEOUT: a bounded wait gave up, and outputs are
- *   incomplete. E = 1, R = 1 with offsets {0, T} is an ordinary dense layer. */
+ *   Products of bf16 values are summed in fp32 by the tensor cores in an order that depends on the
+ *   sizes only. Their additions truncate, so that a sum of K products is off by at most K * 2^-23 of
+ *   the sum of its terms' magnitudes (normal values, measured, relative to the results: 1.2e-7 at
+ *   K = 128, 2.1e-6 at 2048, 7.9e-6 at 7168); what follows is fp32, and each output is rounded once.
+ *   Results are deterministic. EP_FLAG_TIMEOUT: for about 2 s nothing went on (a wait is bounded), and
+ *   outputs are incomplete; without a status nothing says so. E = 1, R = 1 with offsets {0, T} is an
+ *   ordinary dense layer. */
 
 /* ep_expert_gate_up -- for every row of every expert
  *   gate[p][f] = sum over h of x[r][p][h] * w_gate_up[e][f][h]
