@@ -61,3 +61,18 @@ def test_a_captured_call_reads_the_offsets_of_its_replay():
     off.copy_(torch.tensor([0, 0, 2, 2, 2], dtype=torch.int32))
     g.replay()
     assert ep.read_flags(status) == ep.FLAG_CAPACITY
+
+
+def test_a_captured_gradient_of_weights_is_cleared_and_reported():
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dout, x = (torch.empty((1, 0, n), dtype=torch.bfloat16, device="cuda") for n in (F, H))
+    dw = torch.empty((1, F, H), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        ep.ep_expert_wgrad(dout, x, off, dw, status)
+    dw.fill_(SENTINEL)
+    g.replay()
+    assert not dw.any() and ep.read_flags(status) == ep.FLAG_CAPACITY
