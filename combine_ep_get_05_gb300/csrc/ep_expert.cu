@@ -8,9 +8,10 @@
 // is 256 channels by up to 256 rows, K long: 128 flops a byte that comes from L2.
 //
 // The grid is persistent, a CTA an SM. In a CTA two warps copy tensor boxes into a ring of 4 to 11
-// stages of 64 k (3 in the gated product of more than 2048 experts, whose plan takes their place), one (of the pair) multiplies them into tensor memory, one plans tiles ahead, and
-// sixteen finish the sums of one tile while the next is multiplied: 32 lanes by 16 columns at a time
-// as fragments of 8 x 8, through a patch of shared memory into rows of 16-byte vectors.
+// stages of 64 k (3 in the gated product of more than 2048 experts, whose plan takes the place of one),
+// one (of the pair) multiplies them into tensor memory, one plans tiles ahead, and sixteen finish the
+// sums of one tile while the next is multiplied: 32 lanes by 16 columns at a time as fragments of 8 x 8,
+// through a patch of shared memory into rows of 16-byte vectors.
 //
 // With few rows an expert the weights' stream bounds it, with many the tensor cores' power: 4096
 // tokens top-8 of 256 experts of 7168 x 2048, gated with the 8-bit checkpoint 2.34 ms (6.7 TB/s), down
